@@ -1,5 +1,5 @@
-"""ctypes declarations of the libengram.so C ABI (include/engram.h), without
-torch: the binding (engram.py) applies them to the built library, and the
+"""ctypes declarations of the libengram.so C ABI (include/engram.h, and
+include/engram_layer.h in declare_layer), without torch: the binding (engram.py) applies them to the built library, and the
 host-side checks of the same entry points, built for the CPU under
 sanitizers, are driven through them by the tests.
 """
@@ -27,6 +27,11 @@ OP_APPLY = 3
 OP_APPLY_SIGNSGD = 4
 OP_RECORD = 5
 OP_WAIT = 6
+
+BF16 = 0                          # ENGRAM_BF16
+F32 = 1                           # ENGRAM_F32
+ACT_BLOCK = 128                   # ENGRAM_ACT_BLOCK
+NORM_MAX_GROUP = 16384            # ENGRAM_NORM_MAX_GROUP
 
 _i64p = ctypes.POINTER(ctypes.c_int64)
 _vp = ctypes.c_void_p
@@ -120,4 +125,47 @@ def declare(lib):
     lib.engram_ple_conv.argtypes = [_vp, _vp, ctypes.c_int64, _vp, _vp, _vp, ctypes.c_int64,
                                     ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
                                     _vp, _vp]
+    return lib
+
+
+class EngramNormArgs(ctypes.Structure):
+    """struct engram_norm_args of include/engram_layer.h, field for field."""
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("channels", ctypes.c_int64), ("groups", ctypes.c_int64),
+        ("gate_width", ctypes.c_int64), ("eps", ctypes.c_float),
+        ("residual_scale", ctypes.c_float), ("residual_type", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("d_residual", _vp), ("d_y", _vp), ("d_gate", _vp), ("d_w_post", _vp), ("d_scale", _vp),
+        ("d_w_next", _vp), ("d_out", _vp), ("d_next", _vp), ("d_rstd_post", _vp),
+        ("d_rstd_next", _vp), ("d_y_codes", _vp), ("d_y_scales", _vp), ("d_next_codes", _vp),
+        ("d_next_scales", _vp), ("d_grad_out", _vp), ("d_grad_next", _vp),
+        ("d_grad_residual", _vp), ("d_grad_y", _vp), ("d_grad_gate", _vp),
+        ("d_grad_w_post", _vp), ("d_grad_scale", _vp), ("d_grad_w_next", _vp),
+        ("d_workspace", _vp), ("workspace_bytes", ctypes.c_size_t), ("stream", _vp),
+    ]
+
+
+def declare_layer(lib):
+    """declare() for the entry points of include/engram_layer.h."""
+    i64, i32, f32, size = ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
+    norm = ctypes.POINTER(EngramNormArgs)
+    for name, result, args in [
+        ("engram_residual_norm", ctypes.c_int, [norm]),
+        ("engram_residual_norm_backward_workspace", size, [i64, i64, i64]),
+        ("engram_residual_norm_backward", ctypes.c_int, [norm]),
+        ("engram_act_encode", ctypes.c_int, [_vp, i64, i64, _vp, _vp, _vp]),
+        ("engram_act_decode", ctypes.c_int, [_vp, _vp, i64, i64, _vp, _vp]),
+        ("engram_ple_conv_backward_workspace", size, [i64, i64, i64, i64, i32, i32]),
+        ("engram_ple_conv_backward", ctypes.c_int,
+         [_vp, _vp, _vp, _vp, i64, _vp, i64, _vp, _vp, i64, i64, i64, i32, i32, _vp, _vp, _vp,
+          _vp, _vp, size, _vp]),
+        ("engram_ple_conv_step", ctypes.c_int,
+         [_vp, _vp, i64, i64, _vp, _vp, _vp, _vp, i64, i64, i64, i32, i32, _vp, _vp, _vp]),
+        ("engram_embed", ctypes.c_int, [_vp, i64, _vp, i64, i64, f32, i32, _vp, _vp, _vp]),
+        ("engram_embed_grad_workspace", size, [i64, i64, i64]),
+        ("engram_embed_grad", ctypes.c_int,
+         [_vp, i64, _vp, i64, f32, i64, i32, i32, _vp, _vp, size, _vp, _vp]),
+    ]:
+        f = getattr(lib, name)
+        f.restype, f.argtypes = result, args
     return lib

@@ -1,0 +1,404 @@
+// engram_conv_backward.hip -- the gradients of the PLE causal dilated
+// depthwise convolution, for gfx950.
+//
+// What is computed is stated with engram_ple_conv_backward in include/
+// engram_layer.h: the transpose of the convolution of the NeMo AutoModel v0.7
+// API page "qwen3_8_flash_next.engram", Qwen3_8_FlashNextPLELayer
+// (_causal_short_conv, _segmented_conv), with the readings of
+// engram_ple_conv.
+//
+// Mathematics.  Both sums run over the same pairs (p, t = p + j * dilation):
+// grad_x[p] adds w_j * g[t] and grad_w_j adds g[t] * x[p], so a position needs
+// its own x and the K values of g ahead of it.  A pair counts when t lies in
+// the row and no segment begins in (p, t].
+//
+// Bound by HBM: 6 bytes a value (5 from an 8-bit checkpoint) against 17
+// operations.  A wave owns 256 channels, 4 a lane, and a slice of a row's
+// positions, which it walks from the end: the rows of g ahead of a position
+// are those it has just passed, so they stay in registers and each row of g is
+// read once (a slice reads (K-1) * dilation rows past its end).  The
+// segments' bounds are the same for a whole wave: one ballot a tile gives a
+// mask of the positions where a segment begins, and a tile without any takes
+// the path without tests.  Sums over positions stay in registers; each slice
+// leaves one fp32 row of them, which a second kernel adds in fp64.
+#include "engram_layer_dev.h"
+
+namespace engram {
+namespace {
+
+constexpr int kConvWaves = 4;  // waves of a block, each on its own
+constexpr int kConvBlock = kConvWaves * kWave;
+
+struct ConvBackArgs {
+  const u32x2 *g;  // grad_out [batch, seq, quads]
+  const u32x2 *x;
+  const uint32_t *codes;
+  const float *scales;
+  int64_t code_blocks, code_width;  // of a position
+  const u32x2 *halo;
+  const int64_t *seg;
+  const uint16_t *w;
+  u32x2 *gx, *ghalo;
+  float *partials;  // [batch * slices][K + 1][channels], or null
+  int64_t batch, seq, halo_len, quads, units;
+  ConvBackwardShape s;
+  int K, dil;
+  bool want_w;
+};
+
+__device__ __forceinline__ void unpack4(const u32x2 &r, float (&f)[4]) {
+  f[0] = bf16_lo(r.x); f[1] = bf16_hi(r.x);
+  f[2] = bf16_lo(r.y); f[3] = bf16_hi(r.y);
+}
+
+// One wave's place: (batch row, slice, channel group), groups fastest.  The
+// first `halo_slices` slices of a row are the halo's, the others the
+// sequence's: a slice lies on one side of position 0.
+struct ConvPlace {
+  int64_t b, slice, quad, first, last;  // positions [first, last)
+  bool on, halo;
+};
+__device__ __forceinline__ ConvPlace conv_place(const ConvBackArgs &a, int64_t unit) {
+  ConvPlace p;
+  const int64_t grp = unit % a.s.groups, rest = unit / a.s.groups;
+  p.slice = rest % a.s.slices;
+  p.b = rest / a.s.slices;
+  p.quad = grp * kWave + (threadIdx.x & 63);
+  p.on = p.quad < a.quads;
+  if (!p.on) p.quad = 0;
+  p.halo = p.slice < a.s.halo_slices;
+  p.first = p.halo ? p.slice * a.s.slice - a.halo_len
+                   : (p.slice - a.s.halo_slices) * a.s.slice;
+  p.last = min(p.first + a.s.slice, p.halo ? 0 : a.seq);
+  return p;
+}
+
+// x of a position: 4 values of this lane's channels, as bf16 or as codes.
+struct XRow {
+  u32x2 bits;
+  float scale;  // codes only
+};
+__device__ __forceinline__ XRow load_halo(const ConvBackArgs &a, const ConvPlace &p, int64_t pos) {
+  return XRow{a.halo[(p.b * a.halo_len + a.halo_len + pos) * a.quads + p.quad], 0.0f};
+}
+template <bool CODES>
+__device__ __forceinline__ XRow load_x(const ConvBackArgs &a, const ConvPlace &p, int64_t pos,
+                                       int64_t scale_at) {
+  const int64_t at = p.b * a.seq + pos;
+  if (CODES)
+    return XRow{u32x2{a.codes[at * a.quads + p.quad], 0u}, a.scales[at * a.code_blocks + scale_at]};
+  return XRow{a.x[at * a.quads + p.quad], 0.0f};
+}
+template <bool CODES>
+__device__ __forceinline__ void unpack_x(const XRow &r, bool halo, float (&f)[4]) {
+  if (CODES && !halo) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = code_value(r.bits.x, e, r.scale);
+  } else {
+    unpack4(r.bits, f);
+  }
+}
+
+// Bits of the positions pos0 .. pos0 + 63 where a segment begins (from
+// pos0 + 1 on; bit 0 is not used) or the row has ended.
+__device__ __forceinline__ uint64_t begins_mask(const ConvBackArgs &a, int64_t b, int64_t pos0) {
+  const int64_t pos = pos0 + (threadIdx.x & 63);
+  bool begin = pos >= a.seq;
+  if (a.seg != nullptr && !begin && pos > -a.halo_len) {
+    const int64_t *s = a.seg + b * (a.halo_len + a.seq) + a.halo_len + pos;
+    begin = s[0] != s[-1];
+  }
+  return __ballot(begin);
+}
+
+// A tile's positions, from the last: CLEAR: every pair counts; else the
+// slice's own positions' pairs that no boundary cuts.
+template <int D, int T, bool CODES, bool WANT_W, bool CLEAR>
+__device__ __forceinline__ void conv_tile(const ConvBackArgs &a, const ConvPlace &p, int64_t t0,
+                                          uint64_t begins, const u32x2 (&win)[T + 3 * D],
+                                          const XRow (&xr)[T], const float (&w)[4][4],
+                                          float (&sum_w)[4][4], float (&sum_b)[4]) {
+  constexpr int K = 4;
+#pragma unroll
+  for (int i = T - 1; i >= 0; --i) {
+    const int64_t t = t0 + i;
+    float dx[4] = {0.0f, 0.0f, 0.0f, 0.0f}, x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (WANT_W) unpack_x<CODES>(xr[i], !CLEAR && p.halo, x);
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      const uint64_t between = (((uint64_t)1 << (j * D)) - 1) << (i + 1);
+      if (CLEAR || (t >= p.first && t + j * D >= 0 && (begins & between) == 0)) {
+        float v[4];
+        unpack4(win[i + j * D], v);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          dx[c] += w[c][j] * v[c];
+          if (WANT_W) sum_w[c][j] += v[c] * x[c];
+          if (WANT_W && j == 0) sum_b[c] += v[c];
+        }
+      }
+    }
+    if ((CLEAR || t >= p.first) && p.on) {
+      const u32x2 o = {pack_bf16(dx[0], dx[1]), pack_bf16(dx[2], dx[3])};
+      if (CLEAR || !p.halo) {
+        if (a.gx != nullptr) a.gx[(p.b * a.seq + t) * a.quads + p.quad] = o;
+      } else if (a.ghalo != nullptr) {
+        a.ghalo[(p.b * a.halo_len + a.halo_len + t) * a.quads + p.quad] = o;
+      }
+    }
+  }
+}
+
+template <int D, bool CODES, bool WANT_W>
+__global__ __launch_bounds__(kConvBlock) void conv_backward_k4_kernel(const ConvBackArgs a) {
+  constexpr int K = 4, H = (K - 1) * D;
+  constexpr int T = 8;  // positions of a tile
+  static_assert(T + H < 64, "a tile and the rows ahead of it fit one mask");
+  const int64_t unit = (int64_t)blockIdx.x * kConvWaves + __builtin_amdgcn_readfirstlane(
+                                                              threadIdx.x / kWave);
+  if (unit >= a.units) return;
+  const ConvPlace p = conv_place(a, unit);
+  const int64_t scale_at = p.quad * 4 / a.code_width * ((a.code_width + 127) / 128) +
+                           p.quad * 4 % a.code_width / 128;
+  float w[4][K];  // [channel][tap j back]
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int j = 0; j < K; ++j) w[c][j] = bf16_lo(a.w[(p.quad * 4 + c) * K + (K - 1 - j)]);
+  float sum_w[4][K], sum_b[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    sum_b[c] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < K; ++j) sum_w[c][j] = 0.0f;
+  }
+  const u32x2 *g = a.g + p.b * a.seq * a.quads + p.quad;
+  // row i of the window is position t0 + i: the tile, then the rows ahead
+  u32x2 win[T + H];
+  int64_t t0 = p.last - T;
+#pragma unroll
+  for (int i = 0; i < H; ++i) {
+    const int64_t t = p.last + i;
+    win[T + i] = t >= 0 && t < a.seq ? g[t * a.quads] : u32x2{0u, 0u};
+  }
+  for (;;) {
+    // every load of the tile at once; rows below the slice repeat its first,
+    // and their values are not used
+    XRow xr[T];
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+      win[i] = u32x2{0u, 0u};
+      xr[i] = XRow{u32x2{0u, 0u}, 0.0f};
+      const int64_t t = max(t0 + i, p.first);
+      if (!p.halo) {
+        win[i] = g[t * a.quads];
+        if (WANT_W) xr[i] = load_x<CODES>(a, p, t, scale_at);
+      } else if (WANT_W) {
+        xr[i] = load_halo(a, p, t);
+      }
+    }
+    const uint64_t begins = begins_mask(a, p.b, t0);
+    // every pair of the tile counts: the whole tile is the slice's own, inside
+    // the row, and no segment begins in it or in the rows ahead
+    const bool clear = t0 >= p.first && !p.halo &&
+                       (begins & ((((uint64_t)1 << (T + H - 1)) - 1) << 1)) == 0;
+    if (clear)
+      conv_tile<D, T, CODES, WANT_W, true>(a, p, t0, begins, win, xr, w, sum_w, sum_b);
+    else
+      conv_tile<D, T, CODES, WANT_W, false>(a, p, t0, begins, win, xr, w, sum_w, sum_b);
+    if (t0 <= p.first) break;
+    t0 -= T;
+    // the rows ahead of the next tile are this window's first H
+#pragma unroll
+    for (int i = H - 1; i >= 0; --i) win[T + i] = win[i];
+  }
+  if (!WANT_W || !p.on) return;
+  f32x4 *dst = reinterpret_cast<f32x4 *>(a.partials) +
+               (p.b * a.s.slices + p.slice) * (K + 1) * a.quads + p.quad;
+#pragma unroll
+  for (int j = 0; j < K; ++j)
+    dst[(K - 1 - j) * a.quads] = f32x4{sum_w[0][j], sum_w[1][j], sum_w[2][j], sum_w[3][j]};
+  dst[K * a.quads] = f32x4{sum_b[0], sum_b[1], sum_b[2], sum_b[3]};
+}
+
+// Any K up to kConvMaxKernel and any dilation: the same walk, each row of g
+// read from memory and each pair tested against the segment ids.
+template <bool CODES>
+__global__ __launch_bounds__(kConvBlock) void conv_backward_generic_kernel(const ConvBackArgs a) {
+  const int64_t unit = (int64_t)blockIdx.x * kConvWaves + threadIdx.x / kWave;
+  if (unit >= a.units) return;
+  const ConvPlace p = conv_place(a, unit);
+  const int64_t scale_at = p.quad * 4 / a.code_width * ((a.code_width + 127) / 128) +
+                           p.quad * 4 % a.code_width / 128;
+  const int64_t *seg =
+      a.seg != nullptr ? a.seg + p.b * (a.halo_len + a.seq) + a.halo_len : nullptr;
+  const u32x2 *g = a.g + p.b * a.seq * a.quads + p.quad;
+  // one tap at a time for the weight's sums, so that K stays a run-time number
+  float sum_b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int64_t t = p.last - 1; t >= p.first; --t) {
+    float dx[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    int64_t reach = t;  // pairs up to here have been tested
+    for (int j = 0; j < a.K; ++j) {
+      const int64_t q = t + (int64_t)j * a.dil;
+      if (q >= a.seq) break;
+      bool ok = true;
+      for (; ok && seg != nullptr && reach < q; ++reach) ok = seg[reach] == seg[reach + 1];
+      if (!ok) break;
+      if (q < 0) continue;
+      float v[4];
+      unpack4(g[q * a.quads], v);
+      for (int c = 0; c < 4; ++c) {
+        dx[c] += bf16_lo(a.w[(p.quad * 4 + c) * a.K + (a.K - 1 - j)]) * v[c];
+        if (j == 0) sum_b[c] += v[c];
+      }
+    }
+    if (!p.on) continue;
+    const u32x2 o = {pack_bf16(dx[0], dx[1]), pack_bf16(dx[2], dx[3])};
+    if (t >= 0) {
+      if (a.gx != nullptr) a.gx[(p.b * a.seq + t) * a.quads + p.quad] = o;
+    } else if (a.ghalo != nullptr) {
+      a.ghalo[(p.b * a.halo_len + a.halo_len + t) * a.quads + p.quad] = o;
+    }
+  }
+  if (a.partials == nullptr) return;
+  f32x4 *dst = reinterpret_cast<f32x4 *>(a.partials) +
+               (p.b * a.s.slices + p.slice) * (a.K + 1) * a.quads + p.quad;
+  for (int j = 0; j < a.K && a.want_w; ++j) {
+    const int64_t back = (int64_t)j * a.dil;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int64_t t = p.last - 1; t >= p.first; --t) {
+      const int64_t q = t + back;
+      if (q >= a.seq || q < 0) continue;
+      bool ok = true;
+      for (int64_t r = t; ok && seg != nullptr && r < q; ++r) ok = seg[r] == seg[r + 1];
+      if (!ok) continue;
+      float v[4], x[4];
+      unpack4(g[q * a.quads], v);
+      unpack_x<CODES>(p.halo ? load_halo(a, p, t) : load_x<CODES>(a, p, t, scale_at), p.halo, x);
+      for (int c = 0; c < 4; ++c) s[c] += v[c] * x[c];
+    }
+    if (p.on) dst[(a.K - 1 - j) * a.quads] = f32x4{s[0], s[1], s[2], s[3]};
+  }
+  if (p.on) dst[a.K * a.quads] = f32x4{sum_b[0], sum_b[1], sum_b[2], sum_b[3]};
+}
+
+// The weight's and the bias's gradients: sums of the slices' rows, 64 of the
+// (K + 1) * channels columns a block, each of its 16 wavefronts every 16th
+// slice, in fp64.
+constexpr int kConvJoin = 1024;
+__global__ __launch_bounds__(kConvJoin) void conv_join_kernel(const float *partials, int64_t rows,
+                                                              int K, int64_t channels,
+                                                              float *grad_weight,
+                                                              float *grad_bias) {
+  __shared__ double part[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t col = (int64_t)blockIdx.x * 64 + lane, cols = (K + 1) * channels;
+  const bool bias = col >= K * channels;
+  const bool on = col < cols && (bias ? grad_bias : grad_weight) != nullptr;
+  double s = 0.0;
+  if (on)
+#pragma unroll 4
+    for (int64_t r = wave; r < rows; r += 16) s += partials[r * cols + col];
+  part[wave][lane] = s;
+  __syncthreads();
+  if (wave != 0 || !on) return;
+  s = 0.0;
+#pragma unroll
+  for (int v = 0; v < 16; ++v) s += part[v][lane];
+  const int64_t k = col / channels, c = col % channels;
+  if (bias)
+    grad_bias[c] = (float)s;
+  else
+    grad_weight[c * K + k] = (float)s;
+}
+
+__global__ __launch_bounds__(256) void fill_zero_kernel(u32x4 *dst, int64_t n) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) dst[i] = u32x4{0u, 0u, 0u, 0u};
+}
+
+template <bool CODES, bool WANT_W>
+void launch_k4(const ConvBackArgs &a, dim3 grid, hipStream_t s) {
+  switch (a.dil) {
+#define ENGRAM_CONV_CASE(D)                                                                    \
+  case D:                                                                                      \
+    hipLaunchKernelGGL((conv_backward_k4_kernel<D, CODES, WANT_W>), grid, dim3(kConvBlock), 0, s, \
+                       a);                                                                     \
+    break;
+    ENGRAM_CONV_CASE(1)
+    ENGRAM_CONV_CASE(2)
+    ENGRAM_CONV_CASE(3)
+    ENGRAM_CONV_CASE(4)
+    ENGRAM_CONV_CASE(5)
+    ENGRAM_CONV_CASE(6)
+    ENGRAM_CONV_CASE(7)
+    ENGRAM_CONV_CASE(8)
+#undef ENGRAM_CONV_CASE
+  }
+}
+
+}  // namespace
+}  // namespace engram
+
+int engram::launch_conv_backward(const ConvBackwardCall &c, void *stream) {
+  hipStream_t st = as_stream(stream);
+  const bool empty = c.batch == 0 || c.seq == 0;
+  const bool sums = c.grad_weight != nullptr || c.grad_bias != nullptr;
+  const ConvBackwardShape s =
+      conv_backward_shape(c.batch, c.seq, c.halo_len, c.channels, c.K, c.dilation);
+  const int64_t units = c.batch * s.slices * s.groups;
+  const int64_t blocks = ceil_div(units, kConvWaves);
+  const int64_t cols = (c.K + 1) * c.channels;
+  const int64_t halo_words = c.batch * c.halo_len * c.channels / 8;
+  if (!grid_fits(blocks, kConvBlock) || !grid_fits(ceil_div(cols, 64), kConvJoin) ||
+      !grid_fits(ceil_div(halo_words, 256), 256))
+    return ENGRAM_EINVAL;
+  if (empty && c.grad_halo != nullptr && halo_words > 0)
+    hipLaunchKernelGGL(fill_zero_kernel, dim3((unsigned)ceil_div(halo_words, 256)), dim3(256), 0,
+                       st, static_cast<u32x4 *>(c.grad_halo), halo_words);
+  if (!empty) {
+    ConvBackArgs a = {};
+    a.g = static_cast<const u32x2 *>(c.grad_out);
+    a.x = static_cast<const u32x2 *>(c.x);
+    a.codes = reinterpret_cast<const uint32_t *>(c.codes);
+    a.scales = c.scales;
+    a.code_width = c.code_width;
+    a.code_blocks = c.channels / c.code_width * ceil_div(c.code_width, kActBlock);
+    a.halo = static_cast<const u32x2 *>(c.halo);
+    a.seg = c.seg;
+    a.w = static_cast<const uint16_t *>(c.weight);
+    a.gx = static_cast<u32x2 *>(c.grad_x);
+    a.ghalo = static_cast<u32x2 *>(c.grad_halo);
+    a.partials = sums ? c.partials : nullptr;
+    a.batch = c.batch;
+    a.seq = c.seq;
+    a.halo_len = c.halo_len;
+    a.quads = s.quads;
+    a.units = units;
+    a.s = s;
+    a.K = c.K;
+    a.dil = c.dilation;
+    a.want_w = c.grad_weight != nullptr;
+    const dim3 grid((unsigned)blocks);
+    const bool codes = c.codes != nullptr;
+    // the register-window kernel sums the weight's gradient with the bias's: a
+    // bias alone (no x given) takes the plain one
+    if (c.K == 4 && c.dilation <= 8 && (a.want_w || !sums)) {
+      if (!sums)
+        launch_k4<false, false>(a, grid, st);
+      else if (codes)
+        launch_k4<true, true>(a, grid, st);
+      else
+        launch_k4<false, true>(a, grid, st);
+    } else if (codes) {
+      hipLaunchKernelGGL(conv_backward_generic_kernel<true>, grid, dim3(kConvBlock), 0, st, a);
+    } else {
+      hipLaunchKernelGGL(conv_backward_generic_kernel<false>, grid, dim3(kConvBlock), 0, st, a);
+    }
+  }
+  if (sums)
+    hipLaunchKernelGGL(conv_join_kernel, dim3((unsigned)ceil_div(cols, 64)), dim3(kConvJoin), 0,
+                       st, c.partials, empty ? 0 : c.batch * s.slices, c.K, c.channels,
+                       c.grad_weight, c.grad_bias);
+  return launch_status();
+}

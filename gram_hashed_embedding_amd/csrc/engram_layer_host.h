@@ -1,0 +1,117 @@
+// engram_layer_host.h -- the host side of the layer operators (include/
+// engram_layer.h) in plain C++: the calls' checked arguments, the sizes of
+// their workspaces, and the launchers of the HIP sources.  As engram_host.h:
+// the entry points (engram_layer_host.cpp) check, then call one launcher.
+#pragma once
+
+#include "engram_host.h"
+#include "engram_layer.h"
+
+namespace engram {
+
+constexpr int64_t kActBlock = ENGRAM_ACT_BLOCK;
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// ----------------------------------------------------------- residual norm --
+// How a norm kernel covers [rows, groups] groups of n = 8 * chunks channels.
+// A group belongs to `lanes` threads, each holding `items` chunks of 8
+// channels; a block of `threads` threads holds threads / lanes groups at a
+// time: `gcols` adjacent groups of each of `trows` rows.  The grid is
+// `colblocks` column blocks times `rowblocks` blocks of `per_block` rows.
+struct NormShape {
+  int64_t rows, channels, groups, chunks;
+  int lanes, items, threads, gcols, trows;
+  int64_t colblocks, rowblocks, per_block;
+};
+
+// The shape for a kernel that holds at most max_items chunks a lane, with
+// about `blocks` blocks when there is work for them.
+NormShape norm_shape(int64_t rows, int64_t channels, int64_t groups, int max_items,
+                     int64_t blocks);
+
+constexpr int kNormForwardItems = 4;
+constexpr int kNormBackwardItems = 2;
+constexpr int64_t kNormForwardBlocks = 4096;
+constexpr int64_t kNormBackwardBlocks = 1536;
+// Most rows a lane sums in fp32 before the sums go on in fp64.
+constexpr int64_t kNormMaxSteps = 256;
+
+inline NormShape norm_backward_shape(int64_t rows, int64_t channels, int64_t groups) {
+  return norm_shape(rows, channels, groups, kNormBackwardItems, kNormBackwardBlocks);
+}
+// The backward's sums over rows: each row block leaves two fp32 rows.
+inline int64_t norm_partial_floats(const NormShape &s) { return s.rowblocks * 2 * s.channels; }
+
+// ------------------------------------------------------------- convolution --
+// The backward's work: waves of 64 lanes, each owning 4 channels a lane
+// (256 channels) and `slice` consecutive positions of a row's halo (the first
+// halo_slices slices) or of its sequence.  Each leaves kernel_size + 1 fp32
+// sums a channel.
+constexpr int64_t kConvMaxSlice = 1024;
+struct ConvBackwardShape {
+  int64_t quads, groups, slice, halo_slices, slices;  // slices: a row's, the halo's included
+};
+ConvBackwardShape conv_backward_shape(int64_t batch, int64_t seq, int64_t halo_len,
+                                      int64_t channels, int32_t K, int32_t dilation);
+
+struct ConvBackwardCall {
+  const void *grad_out, *x;
+  const int8_t *codes;
+  const float *scales;
+  int64_t code_width;
+  const void *halo;
+  int64_t halo_len;
+  const int64_t *seg;
+  const void *weight;
+  int64_t batch, seq, channels;
+  int32_t K, dilation;
+  void *grad_x, *grad_halo;
+  float *grad_weight, *grad_bias;
+  float *partials;  // [batch * slices][K + 1][channels]
+};
+
+struct ConvStepCall {
+  const void *x;
+  void *ring;
+  int64_t ring_count, ring_rows;
+  const int64_t *ring_ids, *positions;
+  const void *weight, *bias;
+  int64_t batch, tokens, channels;
+  int32_t K, dilation;
+  void *out;
+  int64_t *err;
+};
+
+// --------------------------------------------------------------- embedding --
+// Sorted positions whose sum a block of the gradient leaves as one fp64 row
+// when they are all of one token.
+constexpr int64_t kEmbedChunk = 64;
+
+struct EmbedGradCall {
+  const int64_t *tokens;
+  int64_t n;
+  const void *grads;
+  int64_t channels;
+  float scale;
+  int64_t table_rows;
+  int32_t type, accumulate;
+  void *grad_table;
+  double *partials;  // [n / kEmbedChunk][channels]
+  int64_t *err;
+};
+
+// -------------------------------------------------------------- launchers --
+int launch_residual_norm(const engram_norm_args &a);
+int launch_residual_norm_backward(const engram_norm_args &a);
+int launch_act_encode(const void *d_x, int64_t rows, int64_t channels, int8_t *d_codes,
+                      float *d_scales, void *stream);
+int launch_act_decode(const int8_t *d_codes, const float *d_scales, int64_t rows,
+                      int64_t channels, void *d_x, void *stream);
+int launch_conv_backward(const ConvBackwardCall &c, void *stream);
+int launch_conv_step(const ConvStepCall &c, void *stream);
+int launch_embed(const int64_t *d_tokens, int64_t n, const void *d_table, int64_t table_rows,
+                 int64_t channels, float scale, int32_t out_type, void *d_out,
+                 int64_t *d_err_count, void *stream);
+int launch_embed_grad(const EmbedGradCall &c, const Plan &p, void *d_workspace, void *stream);
+
+}  // namespace engram
