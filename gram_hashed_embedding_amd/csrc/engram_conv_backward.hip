@@ -212,13 +212,15 @@ __global__ __launch_bounds__(kConvBlock) void conv_backward_k4_kernel(const Conv
 #pragma unroll
     for (int i = H - 1; i >= 0; --i) win[T + i] = win[i];
   }
-  if (!WANT_W || !p.on) return;
-  f32x4 *dst = reinterpret_cast<f32x4 *>(a.partials) +
-               (p.b * a.s.slices + p.slice) * (K + 1) * a.quads + p.quad;
+  if constexpr (WANT_W) {
+    if (!p.on) return;
+    f32x4 *dst = reinterpret_cast<f32x4 *>(a.partials) +
+                 (p.b * a.s.slices + p.slice) * (K + 1) * a.quads + p.quad;
 #pragma unroll
-  for (int j = 0; j < K; ++j)
-    dst[(K - 1 - j) * a.quads] = f32x4{sum_w[0][j], sum_w[1][j], sum_w[2][j], sum_w[3][j]};
-  dst[K * a.quads] = f32x4{sum_b[0], sum_b[1], sum_b[2], sum_b[3]};
+    for (int j = 0; j < K; ++j)
+      dst[(K - 1 - j) * a.quads] = f32x4{sum_w[0][j], sum_w[1][j], sum_w[2][j], sum_w[3][j]};
+    dst[K * a.quads] = f32x4{sum_b[0], sum_b[1], sum_b[2], sum_b[3]};
+  }
 }
 
 // Any K up to kConvMaxKernel and any dilation: the same walk, each row of g

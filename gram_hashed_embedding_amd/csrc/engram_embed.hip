@@ -12,12 +12,13 @@
 // The gradient.  The tokens are sorted as the hashed rows are (the plan of
 // engram_sort.hip), so a row's terms are one run of the sorted order and no
 // atomic is needed: the result does not depend on timing, and each row is
-// written once.  A block owns a range of adjacent table rows, finds its part
-// of the sorted tokens by a 64-way search and writes its rows from zero or
-// from their runs.  A frequent token's run is too long for one block: every
-// 64 sorted positions that are all of one token are summed beforehand into an
-// fp64 row, and the row's owner adds those.  Sums are fp64, as the hashed
-// table's, so runs may be cut anywhere.
+// written once.  Walkers take equal chunks of the sorted positions, however
+// the tokens crowd: a run inside a chunk is summed and written by its walker;
+// a run that crosses chunks leaves a part in each, which the walker of the
+// chunk it begins in adds up in a second, short kernel.  Beside the walkers,
+// in the same launch, the other blocks write the zeros of the rows without a
+// token (most of a vocabulary), found by a 64-way search of the sorted tokens
+// a block.  Sums are fp64, as the hashed table's.
 #include "engram_layer_dev.h"
 #include "engram_scatter_dev.h"
 
@@ -26,14 +27,6 @@ namespace {
 
 constexpr int kEmbedThreads = 256;
 constexpr int kEmbedRows = 4;  // rows of a lane in flight
-
-// A row of `chunks` chunks of 8 channels is covered by `lanes` threads (a
-// power of two, at most a block); a block takes 256 / lanes rows at a time.
-inline int row_lanes(int64_t chunks) {
-  int l = 1;
-  while (l < chunks && l < kEmbedThreads) l *= 2;
-  return l;
-}
 
 template <class OUT>
 __device__ __forceinline__ void store8(OUT *row, int64_t chunk, const float (&f)[8]);
@@ -45,8 +38,8 @@ __device__ __forceinline__ void store8<uint16_t>(uint16_t *row, int64_t chunk,
 template <>
 __device__ __forceinline__ void store8<float>(float *row, int64_t chunk, const float (&f)[8]) {
   f32x4 *q = reinterpret_cast<f32x4 *>(row) + 2 * chunk;
-  __builtin_nontemporal_store(f32x4{f[0], f[1], f[2], f[3]}, q);
-  __builtin_nontemporal_store(f32x4{f[4], f[5], f[6], f[7]}, q + 1);
+  q[0] = f32x4{f[0], f[1], f[2], f[3]};
+  q[1] = f32x4{f[4], f[5], f[6], f[7]};
 }
 
 template <class OUT>
@@ -88,12 +81,15 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_kernel(
 }
 
 // ---------------------------------------------------------------- gradient --
+// A row of `chunks` chunks of 8 channels is covered by `lanes` threads (a
+// power of two, at most a block).
 struct EmbedGradArgs {
   const uint32_t *keys, *vals;  // sorted tokens and their positions
   const PlanScalars *plan;
   const u32x4 *grads;
-  double *partials;
+  double *partials;  // [walks][2][channels]: of the run that enters, that leaves
   int64_t n, chunks, table_rows;
+  int64_t walks, walk_len, walk_blocks;
   int lanes, rows_per_block;
   float scale;
   void *out;
@@ -105,45 +101,83 @@ __device__ __forceinline__ bool plan_holds(const EmbedGradArgs &g) {
   return g.plan->stalled == 0 && g.plan->n == (uint64_t)g.n;
 }
 
-// Adds the gradient rows of the sorted positions [a, b), chunk c.
-__device__ __forceinline__ void add_rows(const EmbedGradArgs &g, int64_t a, int64_t b, int64_t c,
-                                         double (&sum)[8]) {
-  constexpr int kAhead = 8;
-  for (int64_t i = a; i < b; i += kAhead) {
-    u32x4 v[kAhead];
+template <class OUT, bool ACCUMULATE>
+__device__ __forceinline__ void write_row(const EmbedGradArgs &g, int64_t row, int64_t c,
+                                          const double (&sum)[8]) {
+  OUT *dst = static_cast<OUT *>(g.out) + row * g.chunks * 8;
+  float f[8];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      v[k] = i + k < b ? g.grads[(int64_t)g.vals[i + k] * g.chunks + c] : u32x4{0u, 0u, 0u, 0u};
+  for (int e = 0; e < 8; ++e) f[e] = (float)(sum[e] * (double)g.scale);
+  if (ACCUMULATE) {
+    const float *old = reinterpret_cast<const float *>(dst) + c * 8;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      float f[8];
-      unpack_bf16x8(v[k], f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] += f[e];
-    }
+    for (int e = 0; e < 8; ++e) f[e] = old[e] + f[e];
   }
+  store8<OUT>(dst, c, f);
 }
 
-// Sums of the kEmbedChunk-position chunks that are all of one token.
-__global__ __launch_bounds__(kEmbedThreads) void embed_chunk_kernel(const EmbedGradArgs g) {
-  const int64_t chunk = blockIdx.x;
-  const int64_t a = chunk * kEmbedChunk, b = a + kEmbedChunk;
-  if (!plan_holds(g)) return;
-  const uint32_t key = g.keys[a];
-  if (key >= g.table_rows || key != g.keys[b - 1]) return;
-  for (int64_t c = threadIdx.x; c < g.chunks; c += kEmbedThreads) {
+__device__ __forceinline__ void write_part(const EmbedGradArgs &g, int64_t walk, int which,
+                                           int64_t c, const double (&sum)[8]) {
+  f64x2 *dst = reinterpret_cast<f64x2 *>(g.partials + ((walk * 2 + which) * g.chunks + c) * 8);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) dst[e] = f64x2{sum[2 * e], sum[2 * e + 1]};
+}
+
+// A walker's chunk [a, b) of the sorted positions: its runs' sums.
+constexpr int kAhead = 8;  // rows in flight
+template <class OUT, bool ACCUMULATE>
+__device__ void walk_chunk(const EmbedGradArgs &g, int64_t walk, int lane) {
+  const int64_t a = walk * g.walk_len, b = min(a + g.walk_len, g.n);
+  const uint32_t before = a > 0 ? g.keys[a - 1] : 0xffffffffu;  // no key (they are smaller)
+  const uint32_t after = b < g.n ? g.keys[b] : 0xffffffffu;
+  for (int64_t c = lane; c < g.chunks; c += g.lanes) {
     double sum[8] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
-    add_rows(g, a, b, c, sum);
-    double *dst = g.partials + (chunk * g.chunks + c) * 8;
+    uint32_t run = g.keys[a];
+    bool entered = run == before;
+    for (int64_t i = a; i < b; i += kAhead) {
+      uint32_t key[kAhead];
+      u32x4 v[kAhead];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dst[e] = sum[e];
+      for (int k = 0; k < kAhead; ++k) {
+        const int64_t at = min(i + k, b - 1);
+        key[k] = g.keys[at];
+        v[k] = g.grads[(int64_t)g.vals[at] * g.chunks + c];
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (i + k >= b) break;
+        if (key[k] != run) {  // a run has ended in this chunk
+          if (run < g.table_rows) {
+            if (entered)
+              write_part(g, walk, 0, c, sum);
+            else
+              write_row<OUT, ACCUMULATE>(g, run, c, sum);
+          }
+          run = key[k];
+          entered = false;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum[e] = 0.0;
+        }
+        float f[8];
+        unpack_bf16x8(v[k], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += f[e];
+      }
+    }
+    if (run >= g.table_rows) continue;  // padding and invalid ids sort last
+    if (entered)
+      write_part(g, walk, 0, c, sum);
+    else if (run == after)
+      write_part(g, walk, 1, c, sum);
+    else
+      write_row<OUT, ACCUMULATE>(g, run, c, sum);
   }
 }
 
-// The first sorted position whose key is at least `key` (a wavefront
-// together: 64 probes a step).
-__device__ __forceinline__ int64_t lower_bound(const EmbedGradArgs &g, int64_t key) {
-  int64_t lo = 0, hi = g.n;
+// The first sorted position in [lo, n) whose key is at least `key` (a
+// wavefront together: 64 probes a step).
+__device__ __forceinline__ int64_t lower_bound(const EmbedGradArgs &g, int64_t lo, int64_t key) {
+  int64_t hi = g.n;
   while (lo < hi) {
     const int64_t step = (hi - lo + 63) / 64;
     const int64_t at = lo + ((int64_t)(threadIdx.x & 63) + 1) * step - 1;
@@ -158,69 +192,98 @@ __device__ __forceinline__ int64_t lower_bound(const EmbedGradArgs &g, int64_t k
 
 constexpr int kMaxRowsPerBlock = 256;
 
+// Blocks below walk_blocks walk the sorted tokens; the others write the zeros
+// of the rows without one.
 template <class OUT, bool ACCUMULATE>
-__global__ __launch_bounds__(kEmbedThreads) void embed_rows_kernel(const EmbedGradArgs g) {
+__global__ __launch_bounds__(kEmbedThreads) void embed_grad_kernel(const EmbedGradArgs g) {
   __shared__ int64_t bound[2];
-  __shared__ uint32_t begin[kMaxRowsPerBlock], end[kMaxRowsPerBlock];
-  const int64_t r0 = (int64_t)blockIdx.x * g.rows_per_block;
+  __shared__ uint32_t present[kMaxRowsPerBlock];
+  if (g.n > 0 && !plan_holds(g)) return;
+  const int slots = kEmbedThreads / g.lanes;
+  const int slot = threadIdx.x / g.lanes, lane = threadIdx.x % g.lanes;
+  if (blockIdx.x < g.walk_blocks) {
+    const int64_t walk = (int64_t)blockIdx.x * slots + slot;
+    if (walk < g.walks) walk_chunk<OUT, ACCUMULATE>(g, walk, lane);
+    return;
+  }
+  const int64_t r0 = ((int64_t)blockIdx.x - g.walk_blocks) * g.rows_per_block;
   const int64_t rows = min((int64_t)g.rows_per_block, g.table_rows - r0);
   int64_t lo = 0, hi = 0;
   if (g.n > 0) {
-    if (!plan_holds(g)) return;
     const int wave = threadIdx.x / kWave;
     if (wave < 2) {
-      const int64_t at = lower_bound(g, r0 + (wave == 0 ? 0 : rows));
+      const int64_t at = lower_bound(g, 0, r0 + (wave == 0 ? 0 : rows));
       if ((threadIdx.x & 63) == 0) bound[wave] = at;
     }
     __syncthreads();
     lo = bound[0];
     hi = bound[1];
   }
-  for (int i = threadIdx.x; i < rows; i += kEmbedThreads) begin[i] = end[i] = 0u;
+  if (threadIdx.x < rows) present[threadIdx.x] = 0u;
   __syncthreads();
-  for (int64_t i = lo + threadIdx.x; i < hi; i += kEmbedThreads) {
-    const uint32_t k = g.keys[i];
-    if (i == lo || g.keys[i - 1] != k) begin[k - r0] = (uint32_t)i;
-    if (i == hi - 1 || g.keys[i + 1] != k) end[k - r0] = (uint32_t)(i + 1);
+  for (int64_t i = lo + threadIdx.x; i < hi; i += kEmbedThreads) present[g.keys[i] - r0] = 1u;
+  __syncthreads();
+  // 16 bytes a lane, side by side
+  const int64_t words = g.chunks * (int64_t)(sizeof(OUT) / 2);
+  for (int64_t r = slot; r < rows; r += slots) {
+    if (present[r] != 0u) continue;
+    u32x4 *row = reinterpret_cast<u32x4 *>(static_cast<OUT *>(g.out) + (r0 + r) * g.chunks * 8);
+    for (int64_t c = lane; c < words; c += g.lanes)
+      __builtin_nontemporal_store(u32x4{0u, 0u, 0u, 0u}, row + c);
   }
-  __syncthreads();
+}
+
+// The runs that cross chunks: the walker of the chunk that one begins in adds
+// its parts, in order.
+template <class OUT, bool ACCUMULATE>
+__global__ __launch_bounds__(kEmbedThreads) void embed_join_kernel(const EmbedGradArgs g) {
   const int slots = kEmbedThreads / g.lanes;
-  const int lane = threadIdx.x % g.lanes;
-  for (int64_t r = threadIdx.x / g.lanes; r < rows; r += slots) {
-    const int64_t a = begin[r], b = end[r];
-    OUT *row = static_cast<OUT *>(g.out) + (r0 + r) * g.chunks * 8;
-    if (a == b) {
-      if (ACCUMULATE) continue;
-      const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      for (int64_t c = lane; c < g.chunks; c += g.lanes) store8<OUT>(row, c, zero);
-      continue;
-    }
-    const int64_t c0 = (a + kEmbedChunk - 1) / kEmbedChunk, c1 = b / kEmbedChunk;
-    for (int64_t c = lane; c < g.chunks; c += g.lanes) {
-      double sum[8] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
-      if (c0 < c1) {
-        add_rows(g, a, c0 * kEmbedChunk, c, sum);
-#pragma unroll 4
-        for (int64_t q = c0; q < c1; ++q) {
-          const double *src = g.partials + (q * g.chunks + c) * 8;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) sum[e] += src[e];
-        }
-        add_rows(g, c1 * kEmbedChunk, b, c, sum);
-      } else {
-        add_rows(g, a, b, c, sum);
-      }
-      float f[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = (float)(sum[e] * (double)g.scale);
-      if (ACCUMULATE) {
-        const float *old = reinterpret_cast<const float *>(row) + c * 8;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = old[e] + f[e];
-      }
-      store8<OUT>(row, c, f);
-    }
+  const int64_t walk = (int64_t)blockIdx.x * slots + threadIdx.x / g.lanes;
+  if (walk + 1 >= g.walks || !plan_holds(g)) return;
+  const int64_t a = walk * g.walk_len, b = a + g.walk_len;
+  const uint32_t run = g.keys[b - 1];
+  if (run >= g.table_rows || g.keys[b] != run) return;           // does not leave
+  if (g.keys[a] == run && a > 0 && g.keys[a - 1] == run) return;  // entered: another's
+  // the last chunk it reaches: chunks whose first key is the run's, so far
+  int64_t last = walk + 1, high = g.walks;  // first key of `last` is the run's; of `high` not
+  while (high - last > 1) {
+    const int64_t mid = last + (high - last) / 2;
+    if (g.keys[mid * g.walk_len] == run)
+      last = mid;
+    else
+      high = mid;
   }
+  for (int64_t c = threadIdx.x % g.lanes; c < g.chunks; c += g.lanes) {
+    double sum[8];
+    const f64x2 *src = reinterpret_cast<const f64x2 *>(g.partials) +
+                       ((walk * 2 + 1) * g.chunks + c) * 4;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const f64x2 v = src[e];
+      sum[2 * e] = v.x;
+      sum[2 * e + 1] = v.y;
+    }
+#pragma unroll 8
+    for (int64_t q = walk + 1; q <= last; ++q) {
+      src = reinterpret_cast<const f64x2 *>(g.partials) + (q * 2 * g.chunks + c) * 4;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const f64x2 v = src[e];
+        sum[2 * e] += v.x;
+        sum[2 * e + 1] += v.y;
+      }
+    }
+    write_row<OUT, ACCUMULATE>(g, run, c, sum);
+  }
+}
+
+template <class OUT, bool ACCUMULATE>
+void launch_grad(const EmbedGradArgs &g, unsigned blocks, hipStream_t s) {
+  const dim3 block(kEmbedThreads);
+  hipLaunchKernelGGL((embed_grad_kernel<OUT, ACCUMULATE>), dim3(blocks), block, 0, s, g);
+  if (g.walks > 1)
+    hipLaunchKernelGGL((embed_join_kernel<OUT, ACCUMULATE>), dim3((unsigned)g.walk_blocks), block,
+                       0, s, g);
 }
 
 }  // namespace
@@ -230,7 +293,7 @@ int engram::launch_embed(const int64_t *d_tokens, int64_t n, const void *d_table
                          int64_t table_rows, int64_t channels, float scale, int32_t out_type,
                          void *d_out, int64_t *d_err_count, void *stream) {
   const int64_t chunks = channels / 8;
-  const int lanes = row_lanes(chunks);
+  const int lanes = embed_row_lanes(channels);
   const int64_t blocks = ceil_div(n, (int64_t)(kEmbedThreads / lanes) * kEmbedRows);
   if (!grid_fits(blocks, kEmbedThreads)) return ENGRAM_EINVAL;
   const dim3 grid((unsigned)blocks), block(kEmbedThreads);
@@ -255,35 +318,33 @@ int engram::launch_embed_grad(const EmbedGradCall &c, const Plan &p, void *d_wor
   g.n = c.n;
   g.chunks = c.channels / 8;
   g.table_rows = c.table_rows;
-  g.lanes = row_lanes(g.chunks);
+  g.lanes = embed_row_lanes(c.channels);
   g.scale = c.scale;
   g.out = c.grad_table;
-  // about 128 KB of fp32 rows a block
+  // about 128 KB of fp32 rows a block of zeros
   g.rows_per_block = 8;
   while (g.rows_per_block < kMaxRowsPerBlock && g.rows_per_block * c.channels < 32768)
     g.rows_per_block *= 2;
-  const int64_t blocks = ceil_div(c.table_rows, g.rows_per_block);
-  const int64_t full_chunks = c.n / kEmbedChunk;
-  if (!grid_fits(blocks, kEmbedThreads) || !grid_fits(full_chunks, kEmbedThreads))
-    return ENGRAM_EINVAL;
+  g.walk_len = embed_chunk(c.n, c.channels);
+  g.walks = ceil_div(c.n, g.walk_len);
+  g.walk_blocks = ceil_div(g.walks, kEmbedThreads / g.lanes);
+  const int64_t zero_blocks = c.accumulate ? 0 : ceil_div(c.table_rows, g.rows_per_block);
+  const int64_t blocks = g.walk_blocks + zero_blocks;
+  if (!grid_fits(blocks, kEmbedThreads)) return ENGRAM_EINVAL;
   if (c.n > 0) {
     const Views v = views_of(p, d_workspace);
     g.keys = v.sorted_keys;
     g.vals = v.sorted_vals;
     g.plan = v.scalars;
-    const int rc = launch_plan(c.tokens, nullptr, c.n, c.table_rows, p, d_workspace, c.err,
-                               stream);
+    const int rc =
+        launch_plan_crowded(c.tokens, c.n, c.table_rows, p, d_workspace, c.err, stream);
     if (rc != ENGRAM_OK || c.table_rows == 0) return rc;
-    if (full_chunks > 0)
-      hipLaunchKernelGGL(embed_chunk_kernel, dim3((unsigned)full_chunks), dim3(kEmbedThreads), 0,
-                         st, g);
   }
-  const dim3 grid((unsigned)blocks), block(kEmbedThreads);
   if (c.accumulate)
-    hipLaunchKernelGGL((embed_rows_kernel<float, true>), grid, block, 0, st, g);
+    launch_grad<float, true>(g, (unsigned)blocks, st);
   else if (c.type == ENGRAM_F32)
-    hipLaunchKernelGGL((embed_rows_kernel<float, false>), grid, block, 0, st, g);
+    launch_grad<float, false>(g, (unsigned)blocks, st);
   else
-    hipLaunchKernelGGL((embed_rows_kernel<uint16_t, false>), grid, block, 0, st, g);
+    launch_grad<uint16_t, false>(g, (unsigned)blocks, st);
   return launch_status();
 }

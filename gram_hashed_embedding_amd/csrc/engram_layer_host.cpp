@@ -44,10 +44,8 @@ NormShape norm_shape(int64_t rows, int64_t channels, int64_t groups, int max_ite
   const int64_t steps = rows > 0 ? ceil_div(rows, s.trows) : 1;  // of trows rows each
   int64_t want = blocks * 256 / s.threads / s.colblocks;
   if (want < 1) want = 1;
-  int64_t per = ceil_div(steps, want);
-  if (per > kNormMaxSteps) per = kNormMaxSteps;
-  s.per_block = per * s.trows;
-  s.rowblocks = ceil_div(steps, per);
+  if (want * kNormMaxSteps < steps) want = ceil_div(steps, kNormMaxSteps);
+  s.rowblocks = steps < want ? steps : want;
   return s;
 }
 
@@ -313,7 +311,7 @@ bool embed_plan(int64_t n, int64_t table_rows, Plan *p) {
 }
 
 size_t embed_partials(int64_t n, int64_t channels) {
-  return (size_t)(n / kEmbedChunk) * (size_t)channels * 8;
+  return (size_t)ceil_div(n, embed_chunk(n, channels)) * 2 * (size_t)channels * 8;
 }
 
 }  // namespace

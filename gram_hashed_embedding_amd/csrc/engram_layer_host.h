@@ -17,11 +17,13 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // A group belongs to `lanes` threads, each holding `items` chunks of 8
 // channels; a block of `threads` threads holds threads / lanes groups at a
 // time: `gcols` adjacent groups of each of `trows` rows.  The grid is
-// `colblocks` column blocks times `rowblocks` blocks of `per_block` rows.
+// `colblocks` column blocks times `rowblocks` row blocks, which take the rows
+// `trows` at a time in turn: the blocks that run together then work on one
+// stretch of memory that moves on.
 struct NormShape {
   int64_t rows, channels, groups, chunks;
   int lanes, items, threads, gcols, trows;
-  int64_t colblocks, rowblocks, per_block;
+  int64_t colblocks, rowblocks;
 };
 
 // The shape for a kernel that holds at most max_items chunks a lane, with
@@ -83,9 +85,22 @@ struct ConvStepCall {
 };
 
 // --------------------------------------------------------------- embedding --
-// Sorted positions whose sum a block of the gradient leaves as one fp64 row
-// when they are all of one token.
-constexpr int64_t kEmbedChunk = 64;
+// The gradient's sorted tokens are cut into chunks of a power of two of
+// positions, one to a walker of row_lanes threads.  A chunk leaves up to two
+// fp64 rows: the part of the run that enters it, and of the one that leaves it.
+inline int embed_row_lanes(int64_t channels) {
+  int l = 1;
+  while (l < channels / 8 && l < 256) l *= 2;
+  return l;
+}
+inline int64_t embed_chunk(int64_t n, int64_t channels) {
+  // about 512 blocks of walkers, so that a frequent token's run is spread over
+  // the GPU while its parts stay few
+  const int64_t walkers = 512 * (256 / embed_row_lanes(channels));
+  int64_t chunk = 16;
+  while (chunk < 128 && chunk * walkers < n) chunk *= 2;
+  return chunk;
+}
 
 struct EmbedGradCall {
   const int64_t *tokens;
@@ -96,7 +111,7 @@ struct EmbedGradCall {
   int64_t table_rows;
   int32_t type, accumulate;
   void *grad_table;
-  double *partials;  // [n / kEmbedChunk][channels]
+  double *partials;  // [chunks][2][channels]
   int64_t *err;
 };
 

@@ -31,21 +31,15 @@ namespace {
 struct NormArgs {
   NormShape s;
   const void *residual;
-  const u32x4 *y;
-  const void *gate;
-  const u32x4 *w_post, *scale, *w_next;
-  void *out;
-  u32x4 *next;
+  const void *y, *gate, *w_post, *scale, *w_next;
+  void *out, *next;
   float *rstd_post, *rstd_next;
-  u32x2 *y_codes;
+  int8_t *y_codes;
   float *y_scales;
-  u32x2 *next_codes;
+  int8_t *next_codes;
   float *next_scales;
-  const void *grad_out;
-  const u32x4 *grad_next;
-  void *grad_residual;
-  u32x4 *grad_y;
-  void *grad_gate;
+  const void *grad_out, *grad_next;
+  void *grad_residual, *grad_y, *grad_gate;
   float *partials;  // [rowblocks][2][channels]: sums of dR a yh, of grad_next xh
   float *grad_w_post, *grad_scale, *grad_w_next;
   int64_t code_blocks;  // 8-bit blocks of a group
@@ -53,46 +47,117 @@ struct NormArgs {
   int gate_kind;  // 0 none, 1 one a group, 2 one a channel
 };
 
-// Eight values of a row of type RT (bf16 bits or float), chunk c.
+// A lane's eight values of a group are two runs of four channels, at the
+// offsets a and b of the group.  With a bf16 stream they are adjacent (16
+// bytes a lane).  With a float stream they are LANES runs apart, so that a
+// wavefront's 16-byte accesses of the stream are side by side too (32 bytes a
+// lane in two halves made every line be touched twice: the non-temporal
+// stores of a float stream then ran at a third of their rate).
+struct Span {
+  int a, b;
+  bool on_a, on_b;
+};
+template <class RT>
+constexpr bool kSplit = sizeof(RT) == 4;
+
+template <class RT, int LANES>
+__device__ __forceinline__ Span span_of(int lane, int item, int n, bool ok) {
+  Span p;
+  if (kSplit<RT>) {
+    p.a = (lane + 2 * item * LANES) * 4;
+    p.b = p.a + LANES * 4;
+  } else {
+    p.a = (lane + item * LANES) * 8;
+    p.b = p.a + 4;
+  }
+  p.on_a = ok && p.a < n;
+  p.on_b = ok && p.b < n;
+  return p;
+}
+
+// bf16 arrays: eight values as four words, zero where there is none.
+template <class RT>
+__device__ __forceinline__ u32x4 load_bf16(const void *base, int64_t at, const Span &p,
+                                           bool live) {
+  const uint16_t *q = static_cast<const uint16_t *>(base) + at;
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if (kSplit<RT>) {
+    if (p.on_a && live) {
+      const u32x2 h = *reinterpret_cast<const u32x2 *>(q + p.a);
+      v.x = h.x;
+      v.y = h.y;
+    }
+    if (p.on_b && live) {
+      const u32x2 h = *reinterpret_cast<const u32x2 *>(q + p.b);
+      v.z = h.x;
+      v.w = h.y;
+    }
+  } else if (p.on_a && live) {
+    v = *reinterpret_cast<const u32x4 *>(q + p.a);
+  }
+  return v;
+}
+template <class RT>
+__device__ __forceinline__ void store_bf16(void *base, int64_t at, const Span &p, bool live,
+                                           const u32x4 &v) {
+  uint16_t *q = static_cast<uint16_t *>(base) + at;
+  if (kSplit<RT>) {
+    if (p.on_a && live)
+      __builtin_nontemporal_store(u32x2{v.x, v.y}, reinterpret_cast<u32x2 *>(q + p.a));
+    if (p.on_b && live)
+      __builtin_nontemporal_store(u32x2{v.z, v.w}, reinterpret_cast<u32x2 *>(q + p.b));
+  } else if (p.on_a && live) {
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(q + p.a));
+  }
+}
+
+// Rows of the stream: bf16 bits (uint16_t) or float.
 template <class RT>
 struct Row;
 template <>
 struct Row<uint16_t> {
   typedef u32x4 Raw;
-  static __device__ __forceinline__ Raw load(const void *p, int64_t c) {
-    return static_cast<const u32x4 *>(p)[c];
+  static __device__ __forceinline__ Raw load(const void *base, int64_t at, const Span &p,
+                                             bool live) {
+    return load_bf16<uint16_t>(base, at, p, live);
   }
   static __device__ __forceinline__ void unpack(const Raw &r, float (&f)[8]) {
     unpack_bf16x8(r, f);
   }
   // Rounds f to what is stored.
-  static __device__ __forceinline__ void store(void *p, int64_t c, float (&f)[8]) {
+  static __device__ __forceinline__ void store(void *base, int64_t at, const Span &p, bool live,
+                                               float (&f)[8]) {
     const u32x4 v = pack_bf16x8(f);
-    static_cast<u32x4 *>(p)[c] = v;
+    store_bf16<uint16_t>(base, at, p, live, v);
     unpack_bf16x8(v, f);
   }
-  static __device__ __forceinline__ Raw zero() { return Raw{0u, 0u, 0u, 0u}; }
 };
 template <>
 struct Row<float> {
   struct Raw {
     f32x4 a, b;
   };
-  static __device__ __forceinline__ Raw load(const void *p, int64_t c) {
-    const f32x4 *q = static_cast<const f32x4 *>(p) + 2 * c;
-    return Raw{q[0], q[1]};
+  static __device__ __forceinline__ Raw load(const void *base, int64_t at, const Span &p,
+                                             bool live) {
+    const float *q = static_cast<const float *>(base) + at;
+    Raw r = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+    if (p.on_a && live) r.a = *reinterpret_cast<const f32x4 *>(q + p.a);
+    if (p.on_b && live) r.b = *reinterpret_cast<const f32x4 *>(q + p.b);
+    return r;
   }
   static __device__ __forceinline__ void unpack(const Raw &r, float (&f)[8]) {
     f[0] = r.a.x; f[1] = r.a.y; f[2] = r.a.z; f[3] = r.a.w;
     f[4] = r.b.x; f[5] = r.b.y; f[6] = r.b.z; f[7] = r.b.w;
   }
-  static __device__ __forceinline__ void store(void *p, int64_t c, float (&f)[8]) {
-    f32x4 *q = static_cast<f32x4 *>(p) + 2 * c;
-    q[0] = f32x4{f[0], f[1], f[2], f[3]};
-    q[1] = f32x4{f[4], f[5], f[6], f[7]};
-  }
-  static __device__ __forceinline__ Raw zero() {
-    return Raw{f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+  static __device__ __forceinline__ void store(void *base, int64_t at, const Span &p, bool live,
+                                               float (&f)[8]) {
+    float *q = static_cast<float *>(base) + at;
+    if (p.on_a && live)
+      __builtin_nontemporal_store(f32x4{f[0], f[1], f[2], f[3]},
+                                  reinterpret_cast<f32x4 *>(q + p.a));
+    if (p.on_b && live)
+      __builtin_nontemporal_store(f32x4{f[4], f[5], f[6], f[7]},
+                                  reinterpret_cast<f32x4 *>(q + p.b));
   }
 };
 
@@ -124,23 +189,78 @@ __device__ __forceinline__ float gate_at(const void *gate, int64_t i) {
   return bf16_lo(static_cast<const uint16_t *>(gate)[i]);
 }
 
-// 8-bit codes of a lane's chunk `c8` of the row (chunk j of the group).  The
-// 16 lanes (or the group's fewer) that share a block take its maximum.
-template <int LANES>
-__device__ __forceinline__ void store_codes(const float (&x)[8], bool ok, int64_t c8, int64_t j,
-                                            int64_t unit, int64_t code_blocks, u32x2 *codes,
-                                            float *scales) {
-  const uint32_t m = lanes_max<(LANES < 16 ? LANES : 16)>(ok ? max_magnitude(x) : 0u);
-  const CodeScale cs = code_scale(m);
-  if (!ok) return;
-  codes[c8] = code_bytes8(x, cs.inv);
-  if ((j & 15) == 0) scales[unit * code_blocks + (j >> 4)] = cs.scale;
+// The 8-bit codes of a lane's eight values.  The lanes whose values lie in one
+// block of 128 channels take their maximum together: 16 lanes of adjacent
+// values; 32 of split ones (a run each), or, in a group of at most 128
+// channels, all its lanes with both runs.
+template <class RT, int LANES>
+__device__ __forceinline__ void store_codes(const float (&x)[8], const Span &p, bool live,
+                                            int64_t at, int64_t unit, int64_t code_blocks,
+                                            int8_t *codes, float *scales) {
+  uint32_t ma = 0u, mb = 0u;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t xa = __float_as_uint(x[e]) & 0x7fffffffu;
+    const uint32_t xb = __float_as_uint(x[4 + e]) & 0x7fffffffu;
+    ma = xa > ma ? xa : ma;
+    mb = xb > mb ? xb : mb;
+  }
+  ma = p.on_a && live ? ma : 0u;
+  mb = p.on_b && live ? mb : 0u;
+  float *scale = scales + unit * code_blocks;
+  if (kSplit<RT> && LANES >= 32) {
+    const CodeScale ca = code_scale(lanes_max<32>(ma)), cb = code_scale(lanes_max<32>(mb));
+    if (p.on_a && live) {
+      *reinterpret_cast<uint32_t *>(codes + at + p.a) = code_bytes(x, ca.inv);
+      if (p.a % 128 == 0) scale[p.a / 128] = ca.scale;
+    }
+    if (p.on_b && live) {
+      *reinterpret_cast<uint32_t *>(codes + at + p.b) = code_bytes(x + 4, cb.inv);
+      if (p.b % 128 == 0) scale[p.b / 128] = cb.scale;
+    }
+    return;
+  }
+  const CodeScale c = code_scale(lanes_max<(LANES < 16 ? LANES : 16)>(ma > mb ? ma : mb));
+  if (kSplit<RT>) {
+    if (p.on_a && live) *reinterpret_cast<uint32_t *>(codes + at + p.a) = code_bytes(x, c.inv);
+    if (p.on_b && live) *reinterpret_cast<uint32_t *>(codes + at + p.b) = code_bytes(x + 4, c.inv);
+  } else if (p.on_a && live) {
+    *reinterpret_cast<u32x2 *>(codes + at + p.a) = code_bytes8(x, c.inv);
+  }
+  if (p.on_a && live && p.a % 128 == 0) scale[p.a / 128] = c.scale;
+}
+
+// Eight codes and their scales, zero where there is none.
+struct Codes {
+  u32x2 words;
+  float scale_a, scale_b;
+};
+template <class RT>
+__device__ __forceinline__ Codes load_codes(const int8_t *codes, const float *scales, int64_t at,
+                                            int64_t unit, int64_t code_blocks, const Span &p,
+                                            bool live) {
+  Codes c = {u32x2{0u, 0u}, 0.0f, 0.0f};
+  const float *scale = scales + unit * code_blocks;
+  if (kSplit<RT>) {
+    if (p.on_a && live) {
+      c.words.x = *reinterpret_cast<const uint32_t *>(codes + at + p.a);
+      c.scale_a = scale[p.a / 128];
+    }
+    if (p.on_b && live) {
+      c.words.y = *reinterpret_cast<const uint32_t *>(codes + at + p.b);
+      c.scale_b = scale[p.b / 128];
+    }
+  } else if (p.on_a && live) {
+    c.words = *reinterpret_cast<const u32x2 *>(codes + at + p.a);
+    c.scale_a = c.scale_b = scale[p.a / 128];
+  }
+  return c;
 }
 
 // Where a block's threads stand.
 struct Place {
   int lane, trow;
-  int64_t group, row0, row_end;
+  int64_t group, row0, stride;  // rows row0, row0 + stride, ...
   bool group_ok;
 };
 template <int LANES, int THREADS>
@@ -152,8 +272,8 @@ __device__ __forceinline__ Place place_of(const NormShape &s) {
   const int64_t cb = blockIdx.x % s.colblocks, rb = blockIdx.x / s.colblocks;
   p.group = cb * s.gcols + slot % s.gcols;
   p.group_ok = p.group < s.groups;
-  p.row0 = rb * s.per_block;
-  p.row_end = min(p.row0 + s.per_block, s.rows);
+  p.row0 = rb * s.trows;
+  p.stride = s.rowblocks * s.trows;
   return p;
 }
 
@@ -161,46 +281,42 @@ template <class RT, int LANES, int ITEMS, int THREADS>
 __global__ __launch_bounds__(THREADS) void norm_forward_kernel(const NormArgs a) {
   __shared__ float part[2][16];
   const Place p = place_of<LANES, THREADS>(a.s);
-  const int64_t row_chunks = a.s.channels / 8;
-  const int64_t g0 = p.group * a.s.chunks;  // the group's first chunk of a row
-  bool on[ITEMS];
+  const int n = (int)a.s.chunks * 8;
+  const int64_t g0 = p.group * n;  // the group's first channel
+  Span sp[ITEMS];
   float sw[ITEMS][8];
   u32x4 wn[ITEMS];
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
-    const int64_t j = p.lane + (int64_t)i * LANES;
-    on[i] = p.group_ok && j < a.s.chunks;
-    const int64_t c = on[i] ? g0 + j : 0;
-    float f[8];
+    sp[i] = span_of<RT, LANES>(p.lane, i, n, p.group_ok);
 #pragma unroll
     for (int e = 0; e < 8; ++e) sw[i][e] = 1.0f;
-    if (a.scale != nullptr) unpack_bf16x8(a.scale[c], sw[i]);
+    if (a.scale != nullptr) unpack_bf16x8(load_bf16<RT>(a.scale, g0, sp[i], true), sw[i]);
     if (a.w_post != nullptr) {
-      unpack_bf16x8(a.w_post[c], f);
+      float f[8];
+      unpack_bf16x8(load_bf16<RT>(a.w_post, g0, sp[i], true), f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) sw[i][e] *= f[e];
     }
-    wn[i] = a.w_next != nullptr ? a.w_next[c] : u32x4{0u, 0u, 0u, 0u};
+    wn[i] = u32x4{0u, 0u, 0u, 0u};
+    if (a.w_next != nullptr) wn[i] = load_bf16<RT>(a.w_next, g0, sp[i], true);
   }
-  for (int64_t t0 = p.row0; t0 < p.row_end; t0 += a.s.trows) {
+  for (int64_t t0 = p.row0; t0 < a.s.rows; t0 += p.stride) {
     const int64_t t = t0 + p.trow;
-    const bool row_ok = t < p.row_end;
-    const int64_t tt = row_ok ? t : p.row0;
-    const int64_t unit = tt * a.s.groups + p.group;
-    const int64_t base = tt * row_chunks + g0;
+    const bool row_ok = t < a.s.rows;
+    const int64_t unit = t * a.s.groups + p.group;
+    const int64_t at = t * a.s.channels + g0;
     typename Row<RT>::Raw r[ITEMS];
     u32x4 y[ITEMS], z[ITEMS];
     float zg = 0.0f;
     // every load of the row before the first use
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-      const int64_t c = base + p.lane + (int64_t)i * LANES;
-      r[i] = on[i] ? Row<RT>::load(a.residual, c) : Row<RT>::zero();
-      if (a.y != nullptr) y[i] = on[i] ? a.y[c] : u32x4{0u, 0u, 0u, 0u};
-      if (a.gate_kind == 2)
-        z[i] = on[i] ? static_cast<const u32x4 *>(a.gate)[c] : u32x4{0u, 0u, 0u, 0u};
+      r[i] = Row<RT>::load(a.residual, at, sp[i], row_ok);
+      if (a.y != nullptr) y[i] = load_bf16<RT>(a.y, at, sp[i], row_ok);
+      if (a.gate_kind == 2) z[i] = load_bf16<RT>(a.gate, at, sp[i], row_ok);
     }
-    if (a.gate_kind == 1 && p.group_ok) zg = gate_at(a.gate, unit);
+    if (a.gate_kind == 1 && p.group_ok && row_ok) zg = gate_at(a.gate, unit);
     float o[ITEMS][8];
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) Row<RT>::unpack(r[i], o[i]);
@@ -222,9 +338,8 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(const NormArgs a)
         float f[8];
         unpack_bf16x8(y[i], f);
         if (a.y_codes != nullptr)
-          store_codes<LANES>(f, on[i] && row_ok, base + p.lane + (int64_t)i * LANES,
-                             p.lane + (int64_t)i * LANES, unit, a.code_blocks, a.y_codes,
-                             a.y_scales);
+          store_codes<RT, LANES>(f, sp[i], row_ok, at, unit, a.code_blocks, a.y_codes,
+                                 a.y_scales);
         if (a.gate_kind == 2) {
           float zf[8];
           unpack_bf16x8(z[i], zf);
@@ -238,8 +353,7 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(const NormArgs a)
 #pragma unroll
           for (int e = 0; e < 8; ++e) o[i][e] = a.alpha * o[i][e] + sw[i][e] * (f[e] * ua);
         }
-        if (on[i] && row_ok)
-          Row<RT>::store(a.out, base + p.lane + (int64_t)i * LANES, o[i]);
+        Row<RT>::store(a.out, at, sp[i], row_ok, o[i]);
       }
       if (a.rstd_post != nullptr && p.lane == 0 && p.group_ok && row_ok) a.rstd_post[unit] = u;
     }
@@ -248,7 +362,8 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(const NormArgs a)
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sq += on[i] ? o[i][e] * o[i][e] : 0.0f;
+        for (int e = 0; e < 8; ++e)
+          sq += (e < 4 ? sp[i].on_a : sp[i].on_b) ? o[i][e] * o[i][e] : 0.0f;
       const float v = 1.0f / sqrtf(group_sum<LANES>(sq, part, 1) * a.inv_n + a.eps);
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i) {
@@ -257,12 +372,11 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(const NormArgs a)
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e] *= o[i][e] * v;
         const u32x4 packed = pack_bf16x8(w);
-        const int64_t j = p.lane + (int64_t)i * LANES;
-        if (on[i] && row_ok) a.next[base + j] = packed;
+        store_bf16<RT>(a.next, at, sp[i], row_ok, packed);
         if (a.next_codes != nullptr) {
           unpack_bf16x8(packed, w);
-          store_codes<LANES>(w, on[i] && row_ok, base + j, j, unit, a.code_blocks, a.next_codes,
-                             a.next_scales);
+          store_codes<RT, LANES>(w, sp[i], row_ok, at, unit, a.code_blocks, a.next_codes,
+                                 a.next_scales);
         }
       }
       if (a.rstd_next != nullptr && p.lane == 0 && p.group_ok && row_ok) a.rstd_next[unit] = v;
@@ -275,53 +389,44 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(const NormArgs a
   __shared__ float part[2][16];
   __shared__ float sums[THREADS == LANES ? 1 : THREADS * ITEMS * 8];
   const Place p = place_of<LANES, THREADS>(a.s);
-  const int64_t row_chunks = a.s.channels / 8;
-  const int64_t g0 = p.group * a.s.chunks;
-  bool on[ITEMS];
+  const int n = (int)a.s.chunks * 8;
+  const int64_t g0 = p.group * n;
+  Span sp[ITEMS];
   u32x4 wp[ITEMS], sc[ITEMS], wn[ITEMS];
   float sum_d[ITEMS][8], sum_n[ITEMS][8];
-  const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
-    const int64_t j = p.lane + (int64_t)i * LANES;
-    on[i] = p.group_ok && j < a.s.chunks;
-    const int64_t c = on[i] ? g0 + j : 0;
-    wp[i] = a.w_post != nullptr ? a.w_post[c] : ones;
-    sc[i] = a.scale != nullptr ? a.scale[c] : ones;
-    wn[i] = a.w_next != nullptr ? a.w_next[c] : ones;
+    sp[i] = span_of<RT, LANES>(p.lane, i, n, p.group_ok);
+    const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+    wp[i] = sc[i] = wn[i] = ones;
+    if (a.w_post != nullptr) wp[i] = load_bf16<RT>(a.w_post, g0, sp[i], true);
+    if (a.scale != nullptr) sc[i] = load_bf16<RT>(a.scale, g0, sp[i], true);
+    if (a.w_next != nullptr) wn[i] = load_bf16<RT>(a.w_next, g0, sp[i], true);
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum_d[i][e] = sum_n[i][e] = 0.0f;
   }
   const bool branch = a.y != nullptr || a.y_codes != nullptr;
-  const u32x4 zero4 = {0u, 0u, 0u, 0u};
-  for (int64_t t0 = p.row0; t0 < p.row_end; t0 += a.s.trows) {
+  for (int64_t t0 = p.row0; t0 < a.s.rows; t0 += p.stride) {
     const int64_t t = t0 + p.trow;
-    const bool row_ok = t < p.row_end;
-    const int64_t tt = row_ok ? t : p.row0;
-    const int64_t unit = tt * a.s.groups + p.group;
-    const int64_t base = tt * row_chunks + g0 + p.lane;
+    const bool row_ok = t < a.s.rows;  // a lane without a value reads nothing and adds zeros
+    const int64_t unit = t * a.s.groups + p.group;
+    const int64_t at = t * a.s.channels + g0;
     typename Row<RT>::Raw go[ITEMS], ro[ITEMS];
     u32x4 gn[ITEMS], y[ITEMS], z[ITEMS];
-    u32x2 yc[ITEMS];
-    float ys[ITEMS];
-    bool live[ITEMS];
+    Codes yc[ITEMS];
     float u = 0.0f, v = 0.0f, zg = 0.0f;
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-      const int64_t j = p.lane + (int64_t)i * LANES, c = base + (int64_t)i * LANES;
-      live[i] = on[i] && row_ok;  // a lane without a value reads nothing and adds zeros
-      go[i] = live[i] && a.grad_out != nullptr ? Row<RT>::load(a.grad_out, c) : Row<RT>::zero();
+      go[i] = Row<RT>::load(a.grad_out, at, sp[i], row_ok && a.grad_out != nullptr);
       if (a.grad_next != nullptr) {
-        gn[i] = live[i] ? a.grad_next[c] : zero4;
-        ro[i] = live[i] ? Row<RT>::load(a.out, c) : Row<RT>::zero();
+        gn[i] = load_bf16<RT>(a.grad_next, at, sp[i], row_ok);
+        ro[i] = Row<RT>::load(a.out, at, sp[i], row_ok);
       }
-      if (a.y != nullptr) {
-        y[i] = live[i] ? a.y[c] : zero4;
-      } else if (a.y_codes != nullptr) {
-        yc[i] = live[i] ? a.y_codes[c] : u32x2{0u, 0u};
-        ys[i] = live[i] ? a.y_scales[unit * a.code_blocks + (j >> 4)] : 0.0f;
-      }
-      if (a.gate_kind == 2) z[i] = live[i] ? static_cast<const u32x4 *>(a.gate)[c] : zero4;
+      if (a.y != nullptr)
+        y[i] = load_bf16<RT>(a.y, at, sp[i], row_ok);
+      else if (a.y_codes != nullptr)
+        yc[i] = load_codes<RT>(a.y_codes, a.y_scales, at, unit, a.code_blocks, sp[i], row_ok);
+      if (a.gate_kind == 2) z[i] = load_bf16<RT>(a.gate, at, sp[i], row_ok);
     }
     if (p.group_ok && row_ok) {
       if (branch) u = a.rstd_post[unit];
@@ -369,8 +474,8 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(const NormArgs a
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            yh[i][e] = code_value(yc[i].x, e, ys[i]);
-            yh[i][4 + e] = code_value(yc[i].y, e, ys[i]);
+            yh[i][e] = code_value(yc[i].words.x, e, yc[i].scale_a);
+            yh[i][4 + e] = code_value(yc[i].words.y, e, yc[i].scale_b);
           }
         }
         unpack_bf16x8(wp[i], w);
@@ -390,8 +495,8 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(const NormArgs a
             q[i][e] *= ac;
             zf[e] = bc * (q[i][e] * (w[e] * k[e])) * yh[i][e];
           }
-          if (a.grad_gate != nullptr && live[i])
-            static_cast<u32x4 *>(a.grad_gate)[base + (int64_t)i * LANES] = pack_bf16x8(zf);
+          if (a.grad_gate != nullptr)
+            store_bf16<RT>(a.grad_gate, at, sp[i], row_ok, pack_bf16x8(zf));
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -407,7 +512,7 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(const NormArgs a
         for (int i = 0; i < ITEMS; ++i) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) q[i][e] = u * (q[i][e] - yh[i][e] * m);
-          if (live[i]) a.grad_y[base + (int64_t)i * LANES] = pack_bf16x8(q[i]);
+          store_bf16<RT>(a.grad_y, at, sp[i], row_ok, pack_bf16x8(q[i]));
         }
       }
       if (a.gate_kind == 1 && a.grad_gate != nullptr && p.lane == 0 && p.group_ok && row_ok)
@@ -418,7 +523,7 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(const NormArgs a
       for (int i = 0; i < ITEMS; ++i) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) dr[i][e] *= a.alpha;
-        if (live[i]) Row<RT>::store(a.grad_residual, base + (int64_t)i * LANES, dr[i]);
+        Row<RT>::store(a.grad_residual, at, sp[i], row_ok, dr[i]);
       }
     }
   }
@@ -446,14 +551,15 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(const NormArgs a
       }
     }
     if (p.trow == 0) {
+      float *dst = a.partials + (rb * 2 + which) * a.s.channels + g0;
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i) {
-        const int64_t j = p.lane + (int64_t)i * LANES;
-        if (!on[i]) continue;
-        f32x4 *dst = reinterpret_cast<f32x4 *>(a.partials + (rb * 2 + which) * a.s.channels) +
-                     2 * (g0 + j);
-        dst[0] = f32x4{mine[i][0], mine[i][1], mine[i][2], mine[i][3]};
-        dst[1] = f32x4{mine[i][4], mine[i][5], mine[i][6], mine[i][7]};
+        if (sp[i].on_a)
+          *reinterpret_cast<f32x4 *>(dst + sp[i].a) =
+              f32x4{mine[i][0], mine[i][1], mine[i][2], mine[i][3]};
+        if (sp[i].on_b)
+          *reinterpret_cast<f32x4 *>(dst + sp[i].b) =
+              f32x4{mine[i][4], mine[i][5], mine[i][6], mine[i][7]};
       }
     }
   }
@@ -484,8 +590,8 @@ __global__ __launch_bounds__(kJoinThreads) void norm_join_kernel(const NormArgs 
     d += part[0][w][lane];
     n += part[1][w][lane];
   }
-  const uint16_t *wp = reinterpret_cast<const uint16_t *>(a.w_post);
-  const uint16_t *sc = reinterpret_cast<const uint16_t *>(a.scale);
+  const uint16_t *wp = static_cast<const uint16_t *>(a.w_post);
+  const uint16_t *sc = static_cast<const uint16_t *>(a.scale);
   if (a.grad_w_post != nullptr) a.grad_w_post[c] = (float)(d * (sc ? bf16_lo(sc[c]) : 1.0f));
   if (a.grad_scale != nullptr) a.grad_scale[c] = (float)(d * (wp ? bf16_lo(wp[c]) : 1.0f));
   if (a.grad_w_next != nullptr) a.grad_w_next[c] = (float)n;
@@ -495,23 +601,23 @@ NormArgs norm_args(const engram_norm_args &c, const NormShape &s) {
   NormArgs a = {};
   a.s = s;
   a.residual = c.d_residual;
-  a.y = static_cast<const u32x4 *>(c.d_y);
+  a.y = c.d_y;
   a.gate = c.d_gate;
-  a.w_post = static_cast<const u32x4 *>(c.d_w_post);
-  a.scale = static_cast<const u32x4 *>(c.d_scale);
-  a.w_next = static_cast<const u32x4 *>(c.d_w_next);
+  a.w_post = c.d_w_post;
+  a.scale = c.d_scale;
+  a.w_next = c.d_w_next;
   a.out = c.d_out;
-  a.next = static_cast<u32x4 *>(c.d_next);
+  a.next = c.d_next;
   a.rstd_post = c.d_rstd_post;
   a.rstd_next = c.d_rstd_next;
-  a.y_codes = reinterpret_cast<u32x2 *>(c.d_y_codes);
+  a.y_codes = c.d_y_codes;
   a.y_scales = c.d_y_scales;
-  a.next_codes = reinterpret_cast<u32x2 *>(c.d_next_codes);
+  a.next_codes = c.d_next_codes;
   a.next_scales = c.d_next_scales;
   a.grad_out = c.d_grad_out;
-  a.grad_next = static_cast<const u32x4 *>(c.d_grad_next);
+  a.grad_next = c.d_grad_next;
   a.grad_residual = c.d_grad_residual;
-  a.grad_y = static_cast<u32x4 *>(c.d_grad_y);
+  a.grad_y = c.d_grad_y;
   a.grad_gate = c.d_grad_gate;
   a.grad_w_post = c.d_grad_w_post;
   a.grad_scale = c.d_grad_scale;

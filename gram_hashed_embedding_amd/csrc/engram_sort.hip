@@ -1045,8 +1045,12 @@ void launch_pass(int src, const SortLayout &L, const PassArgs &a, hipStream_t s)
 // Plan: sort the row ids and give every distinct row its slot (U and the
 // plan's stamp are left in the workspace scalars).  Needs only the ids: given (ids), or computed
 // from the tokens (hp, when ids is null).
-int engram::launch_plan(const int64_t *ids, const HashParams *hp, int64_t n, int64_t table_rows,
-                        const Plan &p, void *ws, int64_t *err, void *stream) {
+namespace engram {
+namespace {
+
+// The plan; id_buckets: whether given ids may take the one-pass bucket sort.
+int plan_of(const int64_t *ids, const HashParams *hp, int64_t n, int64_t table_rows,
+            const Plan &p, void *ws, int64_t *err, void *stream, bool id_buckets) {
   hipStream_t s = as_stream(stream);
   const Views v = views_of(p, ws);
   uint32_t *tickets = v.counters;              // [4], then the slot scan's
@@ -1060,7 +1064,7 @@ int engram::launch_plan(const int64_t *ids, const HashParams *hp, int64_t n, int
   int top_bits = 0;
   if (heads && L.sg.len > kLdsSortKeys && L.bits > kBucketLow && L.bits <= kBucketLow + 8)
     top_bits = L.bits - kBucketLow;
-  if (ids != nullptr && n > kSortTile && n <= kIdBucketKeys) {
+  if (ids != nullptr && id_buckets && n > kSortTile && n <= kIdBucketKeys) {
     const int want = bit_width_u64((uint64_t)(n - 1) / 512);  // about 512 ids a bucket
     const int top = want < 8 ? want : 8;
     if (L.bits - top >= 9 && L.bits - top <= kBucketMaxLow) top_bits = top;
@@ -1181,4 +1185,17 @@ int engram::launch_plan(const int64_t *ids, const HashParams *hp, int64_t n, int
                      v.sorted_keys, n, (uint32_t)table_rows, p.num_ranges, v.status + sort_words,
                      tickets + kSlotTicketAt, v.head_off, v.scalars, err);
   return launch_status();
+}
+
+}  // namespace
+}  // namespace engram
+
+int engram::launch_plan(const int64_t *ids, const HashParams *hp, int64_t n, int64_t table_rows,
+                        const Plan &p, void *ws, int64_t *err, void *stream) {
+  return plan_of(ids, hp, n, table_rows, p, ws, err, stream, true);
+}
+
+int engram::launch_plan_crowded(const int64_t *ids, int64_t n, int64_t table_rows, const Plan &p,
+                                void *ws, int64_t *err, void *stream) {
+  return plan_of(ids, nullptr, n, table_rows, p, ws, err, stream, false);
 }

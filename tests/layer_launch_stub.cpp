@@ -20,7 +20,7 @@ int launch_residual_norm(const engram_norm_args &a) {
   require((a.d_w_next != nullptr) == (a.d_next != nullptr));
   const NormShape s =
       norm_shape(a.rows, a.channels, a.groups, kNormForwardItems, kNormForwardBlocks);
-  require((int64_t)s.lanes * s.items >= s.chunks && s.rowblocks * s.per_block >= a.rows);
+  require((int64_t)s.lanes * s.items >= s.chunks && s.rowblocks >= 1);
   return ENGRAM_OK;
 }
 
