@@ -148,7 +148,7 @@ class EngramNormArgs(ctypes.Structure):
 def declare_layer(lib):
     """declare() for the entry points of include/engram_layer.h."""
     i64, i32, f32, size = ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
-    norm = ctypes.POINTER(EngramNormArgs)
+    norm = _vp  # an EngramNormArgs by reference, or its bytes
     for name, result, args in [
         ("engram_residual_norm", ctypes.c_int, [norm]),
         ("engram_residual_norm_backward_workspace", size, [i64, i64, i64]),

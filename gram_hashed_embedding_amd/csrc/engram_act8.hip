@@ -83,11 +83,8 @@ __global__ __launch_bounds__(kActThreads) void act_decode_kernel(const ActArgs a
   for (int k = 0; k < kActUnroll; ++k) {
     if (!p[k].ok) continue;
     float f[8];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      f[e] = code_value(v[k].x, e, s[k]);
-      f[4 + e] = code_value(v[k].y, e, s[k]);
-    }
+    code_values(v[k].x, s[k], f);
+    code_values(v[k].y, s[k], f + 4);
     a.out[p[k].chunk] = pack_bf16x8(f);
   }
 }

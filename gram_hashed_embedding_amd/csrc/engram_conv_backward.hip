@@ -46,6 +46,8 @@ struct ConvBackArgs {
   bool want_w;
 };
 
+__device__ __forceinline__ int64_t ceil_div_dev(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
 __device__ __forceinline__ void unpack4(const u32x2 &r, float (&f)[4]) {
   f[0] = bf16_lo(r.x); f[1] = bf16_hi(r.x);
   f[2] = bf16_lo(r.y); f[3] = bf16_hi(r.y);
@@ -55,7 +57,8 @@ __device__ __forceinline__ void unpack4(const u32x2 &r, float (&f)[4]) {
 // first `halo_slices` slices of a row are the halo's, the others the
 // sequence's: a slice lies on one side of position 0.
 struct ConvPlace {
-  int64_t b, slice, quad, first, last;  // positions [first, last)
+  int64_t b, slice, quad0, first, last;  // positions [first, last); the wave's first quad
+  uint32_t lane;                         // this lane's quad after quad0
   bool on, halo;
 };
 __device__ __forceinline__ ConvPlace conv_place(const ConvBackArgs &a, int64_t unit) {
@@ -63,9 +66,10 @@ __device__ __forceinline__ ConvPlace conv_place(const ConvBackArgs &a, int64_t u
   const int64_t grp = unit % a.s.groups, rest = unit / a.s.groups;
   p.slice = rest % a.s.slices;
   p.b = rest / a.s.slices;
-  p.quad = grp * kWave + (threadIdx.x & 63);
-  p.on = p.quad < a.quads;
-  if (!p.on) p.quad = 0;
+  p.quad0 = grp * kWave;
+  p.lane = threadIdx.x & 63;
+  p.on = p.quad0 + p.lane < a.quads;
+  if (!p.on) p.lane = 0;  // reads what another lane reads, writes nothing
   p.halo = p.slice < a.s.halo_slices;
   p.first = p.halo ? p.slice * a.s.slice - a.halo_len
                    : (p.slice - a.s.halo_slices) * a.s.slice;
@@ -78,149 +82,72 @@ struct XRow {
   u32x2 bits;
   float scale;  // codes only
 };
+// (Row addresses are the same for a wave: scalar registers; a lane adds its
+// 32-bit offset.)
 __device__ __forceinline__ XRow load_halo(const ConvBackArgs &a, const ConvPlace &p, int64_t pos) {
-  return XRow{a.halo[(p.b * a.halo_len + a.halo_len + pos) * a.quads + p.quad], 0.0f};
+  const u32x2 *row = a.halo + (p.b * a.halo_len + a.halo_len + pos) * a.quads + p.quad0;
+  return XRow{row[p.lane], 0.0f};
 }
 template <bool CODES>
 __device__ __forceinline__ XRow load_x(const ConvBackArgs &a, const ConvPlace &p, int64_t pos,
-                                       int64_t scale_at) {
+                                       uint32_t scale_at) {
   const int64_t at = p.b * a.seq + pos;
-  if (CODES)
-    return XRow{u32x2{a.codes[at * a.quads + p.quad], 0u}, a.scales[at * a.code_blocks + scale_at]};
-  return XRow{a.x[at * a.quads + p.quad], 0.0f};
+  if (CODES) {
+    const uint32_t *row = a.codes + at * a.quads + p.quad0;
+    const float *scales = a.scales + at * a.code_blocks;
+    return XRow{u32x2{row[p.lane], 0u}, scales[scale_at]};
+  }
+  const u32x2 *row = a.x + at * a.quads + p.quad0;
+  return XRow{row[p.lane], 0.0f};
+}
+// The scale of a lane's channels among a position's.
+__device__ __forceinline__ uint32_t scale_of(const ConvBackArgs &a, const ConvPlace &p) {
+  const int64_t c = (p.quad0 + p.lane) * 4;
+  return (uint32_t)(c / a.code_width * ceil_div_dev(a.code_width, 128) + c % a.code_width / 128);
+}
+// One row of the gradient of x or of the halo.
+__device__ __forceinline__ void store_gx(const ConvBackArgs &a, const ConvPlace &p, int64_t t,
+                                         bool halo, const u32x2 &v) {
+  if (!halo) {
+    if (a.gx == nullptr) return;
+    u32x2 *row = a.gx + (p.b * a.seq + t) * a.quads + p.quad0;
+    row[p.lane] = v;
+  } else if (a.ghalo != nullptr) {
+    u32x2 *row = a.ghalo + (p.b * a.halo_len + a.halo_len + t) * a.quads + p.quad0;
+    row[p.lane] = v;
+  }
 }
 template <bool CODES>
 __device__ __forceinline__ void unpack_x(const XRow &r, bool halo, float (&f)[4]) {
   if (CODES && !halo) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) f[e] = code_value(r.bits.x, e, r.scale);
+    code_values(r.bits.x, r.scale, f);
   } else {
     unpack4(r.bits, f);
   }
 }
 
-// Bits of the positions pos0 .. pos0 + 63 where a segment begins (from
-// pos0 + 1 on; bit 0 is not used) or the row has ended.
-__device__ __forceinline__ uint64_t begins_mask(const ConvBackArgs &a, int64_t b, int64_t pos0) {
-  const int64_t pos = pos0 + (threadIdx.x & 63);
-  bool begin = pos >= a.seq;
-  if (a.seg != nullptr && !begin && pos > -a.halo_len) {
-    const int64_t *s = a.seg + b * (a.halo_len + a.seq) + a.halo_len + pos;
-    begin = s[0] != s[-1];
+// The segment ids of the positions at + lane and before it (loaded ahead of
+// their use), and from them the bits of the positions at .. at + 63 where a
+// segment begins (bit 0 is not used) or the row has ended.
+struct SegPair {
+  int64_t here, before;
+};
+__device__ __forceinline__ SegPair load_seg(const ConvBackArgs &a, int64_t b, int64_t at) {
+  // no branch (a load behind one is waited for at once): without ids, any words
+  const int64_t low = -a.halo_len;
+  const int64_t *p = reinterpret_cast<const int64_t *>(a.g);
+  int64_t here = 0, before = 0;
+  if (a.seg != nullptr) {
+    p = a.seg + b * (a.halo_len + a.seq) + a.halo_len;
+    here = min(max(at + (int64_t)(threadIdx.x & 63), low), a.seq - 1);
+    before = max(here - 1, low);
   }
-  return __ballot(begin);
+  return SegPair{p[here], p[before]};
 }
-
-// A tile's positions, from the last: CLEAR: every pair counts; else the
-// slice's own positions' pairs that no boundary cuts.
-template <int D, int T, bool CODES, bool WANT_W, bool CLEAR>
-__device__ __forceinline__ void conv_tile(const ConvBackArgs &a, const ConvPlace &p, int64_t t0,
-                                          uint64_t begins, const u32x2 (&win)[T + 3 * D],
-                                          const XRow (&xr)[T], const float (&w)[4][4],
-                                          float (&sum_w)[4][4], float (&sum_b)[4]) {
-  constexpr int K = 4;
-#pragma unroll
-  for (int i = T - 1; i >= 0; --i) {
-    const int64_t t = t0 + i;
-    float dx[4] = {0.0f, 0.0f, 0.0f, 0.0f}, x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (WANT_W) unpack_x<CODES>(xr[i], !CLEAR && p.halo, x);
-#pragma unroll
-    for (int j = 0; j < K; ++j) {
-      const uint64_t between = (((uint64_t)1 << (j * D)) - 1) << (i + 1);
-      if (CLEAR || (t >= p.first && t + j * D >= 0 && (begins & between) == 0)) {
-        float v[4];
-        unpack4(win[i + j * D], v);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          dx[c] += w[c][j] * v[c];
-          if (WANT_W) sum_w[c][j] += v[c] * x[c];
-          if (WANT_W && j == 0) sum_b[c] += v[c];
-        }
-      }
-    }
-    if ((CLEAR || t >= p.first) && p.on) {
-      const u32x2 o = {pack_bf16(dx[0], dx[1]), pack_bf16(dx[2], dx[3])};
-      if (CLEAR || !p.halo) {
-        if (a.gx != nullptr) a.gx[(p.b * a.seq + t) * a.quads + p.quad] = o;
-      } else if (a.ghalo != nullptr) {
-        a.ghalo[(p.b * a.halo_len + a.halo_len + t) * a.quads + p.quad] = o;
-      }
-    }
-  }
-}
-
-template <int D, bool CODES, bool WANT_W>
-__global__ __launch_bounds__(kConvBlock) void conv_backward_k4_kernel(const ConvBackArgs a) {
-  constexpr int K = 4, H = (K - 1) * D;
-  constexpr int T = 8;  // positions of a tile
-  static_assert(T + H < 64, "a tile and the rows ahead of it fit one mask");
-  const int64_t unit = (int64_t)blockIdx.x * kConvWaves + __builtin_amdgcn_readfirstlane(
-                                                              threadIdx.x / kWave);
-  if (unit >= a.units) return;
-  const ConvPlace p = conv_place(a, unit);
-  const int64_t scale_at = p.quad * 4 / a.code_width * ((a.code_width + 127) / 128) +
-                           p.quad * 4 % a.code_width / 128;
-  float w[4][K];  // [channel][tap j back]
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-#pragma unroll
-    for (int j = 0; j < K; ++j) w[c][j] = bf16_lo(a.w[(p.quad * 4 + c) * K + (K - 1 - j)]);
-  float sum_w[4][K], sum_b[4];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    sum_b[c] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < K; ++j) sum_w[c][j] = 0.0f;
-  }
-  const u32x2 *g = a.g + p.b * a.seq * a.quads + p.quad;
-  // row i of the window is position t0 + i: the tile, then the rows ahead
-  u32x2 win[T + H];
-  int64_t t0 = p.last - T;
-#pragma unroll
-  for (int i = 0; i < H; ++i) {
-    const int64_t t = p.last + i;
-    win[T + i] = t >= 0 && t < a.seq ? g[t * a.quads] : u32x2{0u, 0u};
-  }
-  for (;;) {
-    // every load of the tile at once; rows below the slice repeat its first,
-    // and their values are not used
-    XRow xr[T];
-#pragma unroll
-    for (int i = 0; i < T; ++i) {
-      win[i] = u32x2{0u, 0u};
-      xr[i] = XRow{u32x2{0u, 0u}, 0.0f};
-      const int64_t t = max(t0 + i, p.first);
-      if (!p.halo) {
-        win[i] = g[t * a.quads];
-        if (WANT_W) xr[i] = load_x<CODES>(a, p, t, scale_at);
-      } else if (WANT_W) {
-        xr[i] = load_halo(a, p, t);
-      }
-    }
-    const uint64_t begins = begins_mask(a, p.b, t0);
-    // every pair of the tile counts: the whole tile is the slice's own, inside
-    // the row, and no segment begins in it or in the rows ahead
-    const bool clear = t0 >= p.first && !p.halo &&
-                       (begins & ((((uint64_t)1 << (T + H - 1)) - 1) << 1)) == 0;
-    if (clear)
-      conv_tile<D, T, CODES, WANT_W, true>(a, p, t0, begins, win, xr, w, sum_w, sum_b);
-    else
-      conv_tile<D, T, CODES, WANT_W, false>(a, p, t0, begins, win, xr, w, sum_w, sum_b);
-    if (t0 <= p.first) break;
-    t0 -= T;
-    // the rows ahead of the next tile are this window's first H
-#pragma unroll
-    for (int i = H - 1; i >= 0; --i) win[T + i] = win[i];
-  }
-  if constexpr (WANT_W) {
-    if (!p.on) return;
-    f32x4 *dst = reinterpret_cast<f32x4 *>(a.partials) +
-                 (p.b * a.s.slices + p.slice) * (K + 1) * a.quads + p.quad;
-#pragma unroll
-    for (int j = 0; j < K; ++j)
-      dst[(K - 1 - j) * a.quads] = f32x4{sum_w[0][j], sum_w[1][j], sum_w[2][j], sum_w[3][j]};
-    dst[K * a.quads] = f32x4{sum_b[0], sum_b[1], sum_b[2], sum_b[3]};
-  }
+__device__ __forceinline__ uint64_t begins_mask(const ConvBackArgs &a, const SegPair &s,
+                                                int64_t at) {
+  const int64_t pos = at + (threadIdx.x & 63);
+  return __ballot(pos >= a.seq || (a.seg != nullptr && pos > -a.halo_len && s.here != s.before));
 }
 
 // Any K up to kConvMaxKernel and any dilation: the same walk, each row of g
@@ -230,11 +157,11 @@ __global__ __launch_bounds__(kConvBlock) void conv_backward_generic_kernel(const
   const int64_t unit = (int64_t)blockIdx.x * kConvWaves + threadIdx.x / kWave;
   if (unit >= a.units) return;
   const ConvPlace p = conv_place(a, unit);
-  const int64_t scale_at = p.quad * 4 / a.code_width * ((a.code_width + 127) / 128) +
-                           p.quad * 4 % a.code_width / 128;
+  const uint32_t scale_at = CODES ? scale_of(a, p) : 0u;
   const int64_t *seg =
       a.seg != nullptr ? a.seg + p.b * (a.halo_len + a.seq) + a.halo_len : nullptr;
-  const u32x2 *g = a.g + p.b * a.seq * a.quads + p.quad;
+  const int64_t quad = p.quad0 + p.lane;
+  const u32x2 *g = a.g + p.b * a.seq * a.quads + quad;
   // one tap at a time for the weight's sums, so that K stays a run-time number
   float sum_b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int64_t t = p.last - 1; t >= p.first; --t) {
@@ -250,21 +177,16 @@ __global__ __launch_bounds__(kConvBlock) void conv_backward_generic_kernel(const
       float v[4];
       unpack4(g[q * a.quads], v);
       for (int c = 0; c < 4; ++c) {
-        dx[c] += bf16_lo(a.w[(p.quad * 4 + c) * a.K + (a.K - 1 - j)]) * v[c];
+        dx[c] += bf16_lo(a.w[(quad * 4 + c) * a.K + (a.K - 1 - j)]) * v[c];
         if (j == 0) sum_b[c] += v[c];
       }
     }
     if (!p.on) continue;
-    const u32x2 o = {pack_bf16(dx[0], dx[1]), pack_bf16(dx[2], dx[3])};
-    if (t >= 0) {
-      if (a.gx != nullptr) a.gx[(p.b * a.seq + t) * a.quads + p.quad] = o;
-    } else if (a.ghalo != nullptr) {
-      a.ghalo[(p.b * a.halo_len + a.halo_len + t) * a.quads + p.quad] = o;
-    }
+    store_gx(a, p, t, p.halo, u32x2{pack_bf16(dx[0], dx[1]), pack_bf16(dx[2], dx[3])});
   }
   if (a.partials == nullptr) return;
   f32x4 *dst = reinterpret_cast<f32x4 *>(a.partials) +
-               (p.b * a.s.slices + p.slice) * (a.K + 1) * a.quads + p.quad;
+               (p.b * a.s.slices + p.slice) * (a.K + 1) * a.quads + quad;
   for (int j = 0; j < a.K && a.want_w; ++j) {
     const int64_t back = (int64_t)j * a.dil;
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -282,6 +204,154 @@ __global__ __launch_bounds__(kConvBlock) void conv_backward_generic_kernel(const
     if (p.on) dst[(a.K - 1 - j) * a.quads] = f32x4{s[0], s[1], s[2], s[3]};
   }
   if (p.on) dst[a.K * a.quads] = f32x4{sum_b[0], sum_b[1], sum_b[2], sum_b[3]};
+}
+
+// A tile's positions, from the last.  kClear: every pair counts; kTested: the
+// slice's own positions' pairs that no boundary cuts; kHalo: the same of the
+// halo's positions, which have x in bf16 and pairs with the sequence only.
+enum Tile { kClear, kTested, kHalo };
+template <int D, int T, bool CODES, bool WANT_W, Tile KIND>
+__device__ __forceinline__ void conv_tile(const ConvBackArgs &a, const ConvPlace &p, int64_t t0,
+                                          uint64_t begins, const u32x2 (&win)[T + 3 * D],
+                                          const XRow (&xr)[T], const float (&w)[4][4],
+                                          float (&sum_w)[4][4], float (&sum_b)[4]) {
+  constexpr int K = 4;
+  u32x2 o[T];
+#pragma unroll
+  for (int i = T - 1; i >= 0; --i) {
+    const int64_t t = t0 + i;
+    float dx[4] = {0.0f, 0.0f, 0.0f, 0.0f}, x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (WANT_W) unpack_x<CODES>(xr[i], KIND == kHalo, x);
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      const uint64_t between = (((uint64_t)1 << (j * D)) - 1) << (i + 1);
+      if (KIND == kClear || (t >= p.first && (begins & between) == 0 &&
+                             (KIND != kHalo || t + j * D >= 0))) {
+        float v[4];
+        unpack4(win[i + j * D], v);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          dx[c] += w[c][j] * v[c];
+          if (WANT_W) sum_w[c][j] += v[c] * x[c];
+          if (WANT_W && KIND != kHalo && j == 0) sum_b[c] += v[c];
+        }
+      }
+    }
+    o[i] = u32x2{pack_bf16(dx[0], dx[1]), pack_bf16(dx[2], dx[3])};
+  }
+  // (a lane past the last channel repeats another's values at its place)
+  u32x2 *dst = KIND == kHalo ? a.ghalo : a.gx;
+  if (dst == nullptr) return;
+  dst += (KIND == kHalo ? (p.b + 1) * a.halo_len + t0 : p.b * a.seq + t0) * a.quads + p.quad0;
+#pragma unroll
+  for (int i = 0; i < T; ++i)
+    if (KIND == kClear || t0 + i >= p.first)
+      __builtin_nontemporal_store(o[i], dst + i * a.quads + p.lane);
+}
+
+// A slice's sums: a row of partials for each tap and the bias.
+template <int K>
+__device__ __forceinline__ void store_sums(const ConvBackArgs &a, const ConvPlace &p,
+                                           const float (&sum_w)[4][K], const float (&sum_b)[4]) {
+  if (!p.on) return;
+  f32x4 *dst = reinterpret_cast<f32x4 *>(a.partials) +
+               (p.b * a.s.slices + p.slice) * (K + 1) * a.quads + p.quad0 + p.lane;
+#pragma unroll
+  for (int j = 0; j < K; ++j)
+    dst[(K - 1 - j) * a.quads] = f32x4{sum_w[0][j], sum_w[1][j], sum_w[2][j], sum_w[3][j]};
+  dst[K * a.quads] = f32x4{sum_b[0], sum_b[1], sum_b[2], sum_b[3]};
+}
+
+template <int D, bool CODES, bool WANT_W>
+__global__ __launch_bounds__(kConvBlock) void conv_backward_k4_kernel(const ConvBackArgs a) {
+  constexpr int K = 4, H = (K - 1) * D;
+  constexpr int T = 8;  // positions of a tile
+  static_assert(T + H < 64, "a tile and the rows ahead of it fit one mask");
+  const int64_t unit = (int64_t)blockIdx.x * kConvWaves + __builtin_amdgcn_readfirstlane(
+                                                              threadIdx.x / kWave);
+  if (unit >= a.units) return;
+  const ConvPlace p = conv_place(a, unit);
+  const uint32_t scale_at = CODES ? scale_of(a, p) : 0u;
+  float w[4][K];  // [channel][tap j back]
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int j = 0; j < K; ++j) w[c][j] = bf16_lo(a.w[((p.quad0 + p.lane) * 4 + c) * K + (K - 1 - j)]);
+  float sum_w[4][K], sum_b[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    sum_b[c] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < K; ++j) sum_w[c][j] = 0.0f;
+  }
+  const u32x2 *g = a.g + p.b * a.seq * a.quads + p.quad0;
+  // row i of the window is position t0 + i: the tile, then the rows ahead
+  u32x2 win[T + H];
+  int64_t t0 = p.last - T;
+  if (p.halo) {  // a few positions: each tile loads its whole window
+    for (;; t0 -= T) {
+      XRow xr[T];
+#pragma unroll
+      for (int i = 0; i < T + H; ++i)
+        win[i] = (g + min(max(t0 + i, (int64_t)0), a.seq - 1) * a.quads)[p.lane];
+#pragma unroll
+      for (int i = 0; i < T; ++i) {
+        xr[i] = XRow{u32x2{0u, 0u}, 0.0f};
+        if (WANT_W) xr[i] = load_halo(a, p, max(t0 + i, p.first));
+      }
+      const uint64_t begins = begins_mask(a, load_seg(a, p.b, t0), t0);
+      conv_tile<D, T, CODES, WANT_W, kHalo>(a, p, t0, begins, win, xr, w, sum_w, sum_b);
+      if (t0 <= p.first) break;
+    }
+    if constexpr (WANT_W) store_sums<K>(a, p, sum_w, sum_b);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < H; ++i) {
+    // (past the row's end: its last row, not used)
+    win[T + i] = (g + min(p.last + i, a.seq - 1) * a.quads)[p.lane];
+  }
+  // A tile's rows, all loads at once; rows below the slice repeat its first, and
+  // their values are not used.  The next tile's are loaded while one is worked on
+  // (after the last, the first rows once more).
+  u32x2 next_g[T];
+  XRow next_x[T];
+  auto load_tile = [&](int64_t at) {
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+      const int64_t t = max(at + i, p.first);
+      next_g[i] = (g + t * a.quads)[p.lane];
+      next_x[i] = XRow{u32x2{0u, 0u}, 0.0f};
+      if (WANT_W) next_x[i] = load_x<CODES>(a, p, t, scale_at);
+    }
+  };
+  load_tile(t0);
+  SegPair next_seg = load_seg(a, p.b, t0);
+  for (;;) {
+    XRow xr[T];
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+      win[i] = next_g[i];
+      xr[i] = next_x[i];
+    }
+    const uint64_t begins = begins_mask(a, next_seg, t0);
+    load_tile(t0 - T);
+    next_seg = load_seg(a, p.b, t0 - T);
+    // every pair of the tile counts: the whole tile is the slice's own, inside
+    // the row, and no segment begins in it or in the rows ahead
+    const bool clear = t0 >= p.first &&
+                       (begins & ((((uint64_t)1 << (T + H - 1)) - 1) << 1)) == 0;
+    if (clear)
+      conv_tile<D, T, CODES, WANT_W, kClear>(a, p, t0, begins, win, xr, w, sum_w, sum_b);
+    else
+      conv_tile<D, T, CODES, WANT_W, kTested>(a, p, t0, begins, win, xr, w, sum_w, sum_b);
+    if (t0 <= p.first) break;
+    t0 -= T;
+    // the rows ahead of the next tile are this window's first H
+#pragma unroll
+    for (int i = H - 1; i >= 0; --i) win[T + i] = win[i];
+  }
+  if constexpr (WANT_W) store_sums<K>(a, p, sum_w, sum_b);
 }
 
 // The weight's and the bias's gradients: sums of the slices' rows, 64 of the

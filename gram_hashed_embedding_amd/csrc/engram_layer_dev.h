@@ -107,8 +107,14 @@ __device__ __forceinline__ uint32_t max_magnitude(const float (&x)[8]) {
   return m;
 }
 
-__device__ __forceinline__ float code_value(uint32_t word, int e, float scale) {
-  return (float)(int8_t)(word >> (8 * e)) * scale;
+// Four codes' values.  A byte with its top bit flipped is the code plus 128, which
+// one instruction turns into a float; the multiply-add then gives the code times
+// the scale, rounded once (128 * scale is exact).
+__device__ __forceinline__ void code_values(uint32_t word, float scale, float *f) {
+  const uint32_t biased = word ^ 0x80808080u;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    f[e] = __builtin_fmaf((float)((biased >> (8 * e)) & 0xffu), scale, -128.0f * scale);
 }
 
 }  // namespace engram

@@ -54,9 +54,9 @@ ConvBackwardShape conv_backward_shape(int64_t batch, int64_t seq, int64_t halo_l
   ConvBackwardShape s = {};
   s.quads = channels / 4;
   s.groups = ceil_div(s.quads, 64);
-  // about 4096 waves (16 for each of 256 CUs); a slice not so short that the
-  // rows it reads past its end outweigh its own
-  const int64_t want = ceil_div(4096, (batch > 0 ? batch : 1) * s.groups);
+  // about 2048 waves, as many as stay on 256 CUs at a time (8 each); a slice not
+  // so short that the rows it reads past its end outweigh its own
+  const int64_t want = ceil_div(2048, (batch > 0 ? batch : 1) * s.groups);
   const int64_t least = 32 > 2 * (int64_t)(K - 1) * dilation ? 32 : 2 * (int64_t)(K - 1) * dilation;
   s.slice = ceil_div(seq > 0 ? seq : 1, want);
   if (s.slice < least) s.slice = least;

@@ -472,11 +472,8 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(const NormArgs a
         if (a.y != nullptr) {
           unpack_bf16x8(y[i], yh[i]);
         } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            yh[i][e] = code_value(yc[i].words.x, e, yc[i].scale_a);
-            yh[i][4 + e] = code_value(yc[i].words.y, e, yc[i].scale_b);
-          }
+          code_values(yc[i].words.x, yc[i].scale_a, yh[i]);
+          code_values(yc[i].words.y, yc[i].scale_b, yh[i] + 4);
         }
         unpack_bf16x8(wp[i], w);
         unpack_bf16x8(sc[i], k);
