@@ -46,8 +46,6 @@ struct ConvBackArgs {
   bool want_w;
 };
 
-__device__ __forceinline__ int64_t ceil_div_dev(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 __device__ __forceinline__ void unpack4(const u32x2 &r, float (&f)[4]) {
   f[0] = bf16_lo(r.x); f[1] = bf16_hi(r.x);
   f[2] = bf16_lo(r.y); f[3] = bf16_hi(r.y);
@@ -61,11 +59,13 @@ struct ConvPlace {
   uint32_t lane;                         // this lane's quad after quad0
   bool on, halo;
 };
-__device__ __forceinline__ ConvPlace conv_place(const ConvBackArgs &a, int64_t unit) {
-  ConvPlace p;
-  const int64_t grp = unit % a.s.groups, rest = unit / a.s.groups;
-  p.slice = rest % a.s.slices;
-  p.b = rest / a.s.slices;
+__device__ __forceinline__ ConvPlace conv_place(const ConvBackArgs &a, uint32_t unit) {
+  ConvPlace p;  // (units fit 32 bits: the grid has four to a block of 256 threads)
+  const uint32_t groups = (uint32_t)a.s.groups, slices = (uint32_t)a.s.slices;
+  const uint32_t rest = unit / groups, grp = unit - rest * groups;
+  const uint32_t row = rest / slices;
+  p.slice = rest - row * slices;
+  p.b = row;
   p.quad0 = grp * kWave;
   p.lane = threadIdx.x & 63;
   p.on = p.quad0 + p.lane < a.quads;
@@ -102,8 +102,9 @@ __device__ __forceinline__ XRow load_x(const ConvBackArgs &a, const ConvPlace &p
 }
 // The scale of a lane's channels among a position's.
 __device__ __forceinline__ uint32_t scale_of(const ConvBackArgs &a, const ConvPlace &p) {
-  const int64_t c = (p.quad0 + p.lane) * 4;
-  return (uint32_t)(c / a.code_width * ceil_div_dev(a.code_width, 128) + c % a.code_width / 128);
+  const uint32_t c = (uint32_t)(p.quad0 + p.lane) * 4, width = (uint32_t)a.code_width;
+  const uint32_t g = c / width;  // (channels are below 2^31)
+  return g * ((width + 127) / 128) + (c - g * width) / 128;
 }
 // One row of the gradient of x or of the halo.
 __device__ __forceinline__ void store_gx(const ConvBackArgs &a, const ConvPlace &p, int64_t t,
@@ -154,7 +155,7 @@ __device__ __forceinline__ uint64_t begins_mask(const ConvBackArgs &a, const Seg
 // read from memory and each pair tested against the segment ids.
 template <bool CODES>
 __global__ __launch_bounds__(kConvBlock) void conv_backward_generic_kernel(const ConvBackArgs a) {
-  const int64_t unit = (int64_t)blockIdx.x * kConvWaves + threadIdx.x / kWave;
+  const uint32_t unit = blockIdx.x * kConvWaves + threadIdx.x / kWave;
   if (unit >= a.units) return;
   const ConvPlace p = conv_place(a, unit);
   const uint32_t scale_at = CODES ? scale_of(a, p) : 0u;
@@ -267,16 +268,25 @@ __global__ __launch_bounds__(kConvBlock) void conv_backward_k4_kernel(const Conv
   constexpr int K = 4, H = (K - 1) * D;
   constexpr int T = 8;  // positions of a tile
   static_assert(T + H < 64, "a tile and the rows ahead of it fit one mask");
-  const int64_t unit = (int64_t)blockIdx.x * kConvWaves + __builtin_amdgcn_readfirstlane(
-                                                              threadIdx.x / kWave);
+  const uint32_t unit =
+      blockIdx.x * kConvWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   if (unit >= a.units) return;
   const ConvPlace p = conv_place(a, unit);
   const uint32_t scale_at = CODES ? scale_of(a, p) : 0u;
   float w[4][K];  // [channel][tap j back]
+  {
+    const u32x4 *wp = reinterpret_cast<const u32x4 *>(a.w) + (p.quad0 + p.lane) * 2;
+    float f[8], h[8];
+    unpack_bf16x8(wp[0], f);
+    unpack_bf16x8(wp[1], h);
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
-#pragma unroll
-    for (int j = 0; j < K; ++j) w[c][j] = bf16_lo(a.w[((p.quad0 + p.lane) * 4 + c) * K + (K - 1 - j)]);
+    for (int j = 0; j < K; ++j) {
+      w[0][j] = f[K - 1 - j];
+      w[1][j] = f[2 * K - 1 - j];
+      w[2][j] = h[K - 1 - j];
+      w[3][j] = h[2 * K - 1 - j];
+    }
+  }
   float sum_w[4][K], sum_b[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -354,29 +364,19 @@ __global__ __launch_bounds__(kConvBlock) void conv_backward_k4_kernel(const Conv
   if constexpr (WANT_W) store_sums<K>(a, p, sum_w, sum_b);
 }
 
-// The weight's and the bias's gradients: sums of the slices' rows, 64 of the
-// (K + 1) * channels columns a block, each of its 16 wavefronts every 16th
-// slice, in fp64.
-constexpr int kConvJoin = 1024;
-__global__ __launch_bounds__(kConvJoin) void conv_join_kernel(const float *partials, int64_t rows,
-                                                              int K, int64_t channels,
-                                                              float *grad_weight,
-                                                              float *grad_bias) {
-  __shared__ double part[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t col = (int64_t)blockIdx.x * 64 + lane, cols = (K + 1) * channels;
+// The weight's and the bias's gradients from the slices' sums.
+__global__ __launch_bounds__(kJoinThreads) void conv_join_kernel(const float *partials,
+                                                                 int64_t rows, int K,
+                                                                 int64_t channels,
+                                                                 float *grad_weight,
+                                                                 float *grad_bias) {
+  __shared__ double part[kJoinSlots][kJoinColumns];
+  const int64_t col = (int64_t)blockIdx.x * kJoinColumns + threadIdx.x % kJoinColumns;
+  const int64_t cols = (K + 1) * channels;
   const bool bias = col >= K * channels;
   const bool on = col < cols && (bias ? grad_bias : grad_weight) != nullptr;
-  double s = 0.0;
-  if (on)
-#pragma unroll 4
-    for (int64_t r = wave; r < rows; r += 16) s += partials[r * cols + col];
-  part[wave][lane] = s;
-  __syncthreads();
-  if (wave != 0 || !on) return;
-  s = 0.0;
-#pragma unroll
-  for (int v = 0; v < 16; ++v) s += part[v][lane];
+  const double s = join_column(partials + col, rows, cols, on, part);
+  if (threadIdx.x >= kJoinColumns || !on) return;
   const int64_t k = col / channels, c = col % channels;
   if (bias)
     grad_bias[c] = (float)s;
@@ -422,7 +422,7 @@ int engram::launch_conv_backward(const ConvBackwardCall &c, void *stream) {
   const int64_t blocks = ceil_div(units, kConvWaves);
   const int64_t cols = (c.K + 1) * c.channels;
   const int64_t halo_words = c.batch * c.halo_len * c.channels / 8;
-  if (!grid_fits(blocks, kConvBlock) || !grid_fits(ceil_div(cols, 64), kConvJoin) ||
+  if (!grid_fits(blocks, kConvBlock) || !grid_fits(ceil_div(cols, kJoinColumns), kJoinThreads) ||
       !grid_fits(ceil_div(halo_words, 256), 256))
     return ENGRAM_EINVAL;
   if (empty && c.grad_halo != nullptr && halo_words > 0)
@@ -469,7 +469,8 @@ int engram::launch_conv_backward(const ConvBackwardCall &c, void *stream) {
     }
   }
   if (sums)
-    hipLaunchKernelGGL(conv_join_kernel, dim3((unsigned)ceil_div(cols, 64)), dim3(kConvJoin), 0,
+    hipLaunchKernelGGL(conv_join_kernel, dim3((unsigned)ceil_div(cols, kJoinColumns)),
+                       dim3(kJoinThreads), 0,
                        st, c.partials, empty ? 0 : c.batch * s.slices, c.K, c.channels,
                        c.grad_weight, c.grad_bias);
   return launch_status();

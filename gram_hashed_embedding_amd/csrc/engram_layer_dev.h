@@ -108,13 +108,37 @@ __device__ __forceinline__ uint32_t max_magnitude(const float (&x)[8]) {
 }
 
 // Four codes' values.  A byte with its top bit flipped is the code plus 128, which
-// one instruction turns into a float; the multiply-add then gives the code times
-// the scale, rounded once (128 * scale is exact).
+// one instruction turns into a float.  (128 is taken off before the product: 128
+// scales of the largest blocks are past fp32.)
 __device__ __forceinline__ void code_values(uint32_t word, float scale, float *f) {
   const uint32_t biased = word ^ 0x80808080u;
 #pragma unroll
   for (int e = 0; e < 4; ++e)
-    f[e] = __builtin_fmaf((float)((biased >> (8 * e)) & 0xffu), scale, -128.0f * scale);
+    f[e] = ((float)((biased >> (8 * e)) & 0xffu) - 128.0f) * scale;
+}
+
+// ------------------------------------------------- sums of rows of partials --
+// The sum over rows of the fp32 column that `column` starts, in fp64 and in a
+// fixed order: a block of kJoinThreads takes kJoinColumns adjacent columns,
+// each of its kJoinSlots threads of a column every kJoinSlots-th row.  The sum
+// is left in the threads of slot 0.
+constexpr int kJoinThreads = 1024, kJoinColumns = 16, kJoinSlots = kJoinThreads / kJoinColumns;
+__device__ __forceinline__ double join_column(const float *column, int64_t rows, int64_t stride,
+                                              bool on, double (*part)[kJoinColumns]) {
+  const int slot = threadIdx.x / kJoinColumns, c = threadIdx.x % kJoinColumns;
+  double s = 0.0;
+  if (on) {
+#pragma unroll 8
+    for (int64_t r = slot; r < rows; r += kJoinSlots) s += column[r * stride];
+  }
+  part[slot][c] = s;
+  __syncthreads();
+  s = 0.0;
+  if (slot == 0)
+#pragma unroll
+    for (int q = 0; q < kJoinSlots; ++q) s += part[q][c];
+  __syncthreads();
+  return s;
 }
 
 }  // namespace engram

@@ -562,31 +562,15 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(const NormArgs a
   }
 }
 
-// The weights' gradients from the row blocks' sums: a block takes 64
-// channels, each of its 16 wavefronts every 16th row block, in fp64.
-constexpr int kJoinThreads = 1024;
+// The weights' gradients from the row blocks' sums.
 __global__ __launch_bounds__(kJoinThreads) void norm_join_kernel(const NormArgs a) {
-  __shared__ double part[2][16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
-  double d = 0.0, n = 0.0;
-  if (c < a.s.channels && a.s.rows > 0) {
-#pragma unroll 4
-    for (int64_t rb = wave; rb < a.s.rowblocks; rb += 16) {
-      d += a.partials[(rb * 2) * a.s.channels + c];
-      n += a.partials[(rb * 2 + 1) * a.s.channels + c];
-    }
-  }
-  part[0][wave][lane] = d;
-  part[1][wave][lane] = n;
-  __syncthreads();
-  if (wave != 0 || c >= a.s.channels) return;
-  d = n = 0.0;
-#pragma unroll
-  for (int w = 0; w < 16; ++w) {
-    d += part[0][w][lane];
-    n += part[1][w][lane];
-  }
+  __shared__ double part[kJoinSlots][kJoinColumns];
+  const int64_t c = (int64_t)blockIdx.x * kJoinColumns + threadIdx.x % kJoinColumns;
+  const bool on = c < a.s.channels && a.s.rows > 0;
+  const int64_t stride = 2 * a.s.channels;
+  const double d = join_column(a.partials + c, a.s.rowblocks, stride, on, part);
+  const double n = join_column(a.partials + a.s.channels + c, a.s.rowblocks, stride, on, part);
+  if (threadIdx.x >= kJoinColumns || c >= a.s.channels) return;
   const uint16_t *wp = static_cast<const uint16_t *>(a.w_post);
   const uint16_t *sc = static_cast<const uint16_t *>(a.scale);
   if (a.grad_w_post != nullptr) a.grad_w_post[c] = (float)(d * (sc ? bf16_lo(sc[c]) : 1.0f));
@@ -665,7 +649,7 @@ int engram::launch_residual_norm_backward(const engram_norm_args &c) {
   const NormShape s = norm_backward_shape(c.rows, c.channels, c.groups);
   const NormArgs a = norm_args(c, s);
   if (!grid_fits(s.colblocks * s.rowblocks, s.threads) ||
-      !grid_fits(ceil_div(c.channels, 64), kJoinThreads))
+      !grid_fits(ceil_div(c.channels, kJoinColumns), kJoinThreads))
     return ENGRAM_EINVAL;
   hipStream_t st = as_stream(c.stream);
   if (c.rows > 0) {
@@ -684,7 +668,7 @@ int engram::launch_residual_norm_backward(const engram_norm_args &c) {
     }
   }
   if (a.grad_w_post != nullptr || a.grad_scale != nullptr || a.grad_w_next != nullptr)
-    hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)ceil_div(c.channels, 64)),
+    hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)ceil_div(c.channels, kJoinColumns)),
                        dim3(kJoinThreads), 0, st, a);
   return launch_status();
 }

@@ -172,7 +172,7 @@ def engram_residual_norm(residual, y=None, *, gate=None, w_post=None, scale=None
     if y is not None:
         y_p = _tensor(y, bf, n, "y", index)
         if out is None:
-            out = torch.empty(residual.shape, dtype=rt, device=device)
+            out = torch.empty_like(residual)
         out_p = _tensor(out, rt, n, "out", index)
         if rstd_post is None:
             rstd_post = torch.empty((rows, groups), dtype=torch.float32, device=device)
@@ -237,14 +237,15 @@ def engram_residual_norm_backward(grad_out, grad_next=None, *, out=None, rstd_po
         ys_p = _optional(y_scales, f32, stats * code_blocks(channels // groups), "y_scales",
                          index)
     if grad_residual is None:
-        grad_residual = torch.empty(like.shape, dtype=rt, device=device)
+        grad_residual = torch.empty_like(like)
     gy = gz = gp = gs = gn = None
     gy_p = gz_p = gp_p = gs_p = gn_p = ws_p = size = 0
     if branch:
-        gy = torch.empty(like.shape, dtype=bf, device=device)
+        gy = torch.empty_like(y) if y is not None else torch.empty(like.shape, dtype=bf,
+                                                                   device=device)
         gy_p = gy.data_ptr()
         if gate is not None:
-            gz = torch.empty(gate.shape, dtype=bf, device=device)
+            gz = torch.empty_like(gate)
             gz_p = gz.data_ptr()
         if w_post is not None:
             gp = torch.empty((channels,), dtype=f32, device=device)
@@ -368,7 +369,7 @@ def engram_ple_conv_backward(grad_out, weight, dilation, x=None, x_codes=None, x
                 raise ValueError("code_width must divide channels")
             sp = _tensor(x_scales, torch.float32,
                          batch * seq * (channels // width) * code_blocks(width), "x_scales", index)
-    gx = torch.empty(grad_out.shape, dtype=torch.bfloat16, device=device) if need_x else None
+    gx = torch.empty_like(grad_out) if need_x else None
     gh = torch.empty_like(halo) if need_x and halo_len else None
     gw = gb = None
     if need_weight:
