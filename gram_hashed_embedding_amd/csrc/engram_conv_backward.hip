@@ -365,18 +365,18 @@ __global__ __launch_bounds__(kConvBlock) void conv_backward_k4_kernel(const Conv
 }
 
 // The weight's and the bias's gradients from the slices' sums.
+template <int COLUMNS>
 __global__ __launch_bounds__(kJoinThreads) void conv_join_kernel(const float *partials,
                                                                  int64_t rows, int K,
                                                                  int64_t channels,
                                                                  float *grad_weight,
                                                                  float *grad_bias) {
-  __shared__ double part[kJoinSlots][kJoinColumns];
-  const int64_t col = (int64_t)blockIdx.x * kJoinColumns + threadIdx.x % kJoinColumns;
+  const int64_t col = (int64_t)blockIdx.x * COLUMNS + threadIdx.x % COLUMNS;
   const int64_t cols = (K + 1) * channels;
   const bool bias = col >= K * channels;
   const bool on = col < cols && (bias ? grad_bias : grad_weight) != nullptr;
-  const double s = join_column(partials + col, rows, cols, on, part);
-  if (threadIdx.x >= kJoinColumns || !on) return;
+  const double s = join_column<COLUMNS>(partials + col, rows, cols, on);
+  if (threadIdx.x >= COLUMNS || !on) return;
   const int64_t k = col / channels, c = col % channels;
   if (bias)
     grad_bias[c] = (float)s;
@@ -422,7 +422,7 @@ int engram::launch_conv_backward(const ConvBackwardCall &c, void *stream) {
   const int64_t blocks = ceil_div(units, kConvWaves);
   const int64_t cols = (c.K + 1) * c.channels;
   const int64_t halo_words = c.batch * c.halo_len * c.channels / 8;
-  if (!grid_fits(blocks, kConvBlock) || !grid_fits(ceil_div(cols, kJoinColumns), kJoinThreads) ||
+  if (!grid_fits(blocks, kConvBlock) || !grid_fits(ceil_div(cols, 16), kJoinThreads) ||
       !grid_fits(ceil_div(halo_words, 256), 256))
     return ENGRAM_EINVAL;
   if (empty && c.grad_halo != nullptr && halo_words > 0)
@@ -468,10 +468,16 @@ int engram::launch_conv_backward(const ConvBackwardCall &c, void *stream) {
       hipLaunchKernelGGL(conv_backward_generic_kernel<false>, grid, dim3(kConvBlock), 0, st, a);
     }
   }
-  if (sums)
-    hipLaunchKernelGGL(conv_join_kernel, dim3((unsigned)ceil_div(cols, kJoinColumns)),
-                       dim3(kJoinThreads), 0,
-                       st, c.partials, empty ? 0 : c.batch * s.slices, c.K, c.channels,
-                       c.grad_weight, c.grad_bias);
+  if (sums) {
+    const int64_t rows = empty ? 0 : c.batch * s.slices;
+    const int columns = join_columns(rows);
+    const dim3 grid((unsigned)ceil_div(cols, columns));
+    if (columns == 64)
+      hipLaunchKernelGGL(conv_join_kernel<64>, grid, dim3(kJoinThreads), 0, st, c.partials, rows,
+                         c.K, c.channels, c.grad_weight, c.grad_bias);
+    else
+      hipLaunchKernelGGL(conv_join_kernel<16>, grid, dim3(kJoinThreads), 0, st, c.partials, rows,
+                         c.K, c.channels, c.grad_weight, c.grad_bias);
+  }
   return launch_status();
 }

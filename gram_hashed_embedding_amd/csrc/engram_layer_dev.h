@@ -119,26 +119,32 @@ __device__ __forceinline__ void code_values(uint32_t word, float scale, float *f
 
 // ------------------------------------------------- sums of rows of partials --
 // The sum over rows of the fp32 column that `column` starts, in fp64 and in a
-// fixed order: a block of kJoinThreads takes kJoinColumns adjacent columns,
-// each of its kJoinSlots threads of a column every kJoinSlots-th row.  The sum
-// is left in the threads of slot 0.
-constexpr int kJoinThreads = 1024, kJoinColumns = 16, kJoinSlots = kJoinThreads / kJoinColumns;
+// fixed order: a block of kJoinThreads takes COLUMNS adjacent columns, each of
+// its other threads of a column every so many rows.  The sum is left in the
+// first thread of each column.
+constexpr int kJoinThreads = 1024;
+template <int COLUMNS>
 __device__ __forceinline__ double join_column(const float *column, int64_t rows, int64_t stride,
-                                              bool on, double (*part)[kJoinColumns]) {
-  const int slot = threadIdx.x / kJoinColumns, c = threadIdx.x % kJoinColumns;
+                                              bool on) {
+  constexpr int kSlots = kJoinThreads / COLUMNS;
+  __shared__ double part[kSlots][COLUMNS];
+  const int slot = threadIdx.x / COLUMNS, c = threadIdx.x % COLUMNS;
   double s = 0.0;
   if (on) {
 #pragma unroll 8
-    for (int64_t r = slot; r < rows; r += kJoinSlots) s += column[r * stride];
+    for (int64_t r = slot; r < rows; r += kSlots) s += column[r * stride];
   }
   part[slot][c] = s;
   __syncthreads();
   s = 0.0;
   if (slot == 0)
 #pragma unroll
-    for (int q = 0; q < kJoinSlots; ++q) s += part[q][c];
+    for (int q = 0; q < kSlots; ++q) s += part[q][c];
   __syncthreads();
   return s;
 }
+// Few rows leave 16 threads a column enough to do; many take 64.
+constexpr int64_t kJoinFewRows = 256;
+inline int join_columns(int64_t rows) { return rows <= kJoinFewRows ? 64 : 16; }
 
 }  // namespace engram

@@ -563,14 +563,15 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(const NormArgs a
 }
 
 // The weights' gradients from the row blocks' sums.
+template <int COLUMNS>
 __global__ __launch_bounds__(kJoinThreads) void norm_join_kernel(const NormArgs a) {
-  __shared__ double part[kJoinSlots][kJoinColumns];
-  const int64_t c = (int64_t)blockIdx.x * kJoinColumns + threadIdx.x % kJoinColumns;
+  const int64_t c = (int64_t)blockIdx.x * COLUMNS + threadIdx.x % COLUMNS;
   const bool on = c < a.s.channels && a.s.rows > 0;
   const int64_t stride = 2 * a.s.channels;
-  const double d = join_column(a.partials + c, a.s.rowblocks, stride, on, part);
-  const double n = join_column(a.partials + a.s.channels + c, a.s.rowblocks, stride, on, part);
-  if (threadIdx.x >= kJoinColumns || c >= a.s.channels) return;
+  const double d = join_column<COLUMNS>(a.partials + c, a.s.rowblocks, stride, on);
+  const double n =
+      join_column<COLUMNS>(a.partials + a.s.channels + c, a.s.rowblocks, stride, on);
+  if (threadIdx.x >= COLUMNS || c >= a.s.channels) return;
   const uint16_t *wp = static_cast<const uint16_t *>(a.w_post);
   const uint16_t *sc = static_cast<const uint16_t *>(a.scale);
   if (a.grad_w_post != nullptr) a.grad_w_post[c] = (float)(d * (sc ? bf16_lo(sc[c]) : 1.0f));
@@ -649,7 +650,7 @@ int engram::launch_residual_norm_backward(const engram_norm_args &c) {
   const NormShape s = norm_backward_shape(c.rows, c.channels, c.groups);
   const NormArgs a = norm_args(c, s);
   if (!grid_fits(s.colblocks * s.rowblocks, s.threads) ||
-      !grid_fits(ceil_div(c.channels, kJoinColumns), kJoinThreads))
+      !grid_fits(ceil_div(c.channels, 16), kJoinThreads))
     return ENGRAM_EINVAL;
   hipStream_t st = as_stream(c.stream);
   if (c.rows > 0) {
@@ -667,8 +668,13 @@ int engram::launch_residual_norm_backward(const engram_norm_args &c) {
       default: return ENGRAM_EINVAL;
     }
   }
-  if (a.grad_w_post != nullptr || a.grad_scale != nullptr || a.grad_w_next != nullptr)
-    hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)ceil_div(c.channels, kJoinColumns)),
-                       dim3(kJoinThreads), 0, st, a);
+  if (a.grad_w_post != nullptr || a.grad_scale != nullptr || a.grad_w_next != nullptr) {
+    const int columns = join_columns(c.rows > 0 ? s.rowblocks : 0);
+    const dim3 grid((unsigned)ceil_div(c.channels, columns));
+    if (columns == 64)
+      hipLaunchKernelGGL(norm_join_kernel<64>, grid, dim3(kJoinThreads), 0, st, a);
+    else
+      hipLaunchKernelGGL(norm_join_kernel<16>, grid, dim3(kJoinThreads), 0, st, a);
+  }
   return launch_status();
 }
