@@ -85,7 +85,7 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_kernel(
 // power of two, at most a block).
 struct EmbedGradArgs {
   const uint32_t *keys, *vals;  // sorted tokens and their positions
-  const PlanScalars *plan;
+  const PlanScalars *plan;      // of the sort, or null (sorted without one)
   const u32x4 *grads;
   double *partials;  // [walks][2][channels]: of the run that enters, that leaves
   int64_t n, chunks, table_rows;
@@ -95,10 +95,69 @@ struct EmbedGradArgs {
   void *out;
 };
 
-// Whether the plan holds a valid order (a wait of it that expired has marked
-// the error counter; nothing is read by such an order, and nothing written).
-__device__ __forceinline__ bool plan_holds(const EmbedGradArgs &g) {
-  return g.plan->stalled == 0 && g.plan->n == (uint64_t)g.n;
+// Whether the order is valid (a wait of the sort that expired has marked the
+// error counter; nothing is read by such an order, and nothing written).
+__device__ __forceinline__ bool order_holds(const EmbedGradArgs &g) {
+  return g.plan == nullptr || g.plan->stalled == 0;
+}
+
+// A few thousand tokens are sorted by counting, in one launch: a token's place
+// is the number of smaller ones, and of equal ones before it.  A block places
+// kRankBlock tokens; its threads are kRankBlock tokens wide and share out the
+// tokens to compare with, four at a time from LDS.  n^2 comparisons over the
+// whole GPU beat the sort's passes, which wait on one another, up to
+// kRankTokens.
+constexpr int kRankThreads = 1024, kRankBlock = 16, kRankParts = kRankThreads / kRankBlock;
+constexpr int64_t kRankTokens = 8192;
+
+__global__ __launch_bounds__(kRankThreads) void embed_rank_kernel(
+    const int64_t *__restrict__ tokens, int n, uint32_t table_rows, uint32_t *keys,
+    uint32_t *vals, int64_t *err) {
+  __shared__ u32x4 s_key4[kRankTokens / 4];
+  __shared__ uint32_t s_count[kRankParts][kRankBlock];
+  uint32_t *s_key = reinterpret_cast<uint32_t *>(s_key4);
+  const int i0 = blockIdx.x * kRankBlock;
+  int bad = 0;
+  for (int j = threadIdx.x; j < ((n + 3) & ~3); j += kRankThreads) {
+    uint32_t k = 0xffffffffu;  // past the end: above every key
+    if (j < n) {
+      const int64_t t = tokens[j];
+      const bool ok = t >= 0 && t < (int64_t)table_rows;
+      k = ok ? (uint32_t)t : table_rows;
+      bad += !ok && t != -1 && j >= i0 && j < i0 + kRankBlock ? 1 : 0;
+    }
+    s_key[j] = k;
+  }
+  count_errors(bad, err);
+  __syncthreads();
+  const int lane = threadIdx.x % kRankBlock, part = threadIdx.x / kRankBlock;
+  const int i = i0 + lane;
+  const uint32_t key = i < n ? s_key[i] : 0u;
+  const int quads = (n + 3) / 4;
+  uint32_t count = 0;
+  // the block's own tokens lie in quads [i0 / 4, i0 / 4 + kRankBlock / 4)
+  for (int q = part; q < quads; q += kRankParts) {
+    const u32x4 k = s_key4[q];
+    if (q < i0 / 4) {
+      count += (k.x <= key) + (k.y <= key) + (k.z <= key) + (k.w <= key);
+    } else if (q >= i0 / 4 + kRankBlock / 4) {
+      count += (k.x < key) + (k.y < key) + (k.z < key) + (k.w < key);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t other = e == 0 ? k.x : e == 1 ? k.y : e == 2 ? k.z : k.w;
+        count += other < key || (other == key && q * 4 + e < i) ? 1u : 0u;
+      }
+    }
+  }
+  s_count[part][lane] = count;
+  __syncthreads();
+  if (threadIdx.x >= kRankBlock || i >= n) return;
+  uint32_t place = 0;
+#pragma unroll
+  for (int p = 0; p < kRankParts; ++p) place += s_count[p][lane];
+  keys[place] = key;
+  vals[place] = (uint32_t)i;
 }
 
 template <class OUT, bool ACCUMULATE>
@@ -198,7 +257,7 @@ template <class OUT, bool ACCUMULATE>
 __global__ __launch_bounds__(kEmbedThreads) void embed_grad_kernel(const EmbedGradArgs g) {
   __shared__ int64_t bound[2];
   __shared__ uint32_t present[kMaxRowsPerBlock];
-  if (g.n > 0 && !plan_holds(g)) return;
+  if (!order_holds(g)) return;
   const int slots = kEmbedThreads / g.lanes;
   const int slot = threadIdx.x / g.lanes, lane = threadIdx.x % g.lanes;
   if (blockIdx.x < g.walk_blocks) {
@@ -233,57 +292,63 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_grad_kernel(const EmbedGr
   }
 }
 
-// The runs that cross chunks: the walker of the chunk that one begins in adds
-// its parts, in order.
+// The runs that cross chunks: a block of the chunk that one begins in adds its
+// parts.  It takes up to 64 chunks of 8 channels; its other threads share the
+// parts out, so a frequent token's hundreds of them are on their way together,
+// and their sums are added in order.
 template <class OUT, bool ACCUMULATE>
-__global__ __launch_bounds__(kEmbedThreads) void embed_join_kernel(const EmbedGradArgs g) {
-  const int slots = kEmbedThreads / g.lanes;
-  const int64_t walk = (int64_t)blockIdx.x * slots + threadIdx.x / g.lanes;
-  if (walk + 1 >= g.walks || !plan_holds(g)) return;
+__global__ __launch_bounds__(kEmbedThreads) void embed_join_kernel(const EmbedGradArgs g,
+                                                                   int64_t col_blocks) {
+  __shared__ double sums[kEmbedThreads][9];  // (9: rows in other banks)
+  const int64_t walk = blockIdx.x / col_blocks;
+  if (walk + 1 >= g.walks || !order_holds(g)) return;
   const int64_t a = walk * g.walk_len, b = a + g.walk_len;
   const uint32_t run = g.keys[b - 1];
   if (run >= g.table_rows || g.keys[b] != run) return;           // does not leave
   if (g.keys[a] == run && a > 0 && g.keys[a - 1] == run) return;  // entered: another's
-  // the last chunk it reaches: chunks whose first key is the run's, so far
-  int64_t last = walk + 1, high = g.walks;  // first key of `last` is the run's; of `high` not
-  while (high - last > 1) {
-    const int64_t mid = last + (high - last) / 2;
-    if (g.keys[mid * g.walk_len] == run)
-      last = mid;
-    else
-      high = mid;
+  // the last chunk it reaches: those after begin with its key, 64 tested at once
+  int64_t last = walk;
+  for (int more = 64; more == 64; last += more) {
+    const int64_t q = last + 1 + (threadIdx.x & 63);
+    more = __popcll(__ballot(q < g.walks && g.keys[q * g.walk_len] == run));
   }
-  for (int64_t c = threadIdx.x % g.lanes; c < g.chunks; c += g.lanes) {
-    double sum[8];
+  const int cols = g.lanes < 64 ? g.lanes : 64, parts = kEmbedThreads / cols;
+  const int col = threadIdx.x % cols, part = threadIdx.x / cols;
+  const int64_t c = (blockIdx.x % col_blocks) * cols + col;
+  const bool on = c < g.chunks;
+  double sum[8] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
+  // part 0 begins with the run's first piece, the one that leaves `walk`
+  for (int64_t q = walk + part; on && q <= last; q += parts) {
     const f64x2 *src = reinterpret_cast<const f64x2 *>(g.partials) +
-                       ((walk * 2 + 1) * g.chunks + c) * 4;
+                       ((q * 2 + (q == walk ? 1 : 0)) * g.chunks + c) * 4;
+    f64x2 v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = src[e];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const f64x2 v = src[e];
-      sum[2 * e] = v.x;
-      sum[2 * e + 1] = v.y;
+      sum[2 * e] += v[e].x;
+      sum[2 * e + 1] += v[e].y;
     }
-#pragma unroll 8
-    for (int64_t q = walk + 1; q <= last; ++q) {
-      src = reinterpret_cast<const f64x2 *>(g.partials) + (q * 2 * g.chunks + c) * 4;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const f64x2 v = src[e];
-        sum[2 * e] += v.x;
-        sum[2 * e + 1] += v.y;
-      }
-    }
-    write_row<OUT, ACCUMULATE>(g, run, c, sum);
   }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sums[threadIdx.x][e] = sum[e];
+  __syncthreads();
+  if (part != 0 || !on) return;
+  for (int q = 1; q < parts; ++q)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] += sums[q * cols + col][e];
+  write_row<OUT, ACCUMULATE>(g, run, c, sum);
 }
 
 template <class OUT, bool ACCUMULATE>
 void launch_grad(const EmbedGradArgs &g, unsigned blocks, hipStream_t s) {
   const dim3 block(kEmbedThreads);
   hipLaunchKernelGGL((embed_grad_kernel<OUT, ACCUMULATE>), dim3(blocks), block, 0, s, g);
-  if (g.walks > 1)
-    hipLaunchKernelGGL((embed_join_kernel<OUT, ACCUMULATE>), dim3((unsigned)g.walk_blocks), block,
-                       0, s, g);
+  if (g.walks > 1) {
+    const int64_t col_blocks = ceil_div(g.chunks, 64);
+    hipLaunchKernelGGL((embed_join_kernel<OUT, ACCUMULATE>), dim3((unsigned)(g.walks * col_blocks)),
+                       block, 0, s, g, col_blocks);
+  }
 }
 
 }  // namespace
@@ -321,24 +386,34 @@ int engram::launch_embed_grad(const EmbedGradCall &c, const Plan &p, void *d_wor
   g.lanes = embed_row_lanes(c.channels);
   g.scale = c.scale;
   g.out = c.grad_table;
-  // about 128 KB of fp32 rows a block of zeros
+  // about 128 KB of rows a block of zeros
+  const int64_t row_bytes = c.channels * (c.type == ENGRAM_F32 ? 4 : 2);
   g.rows_per_block = 8;
-  while (g.rows_per_block < kMaxRowsPerBlock && g.rows_per_block * c.channels < 32768)
+  while (g.rows_per_block < kMaxRowsPerBlock && g.rows_per_block * row_bytes < (128 << 10))
     g.rows_per_block *= 2;
   g.walk_len = embed_chunk(c.n, c.channels);
   g.walks = ceil_div(c.n, g.walk_len);
   g.walk_blocks = ceil_div(g.walks, kEmbedThreads / g.lanes);
   const int64_t zero_blocks = c.accumulate ? 0 : ceil_div(c.table_rows, g.rows_per_block);
   const int64_t blocks = g.walk_blocks + zero_blocks;
-  if (!grid_fits(blocks, kEmbedThreads)) return ENGRAM_EINVAL;
+  if (!grid_fits(blocks, kEmbedThreads) ||
+      !grid_fits(g.walks * ceil_div(g.chunks, 64), kEmbedThreads))
+    return ENGRAM_EINVAL;
   if (c.n > 0) {
     const Views v = views_of(p, d_workspace);
     g.keys = v.sorted_keys;
     g.vals = v.sorted_vals;
-    g.plan = v.scalars;
-    const int rc =
-        launch_plan_crowded(c.tokens, c.n, c.table_rows, p, d_workspace, c.err, stream);
-    if (rc != ENGRAM_OK || c.table_rows == 0) return rc;
+    if (c.n <= kRankTokens) {
+      hipLaunchKernelGGL(embed_rank_kernel, dim3((unsigned)ceil_div(c.n, kRankBlock)),
+                         dim3(kRankThreads), 0, st, c.tokens, (int)c.n, (uint32_t)c.table_rows,
+                         const_cast<uint32_t *>(g.keys), const_cast<uint32_t *>(g.vals), c.err);
+    } else {
+      g.plan = v.scalars;
+      const int rc =
+          launch_sort_crowded(c.tokens, c.n, c.table_rows, p, d_workspace, c.err, stream);
+      if (rc != ENGRAM_OK) return rc;
+    }
+    if (c.table_rows == 0) return launch_status();
   }
   if (c.accumulate)
     launch_grad<float, true>(g, (unsigned)blocks, st);

@@ -1048,9 +1048,10 @@ void launch_pass(int src, const SortLayout &L, const PassArgs &a, hipStream_t s)
 namespace engram {
 namespace {
 
-// The plan; id_buckets: whether given ids may take the one-pass bucket sort.
+// The plan; id_buckets: whether given ids may take the one-pass bucket sort;
+// slots: whether the distinct rows' slots are wanted (and the plan's stamp).
 int plan_of(const int64_t *ids, const HashParams *hp, int64_t n, int64_t table_rows,
-            const Plan &p, void *ws, int64_t *err, void *stream, bool id_buckets) {
+            const Plan &p, void *ws, int64_t *err, void *stream, bool id_buckets, bool slots) {
   hipStream_t s = as_stream(stream);
   const Views v = views_of(p, ws);
   uint32_t *tickets = v.counters;              // [4], then the slot scan's
@@ -1181,6 +1182,7 @@ int plan_of(const int64_t *ids, const HashParams *hp, int64_t n, int64_t table_r
                          L.sg, top_bits, low_bits, hist, last_k, last_v, other_k, other_v);
   }
   // distinct-row slots
+  if (!slots) return launch_status();
   hipLaunchKernelGGL(range_slots_kernel, dim3((unsigned)p.slot_tiles), dim3(kSlotThreads), 0, s,
                      v.sorted_keys, n, (uint32_t)table_rows, p.num_ranges, v.status + sort_words,
                      tickets + kSlotTicketAt, v.head_off, v.scalars, err);
@@ -1192,10 +1194,10 @@ int plan_of(const int64_t *ids, const HashParams *hp, int64_t n, int64_t table_r
 
 int engram::launch_plan(const int64_t *ids, const HashParams *hp, int64_t n, int64_t table_rows,
                         const Plan &p, void *ws, int64_t *err, void *stream) {
-  return plan_of(ids, hp, n, table_rows, p, ws, err, stream, true);
+  return plan_of(ids, hp, n, table_rows, p, ws, err, stream, true, true);
 }
 
-int engram::launch_plan_crowded(const int64_t *ids, int64_t n, int64_t table_rows, const Plan &p,
+int engram::launch_sort_crowded(const int64_t *ids, int64_t n, int64_t table_rows, const Plan &p,
                                 void *ws, int64_t *err, void *stream) {
-  return plan_of(ids, nullptr, n, table_rows, p, ws, err, stream, false);
+  return plan_of(ids, nullptr, n, table_rows, p, ws, err, stream, false, false);
 }
