@@ -10,7 +10,7 @@
 namespace engram {
 
 NormShape norm_shape(int64_t rows, int64_t channels, int64_t groups, int max_items,
-                     int64_t blocks) {
+                     int64_t blocks, bool sums) {
   NormShape s = {};
   s.rows = rows;
   s.channels = channels;
@@ -44,12 +44,14 @@ NormShape norm_shape(int64_t rows, int64_t channels, int64_t groups, int max_ite
   const int64_t steps = rows > 0 ? ceil_div(rows, s.trows) : 1;  // of trows rows each
   int64_t want = blocks * 256 / s.threads / s.colblocks;
   if (want < 1) want = 1;
-  // Few rows: four steps a block while that leaves 512 blocks (the sums' rows that
-  // the blocks leave cost as much as their idle threads: [4099, 1024] with 16
-  // groups took 26.3 us so, 32 us with a block to a step or two).
-  const int64_t least = ceil_div(512, s.colblocks), four = steps / 4;
-  if (want > four && want > least) want = four > least ? four : least;
-  if (want * kNormMaxSteps < steps) want = ceil_div(steps, kNormMaxSteps);
+  if (sums) {
+    // Few rows: four steps a block while that leaves 512 blocks (the sums' rows
+    // that the blocks leave cost as much as their idle threads: [4099, 1024] with
+    // 16 groups took 26.3 us so, 32 us with a block to a step or two).
+    const int64_t least = ceil_div(512, s.colblocks), four = steps / 4;
+    if (want > four && want > least) want = four > least ? four : least;
+    if (want * kNormMaxSteps < steps) want = ceil_div(steps, kNormMaxSteps);
+  }
   s.rowblocks = steps < want ? steps : want;
   return s;
 }

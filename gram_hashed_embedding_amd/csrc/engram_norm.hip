@@ -623,8 +623,7 @@ NormArgs norm_args(const engram_norm_args &c, const NormShape &s) {
   CASE(64, 2, 256) CASE(256, 1, 256) CASE(256, 2, 256) CASE(1024, 1, 1024) CASE(1024, 2, 1024)
 
 int engram::launch_residual_norm(const engram_norm_args &c) {
-  const NormShape s =
-      norm_shape(c.rows, c.channels, c.groups, kNormForwardItems, kNormForwardBlocks);
+  const NormShape s = norm_forward_shape(c.rows, c.channels, c.groups);
   const NormArgs a = norm_args(c, s);
   if (!grid_fits(s.colblocks * s.rowblocks, s.threads)) return ENGRAM_EINVAL;
   const dim3 grid((unsigned)(s.colblocks * s.rowblocks)), block(s.threads);

@@ -22,7 +22,7 @@ import torch
 
 from . import abi
 from .abi import ACT_BLOCK, BF16, F32, NORM_MAX_GROUP  # noqa: F401
-from .engram import EngramError, _check, _lib, _on  # noqa: F401
+from .engram import EngramError, _lib
 
 abi.declare_layer(_lib)
 
@@ -79,6 +79,17 @@ def _bytes(workspace, need, device, index, what):
         raise ValueError(f"workspace must hold {need} bytes, holds {workspace.numel()}")
     _tensor(workspace, torch.uint8, workspace.numel(), "workspace", index)
     return workspace
+
+
+def _run(index, name, *args):
+    """The library's call `name` with device `index` current; raises on a status."""
+    if torch.cuda.current_device() == index:
+        status = getattr(_lib, name)(*args)
+    else:
+        with torch.cuda.device(index):
+            status = getattr(_lib, name)(*args)
+    if status != abi.ENGRAM_OK:
+        raise EngramError(status, name)
 
 
 def _streamed(call):
@@ -194,15 +205,13 @@ def engram_residual_norm(residual, y=None, *, gate=None, w_post=None, scale=None
     if next_codes:
         nc, ns = _codes(rows, channels, groups, device)
         nc_p, ns_p = nc.data_ptr(), ns.data_ptr()
-    with _on(device):
-        status = _lib.engram_residual_norm(_NORM.pack(
-            rows, channels, groups, width, eps, residual_scale, kind, 0,
-            _tensor(residual, rt, n, "residual", index), y_p, gate_p,
-            _optional(w_post, bf, channels, "w_post", index),
-            _optional(scale, bf, channels, "scale", index),
-            _optional(w_next, bf, channels, "w_next", index), out_p, next_p, post_p, rnext_p,
-            yc_p, ys_p, nc_p, ns_p, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, _stream_of(index)))
-    _check(status, "engram_residual_norm")
+    _run(index, "engram_residual_norm", _NORM.pack(
+        rows, channels, groups, width, eps, residual_scale, kind, 0,
+        _tensor(residual, rt, n, "residual", index), y_p, gate_p,
+        _optional(w_post, bf, channels, "w_post", index),
+        _optional(scale, bf, channels, "scale", index),
+        _optional(w_next, bf, channels, "w_next", index), out_p, next_p, post_p, rnext_p,
+        yc_p, ys_p, nc_p, ns_p, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, _stream_of(index)))
     return ResidualNorm(out, next_out, rstd_post, rstd_next, yc, ys, nc, ns)
 
 
@@ -261,16 +270,14 @@ def engram_residual_norm_backward(grad_out, grad_next=None, *, out=None, rstd_po
         workspace = _bytes(workspace, need, device, index,
                            "engram_residual_norm_backward_workspace")
         ws_p, size = workspace.data_ptr(), workspace.numel()
-    with _on(device):
-        status = _lib.engram_residual_norm_backward(_NORM.pack(
-            rows, channels, groups, width, 0.0, residual_scale, kind, 0, 0, y_p, gate_p,
-            _optional(w_post, bf, channels, "w_post", index),
-            _optional(scale, bf, channels, "scale", index),
-            _optional(w_next, bf, channels, "w_next", index), out_p, 0, post_p, rnext_p, yc_p,
-            ys_p, 0, 0, _optional(grad_out, rt, n, "grad_out", index), dn_p,
-            _tensor(grad_residual, rt, n, "grad_residual", index), gy_p, gz_p, gp_p, gs_p, gn_p,
-            ws_p, size, _stream_of(index)))
-    _check(status, "engram_residual_norm_backward")
+    _run(index, "engram_residual_norm_backward", _NORM.pack(
+        rows, channels, groups, width, 0.0, residual_scale, kind, 0, 0, y_p, gate_p,
+        _optional(w_post, bf, channels, "w_post", index),
+        _optional(scale, bf, channels, "scale", index),
+        _optional(w_next, bf, channels, "w_next", index), out_p, 0, post_p, rnext_p, yc_p,
+        ys_p, 0, 0, _optional(grad_out, rt, n, "grad_out", index), dn_p,
+        _tensor(grad_residual, rt, n, "grad_residual", index), gy_p, gz_p, gp_p, gs_p, gn_p,
+        ws_p, size, _stream_of(index)))
     return ResidualNormGrads(grad_residual, gy, gz, gp, gs, gn)
 
 
@@ -299,9 +306,7 @@ def engram_act_encode(x, codes=None, scales=None):
                              device=device)
     cp = _tensor(codes, torch.int8, rows * channels, "codes", index)
     sp = _tensor(scales, torch.float32, rows * code_blocks(channels), "scales", index)
-    with _on(device):
-        status = _lib.engram_act_encode(xp, rows, channels, cp, sp, _stream_of(index))
-    _check(status, "engram_act_encode")
+    _run(index, "engram_act_encode", xp, rows, channels, cp, sp, _stream_of(index))
     return codes, scales
 
 
@@ -318,9 +323,7 @@ def engram_act_decode(codes, scales, out=None):
     if out is None:
         out = torch.empty(codes.shape, dtype=torch.bfloat16, device=device)
     op = _tensor(out, torch.bfloat16, rows * channels, "out", index)
-    with _on(device):
-        status = _lib.engram_act_decode(cp, sp, rows, channels, op, _stream_of(index))
-    _check(status, "engram_act_decode")
+    _run(index, "engram_act_decode", cp, sp, rows, channels, op, _stream_of(index))
     return out
 
 
@@ -386,12 +389,10 @@ def engram_ple_conv_backward(grad_out, weight, dilation, x=None, x_codes=None, x
     def ptr(t):
         return None if t is None else t.data_ptr()
 
-    with _on(device):
-        status = _lib.engram_ple_conv_backward(
-            gp, xp, cp, sp, code_width, hp if halo_len else None, halo_len, ids, wp, batch, seq,
-            channels, kernel, int(dilation), ptr(gx), ptr(gh), ptr(gw), ptr(gb),
-            ptr(workspace) if size else None, size, _stream_of(index))
-    _check(status, "engram_ple_conv_backward")
+    _run(index, "engram_ple_conv_backward", gp, xp, cp, sp, code_width,
+         hp if halo_len else None, halo_len, ids, wp, batch, seq, channels, kernel, int(dilation),
+         ptr(gx), ptr(gh), ptr(gw), ptr(gb), ptr(workspace) if size else None, size,
+         _stream_of(index))
     if need_x and halo is not None and gh is None:
         gh = torch.empty_like(halo)  # a halo of no positions
     return ConvGrads(gx, gw, gb, gh)
@@ -431,11 +432,8 @@ def engram_ple_conv_step(x, ring, weight, dilation, positions, slots=None, bias=
         op = _tensor(out, torch.bfloat16, n, "out", index)
     elif out is not None:
         raise ValueError("write_only computes no out")
-    with _on(device):
-        status = _lib.engram_ple_conv_step(xp, rp, ring.shape[0], ring.shape[1], ip, pp, wp, bp,
-                                           batch, tokens, channels, kernel, int(dilation), op, ep,
-                                           _stream_of(index))
-    _check(status, "engram_ple_conv_step")
+    _run(index, "engram_ple_conv_step", xp, rp, ring.shape[0], ring.shape[1], ip, pp, wp, bp,
+         batch, tokens, channels, kernel, int(dilation), op, ep, _stream_of(index))
     return out
 
 
@@ -457,10 +455,8 @@ def engram_embed(tokens, table, scale=1.0, out=None, out_dtype=torch.bfloat16, e
         raise TypeError(f"out must be bfloat16 or float32, is {out.dtype}")
     op = _tensor(out, out.dtype, n * channels, "out", index)
     ep = _optional(err_count, torch.int64, 1, "err_count", index)
-    with _on(device):
-        status = _lib.engram_embed(tp, n, bp, table_rows, channels, float(scale),
-                                   _TYPES[out.dtype], op, ep, _stream_of(index))
-    _check(status, "engram_embed")
+    _run(index, "engram_embed", tp, n, bp, table_rows, channels, float(scale),
+         _TYPES[out.dtype], op, ep, _stream_of(index))
     return out
 
 
@@ -487,10 +483,7 @@ def engram_embed_grad(tokens, grads, table_rows, scale=1.0, grad_table=None,
     ep = _optional(err_count, torch.int64, 1, "err_count", index)
     need = _lib.engram_embed_grad_workspace(n, channels, table_rows)
     workspace = _bytes(workspace, need, device, index, "engram_embed_grad_workspace")
-    with _on(device):
-        status = _lib.engram_embed_grad(tp, n, gp, channels, float(scale), table_rows,
-                                        _TYPES[grad_table.dtype], int(accumulate), op,
-                                        workspace.data_ptr(), workspace.numel(), ep,
-                                        _stream_of(index))
-    _check(status, "engram_embed_grad")
+    _run(index, "engram_embed_grad", tp, n, gp, channels, float(scale), table_rows,
+         _TYPES[grad_table.dtype], int(accumulate), op, workspace.data_ptr(), workspace.numel(),
+         ep, _stream_of(index))
     return grad_table

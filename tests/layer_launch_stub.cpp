@@ -18,8 +18,7 @@ int launch_residual_norm(const engram_norm_args &a) {
   require(a.rows > 0 && a.d_residual != nullptr && a.channels % (8 * a.groups) == 0);
   require(a.d_y == nullptr ? a.d_out == nullptr && a.d_next != nullptr : a.d_out != nullptr);
   require((a.d_w_next != nullptr) == (a.d_next != nullptr));
-  const NormShape s =
-      norm_shape(a.rows, a.channels, a.groups, kNormForwardItems, kNormForwardBlocks);
+  const NormShape s = norm_forward_shape(a.rows, a.channels, a.groups);
   require((int64_t)s.lanes * s.items >= s.chunks && s.rowblocks >= 1);
   return ENGRAM_OK;
 }
