@@ -164,7 +164,7 @@ def declare_layer(lib):
         ("engram_embed", ctypes.c_int, [_vp, i64, _vp, i64, i64, f32, i32, _vp, _vp, _vp]),
         ("engram_embed_grad_workspace", size, [i64, i64, i64]),
         ("engram_embed_grad", ctypes.c_int,
-         [_vp, i64, _vp, i64, f32, i64, i32, i32, _vp, _vp, size, _vp, _vp]),
+         [_vp, i64, _vp, i32, i64, f32, i64, i32, i32, _vp, _vp, size, _vp, _vp]),
     ]:
         f = getattr(lib, name)
         f.restype, f.argtypes = result, args

@@ -86,7 +86,7 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_kernel(
 struct EmbedGradArgs {
   const uint32_t *keys, *vals;  // sorted tokens and their positions
   const PlanScalars *plan;      // of the sort, or null (sorted without one)
-  const u32x4 *grads;
+  const void *grads;
   double *partials;  // [walks][2][channels]: of the run that enters, that leaves
   int64_t n, chunks, table_rows;
   int64_t walks, walk_len, walk_blocks;
@@ -183,8 +183,37 @@ __device__ __forceinline__ void write_part(const EmbedGradArgs &g, int64_t walk,
 }
 
 // A walker's chunk [a, b) of the sorted positions: its runs' sums.
-constexpr int kAhead = 8;  // rows in flight
-template <class OUT, bool ACCUMULATE>
+// Eight values of a gradient row, bf16 (uint16_t) or float.
+template <class G>
+struct GradRow;
+template <>
+struct GradRow<uint16_t> {
+  static constexpr int kAhead = 8;  // rows in flight
+  typedef u32x4 Raw;
+  static __device__ __forceinline__ Raw load(const void *p, int64_t chunk) {
+    return static_cast<const u32x4 *>(p)[chunk];
+  }
+  static __device__ __forceinline__ void unpack(const Raw &r, float (&f)[8]) {
+    unpack_bf16x8(r, f);
+  }
+};
+template <>
+struct GradRow<float> {
+  static constexpr int kAhead = 4;
+  struct Raw {
+    f32x4 a, b;
+  };
+  static __device__ __forceinline__ Raw load(const void *p, int64_t chunk) {
+    const f32x4 *q = static_cast<const f32x4 *>(p) + 2 * chunk;
+    return Raw{q[0], q[1]};
+  }
+  static __device__ __forceinline__ void unpack(const Raw &r, float (&f)[8]) {
+    f[0] = r.a.x; f[1] = r.a.y; f[2] = r.a.z; f[3] = r.a.w;
+    f[4] = r.b.x; f[5] = r.b.y; f[6] = r.b.z; f[7] = r.b.w;
+  }
+};
+
+template <class G, class OUT, bool ACCUMULATE>
 __device__ void walk_chunk(const EmbedGradArgs &g, int64_t walk, int lane) {
   const int64_t a = walk * g.walk_len, b = min(a + g.walk_len, g.n);
   const uint32_t before = a > 0 ? g.keys[a - 1] : 0xffffffffu;  // no key (they are smaller)
@@ -193,14 +222,15 @@ __device__ void walk_chunk(const EmbedGradArgs &g, int64_t walk, int lane) {
     double sum[8] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
     uint32_t run = g.keys[a];
     bool entered = run == before;
+    constexpr int kAhead = GradRow<G>::kAhead;
     for (int64_t i = a; i < b; i += kAhead) {
       uint32_t key[kAhead];
-      u32x4 v[kAhead];
+      typename GradRow<G>::Raw v[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         const int64_t at = min(i + k, b - 1);
         key[k] = g.keys[at];
-        v[k] = g.grads[(int64_t)g.vals[at] * g.chunks + c];
+        v[k] = GradRow<G>::load(g.grads, (int64_t)g.vals[at] * g.chunks + c);
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
@@ -218,7 +248,7 @@ __device__ void walk_chunk(const EmbedGradArgs &g, int64_t walk, int lane) {
           for (int e = 0; e < 8; ++e) sum[e] = 0.0;
         }
         float f[8];
-        unpack_bf16x8(v[k], f);
+        GradRow<G>::unpack(v[k], f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[e] += f[e];
       }
@@ -253,7 +283,7 @@ constexpr int kMaxRowsPerBlock = 256;
 
 // Blocks below walk_blocks walk the sorted tokens; the others write the zeros
 // of the rows without one.
-template <class OUT, bool ACCUMULATE>
+template <class G, class OUT, bool ACCUMULATE>
 __global__ __launch_bounds__(kEmbedThreads) void embed_grad_kernel(const EmbedGradArgs g) {
   __shared__ int64_t bound[2];
   __shared__ uint32_t present[kMaxRowsPerBlock];
@@ -262,7 +292,7 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_grad_kernel(const EmbedGr
   const int slot = threadIdx.x / g.lanes, lane = threadIdx.x % g.lanes;
   if (blockIdx.x < g.walk_blocks) {
     const int64_t walk = (int64_t)blockIdx.x * slots + slot;
-    if (walk < g.walks) walk_chunk<OUT, ACCUMULATE>(g, walk, lane);
+    if (walk < g.walks) walk_chunk<G, OUT, ACCUMULATE>(g, walk, lane);
     return;
   }
   const int64_t r0 = ((int64_t)blockIdx.x - g.walk_blocks) * g.rows_per_block;
@@ -341,9 +371,13 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_join_kernel(const EmbedGr
 }
 
 template <class OUT, bool ACCUMULATE>
-void launch_grad(const EmbedGradArgs &g, unsigned blocks, hipStream_t s) {
+void launch_grad(const EmbedGradArgs &g, bool float_grads, unsigned blocks, hipStream_t s) {
   const dim3 block(kEmbedThreads);
-  hipLaunchKernelGGL((embed_grad_kernel<OUT, ACCUMULATE>), dim3(blocks), block, 0, s, g);
+  if (float_grads)
+    hipLaunchKernelGGL((embed_grad_kernel<float, OUT, ACCUMULATE>), dim3(blocks), block, 0, s, g);
+  else
+    hipLaunchKernelGGL((embed_grad_kernel<uint16_t, OUT, ACCUMULATE>), dim3(blocks), block, 0, s,
+                       g);
   if (g.walks > 1) {
     const int64_t col_blocks = ceil_div(g.chunks, 64);
     hipLaunchKernelGGL((embed_join_kernel<OUT, ACCUMULATE>), dim3((unsigned)(g.walks * col_blocks)),
@@ -378,7 +412,7 @@ int engram::launch_embed_grad(const EmbedGradCall &c, const Plan &p, void *d_wor
                               void *stream) {
   hipStream_t st = as_stream(stream);
   EmbedGradArgs g = {};
-  g.grads = static_cast<const u32x4 *>(c.grads);
+  g.grads = c.grads;
   g.partials = c.partials;
   g.n = c.n;
   g.chunks = c.channels / 8;
@@ -415,11 +449,12 @@ int engram::launch_embed_grad(const EmbedGradCall &c, const Plan &p, void *d_wor
     }
     if (c.table_rows == 0) return launch_status();
   }
+  const bool wide = c.grads_type == ENGRAM_F32;
   if (c.accumulate)
-    launch_grad<float, true>(g, (unsigned)blocks, st);
+    launch_grad<float, true>(g, wide, (unsigned)blocks, st);
   else if (c.type == ENGRAM_F32)
-    launch_grad<float, false>(g, (unsigned)blocks, st);
+    launch_grad<float, false>(g, wide, (unsigned)blocks, st);
   else
-    launch_grad<uint16_t, false>(g, (unsigned)blocks, st);
+    launch_grad<uint16_t, false>(g, wide, (unsigned)blocks, st);
   return launch_status();
 }

@@ -343,14 +343,15 @@ extern "C" size_t engram_embed_grad_workspace(int64_t n, int64_t channels, int64
 }
 
 extern "C" int engram_embed_grad(const int64_t *d_tokens, int64_t n, const void *d_grads,
-                                 int64_t channels, float scale, int64_t table_rows,
-                                 int32_t grad_type, int32_t accumulate, void *d_grad_table,
+                                 int32_t grads_type, int64_t channels, float scale,
+                                 int64_t table_rows, int32_t table_type, int32_t accumulate, void *d_grad_table,
                                  void *d_workspace, size_t workspace_bytes,
                                  int64_t *d_err_count, void *stream) {
   Plan p;
-  if (!embed_sizes_ok(n, channels, table_rows, grad_type) || !embed_plan(n, table_rows, &p))
+  if (!embed_sizes_ok(n, channels, table_rows, table_type) || !embed_plan(n, table_rows, &p))
     return ENGRAM_EINVAL;
-  if (accumulate != 0 && (accumulate != 1 || grad_type != ENGRAM_F32)) return ENGRAM_EINVAL;
+  if (grads_type != ENGRAM_BF16 && grads_type != ENGRAM_F32) return ENGRAM_EINVAL;
+  if (accumulate != 0 && (accumulate != 1 || table_type != ENGRAM_F32)) return ENGRAM_EINVAL;
   if (table_rows > 0 && d_grad_table == nullptr && !(n == 0 && accumulate)) return ENGRAM_EINVAL;
   if (n > 0 && (d_tokens == nullptr || d_grads == nullptr)) return ENGRAM_EINVAL;
   if (any_misaligned({d_grads, d_grad_table})) return ENGRAM_EALIGN;
@@ -360,7 +361,7 @@ extern "C" int engram_embed_grad(const int64_t *d_tokens, int64_t n, const void 
   if (n == 0 && (accumulate || table_rows == 0)) return ENGRAM_OK;
   double *partials =
       n > 0 ? reinterpret_cast<double *>(static_cast<char *>(d_workspace) + p.total) : nullptr;
-  const EmbedGradCall c = {d_tokens, n,         d_grads,    channels,     scale, table_rows,
-                           grad_type, accumulate, d_grad_table, partials, d_err_count};
+  const EmbedGradCall c = {d_tokens,   n,          d_grads,    grads_type,   channels, scale,
+                           table_rows, table_type, accumulate, d_grad_table, partials, d_err_count};
   return launch_embed_grad(c, p, d_workspace, stream);
 }

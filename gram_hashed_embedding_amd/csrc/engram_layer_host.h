@@ -114,6 +114,7 @@ struct EmbedGradCall {
   const int64_t *tokens;
   int64_t n;
   const void *grads;
+  int32_t grads_type;
   int64_t channels;
   float scale;
   int64_t table_rows;

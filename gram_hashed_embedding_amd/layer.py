@@ -463,8 +463,8 @@ def engram_embed(tokens, table, scale=1.0, out=None, out_dtype=torch.bfloat16, e
 @_streamed
 def engram_embed_grad(tokens, grads, table_rows, scale=1.0, grad_table=None,
                       grad_dtype=torch.float32, accumulate=False, workspace=None, err_count=None):
-    """The gradient of engram_embed into the whole table [table_rows, channels] (grad_dtype:
-    fp32 or bf16): rows without a token get zeros; with accumulate (fp32, grad_table given) the
+    """The gradient of engram_embed, from grads bf16 or fp32 [..., channels], into the whole
+    table [table_rows, channels] (grad_dtype: fp32 or bf16): rows without a token get zeros; with accumulate (fp32, grad_table given) the
     sums are added to the rows that have tokens."""
     device, index = _device_of(grads, "grads")
     n = tokens.numel()
@@ -472,7 +472,9 @@ def engram_embed_grad(tokens, grads, table_rows, scale=1.0, grad_table=None,
     if channels < 1:
         raise ValueError("grads must be [..., channels]")
     tp = _tensor(tokens, torch.int64, n, "tokens", index)
-    gp = _tensor(grads, torch.bfloat16, n * channels, "grads", index)
+    if grads.dtype not in _TYPES:
+        raise TypeError(f"grads must be bfloat16 or float32, is {grads.dtype}")
+    gp = _tensor(grads, grads.dtype, n * channels, "grads", index)
     if grad_table is None:
         if accumulate:
             raise ValueError("accumulate needs grad_table")
@@ -483,7 +485,7 @@ def engram_embed_grad(tokens, grads, table_rows, scale=1.0, grad_table=None,
     ep = _optional(err_count, torch.int64, 1, "err_count", index)
     need = _lib.engram_embed_grad_workspace(n, channels, table_rows)
     workspace = _bytes(workspace, need, device, index, "engram_embed_grad_workspace")
-    _run(index, "engram_embed_grad", tp, n, gp, channels, float(scale), table_rows,
-         _TYPES[grad_table.dtype], int(accumulate), op, workspace.data_ptr(), workspace.numel(),
-         ep, _stream_of(index))
+    _run(index, "engram_embed_grad", tp, n, gp, _TYPES[grads.dtype], channels, float(scale),
+         table_rows, _TYPES[grad_table.dtype], int(accumulate), op, workspace.data_ptr(),
+         workspace.numel(), ep, _stream_of(index))
     return grad_table

@@ -240,10 +240,10 @@ int engram_ple_conv_step(const void *d_x, void *d_ring, int64_t ring_count, int6
  * product is added to the row (one fp32 add) and rows without a token are
  * left alone.  The sum and the product are fp64, rounded once to fp32 (and
  * that to bf16 for a bf16 table): deterministic, and for gradients whose sums
- * fit fp64 the same in any order (engram_scatter_add has the limits).
+ * fit fp64 the same in any order (engram_scatter_add has the limits, for bf16).
  *   d_tokens as above (padding and invalid ids are skipped, the latter
- *   counted); d_grads bf16 [n, channels]; d_grad_table [table_rows, channels]
- *   of grad_type (accumulate: fp32 only).  table_rows < 2^32 - 1, n < 2^32 - 1.
+ *   counted); d_grads [n, channels] of grads_type; d_grad_table [table_rows,
+ *   channels] of table_type (accumulate: fp32 only).  table_rows < 2^32 - 1, n < 2^32 - 1.
  *   The workspace holds engram_embed_grad_workspace bytes, 16-byte aligned.
  * Errors: EINVAL, EALIGN, EWORKSPACE.  n == 0 writes zeros (accumulate:
  * nothing).
@@ -252,10 +252,11 @@ int engram_embed(const int64_t *d_tokens, int64_t n, const void *d_table, int64_
                  int64_t channels, float scale, int32_t out_type, void *d_out,
                  int64_t *d_err_count, void *stream);
 size_t engram_embed_grad_workspace(int64_t n, int64_t channels, int64_t table_rows);
-int engram_embed_grad(const int64_t *d_tokens, int64_t n, const void *d_grads, int64_t channels,
-                      float scale, int64_t table_rows, int32_t grad_type, int32_t accumulate,
-                      void *d_grad_table, void *d_workspace, size_t workspace_bytes,
-                      int64_t *d_err_count, void *stream);
+int engram_embed_grad(const int64_t *d_tokens, int64_t n, const void *d_grads,
+                      int32_t grads_type, int64_t channels, float scale, int64_t table_rows,
+                      int32_t table_type, int32_t accumulate, void *d_grad_table,
+                      void *d_workspace, size_t workspace_bytes, int64_t *d_err_count,
+                      void *stream);
 
 #ifdef __cplusplus
 }

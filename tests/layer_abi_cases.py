@@ -184,12 +184,13 @@ def case_embed_grad_rejects(lib):
     assert need >= 500 // 64 * 16 * 8
 
     def e(tokens=A, n=500, grads=A, channels=16, rows=10, kind=abi.F32, acc=0, out=A, ws=A,
-          size=need):
-        return lib.engram_embed_grad(tokens, n, grads, channels, 1.0, rows, kind, acc, out, ws,
-                                     size, None, None)
+          size=need, given=abi.BF16):
+        return lib.engram_embed_grad(tokens, n, grads, given, channels, 1.0, rows, kind, acc, out,
+                                     ws, size, None, None)
     for bad in (dict(n=-1), dict(rows=-1), dict(channels=12), dict(kind=2), dict(acc=2),
                 dict(acc=1, kind=abi.BF16), dict(tokens=None), dict(grads=None), dict(out=None),
-                dict(n=1 << 32), dict(rows=(1 << 32) - 1)):
+                dict(n=1 << 32), dict(rows=(1 << 32) - 1),
+                dict(given=2)):
         assert e(**bad) == INVALID, bad
     assert e(grads=ODD) == ALIGN and e(out=ODD) == ALIGN
     for bad in (dict(ws=None), dict(ws=ODD), dict(size=need - 1)):

@@ -73,6 +73,23 @@ def test_gradient(n, rows, channels, dtype):
     grad_case(n, rows, channels, n + rows, dtype=dtype)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,rows,channels,hot", [(1, 5, 8, 0), (4099, 300, 136, 0.5),
+                                                 (20000, 900, 2056, 0.3)])
+def test_float_gradients(n, rows, channels, hot, dtype):
+    """Float gradients (of a float stream), of values that bf16 does not hold: their 24 bits over
+    a factor of 2^11 and up to 2^13 terms leave the fp64 sums exact."""
+    t = tokens(n, rows, n, hot)
+    g = torch.randn((n, channels), generator=torch.Generator("cuda").manual_seed(n),
+                    device="cuda").clamp_(-8, 8)
+    g[g.abs() < 2.0 ** -8] = 0
+    got = L.engram_embed_grad(dev(t), g, rows, 0.7, grad_dtype=dtype)
+    want = ref.embed_grad(t, ref.f64(g), rows, 0.7).astype(np.float64)
+    if dtype == torch.bfloat16:
+        want = ref.bf16(want)
+    assert np.array_equal(ref.f64(got), want)
+
+
 @pytest.mark.parametrize("n", [128, 1000, 20000, 70000])
 @pytest.mark.parametrize("hot", [0.3, 0.95, 1.0])
 @pytest.mark.parametrize("channels", [8, 264])
