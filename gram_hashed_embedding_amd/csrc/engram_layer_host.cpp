@@ -27,14 +27,13 @@ NormShape norm_shape(int64_t rows, int64_t channels, int64_t groups, int max_ite
     while (s.lanes < s.chunks) s.lanes *= 2;
   } else if (s.chunks <= 64 * (int64_t)max_items && rows * groups >= 4096) {
     s.lanes = 64;
-    s.items = s.chunks <= 128 ? 2 : 4;
+    s.items = (int)ceil_div(s.chunks, 64);
   } else {
     s.lanes = s.chunks <= 256 * (int64_t)max_items && (s.chunks <= 256 || rows * groups >= 1024)
                   ? 256
                   : 1024;
     s.threads = s.lanes;
-    s.items = 1;
-    while ((int64_t)s.lanes * s.items < s.chunks) s.items *= 2;
+    s.items = (int)ceil_div(s.chunks, s.lanes);
   }
   const int slots = s.threads / s.lanes;
   s.gcols = 1;

@@ -637,7 +637,9 @@ int engram::launch_residual_norm(const engram_norm_args &c) {
       hipLaunchKernelGGL((norm_forward_kernel<uint16_t, L, I, T>), grid, block, 0, st, a);  \
     break;
     ENGRAM_NORM_COMMON(ENGRAM_NORM_CASE)
+    ENGRAM_NORM_CASE(64, 3, 256)
     ENGRAM_NORM_CASE(64, 4, 256)
+    ENGRAM_NORM_CASE(256, 3, 256)
     ENGRAM_NORM_CASE(256, 4, 256)
 #undef ENGRAM_NORM_CASE
     default: return ENGRAM_EINVAL;

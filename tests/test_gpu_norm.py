@@ -111,6 +111,7 @@ def run_case(rows, channels, groups, gate, residual, codes, seed, with_weights=T
 # every way a group is held: 4 to 64 lanes, several chunks a lane, whole blocks
 SHAPES = [(1, 8, 1), (3, 32, 1), (70, 120, 5), (9, 128, 1), (33, 1024, 16), (65, 6144, 24),
           (5, 504, 1), (2, 1536, 3), (4097, 520, 1), (1400, 3000, 3), (4098, 1040, 1),
+          (4099, 2048, 1), (1026, 6144, 1),
           (7, 1000, 1), (8, 6144, 1), (40, 4104, 1), (1030, 4096, 1), (1025, 8192, 1),
           (5, 8200, 1), (3, 16384, 1), (2, 32768, 2), (700, 64, 1), (1, 2048, 64)]
 
