@@ -14,11 +14,11 @@
 // atomic is needed: the result does not depend on timing, and each row is
 // written once.  Walkers take equal chunks of the sorted positions, however
 // the tokens crowd: a run inside a chunk is summed and written by its walker;
-// a run that crosses chunks leaves a part in each, which the walker of the
-// chunk it begins in adds up in a second, short kernel.  Beside the walkers,
-// in the same launch, the other blocks write the zeros of the rows without a
-// token (most of a vocabulary), found by a 64-way search of the sorted tokens
-// a block.  Sums are fp64, as the hashed table's.
+// a run that crosses chunks leaves a part in each, which a block of the chunk
+// it begins in adds up in a second, short kernel.  Beside the walkers, in the
+// same launch, small blocks write the zeros of the rows without a token (most
+// of a vocabulary), which a mark a row tells apart.  Sums are fp64, as the
+// hashed table's.
 #include "engram_layer_dev.h"
 #include "engram_scatter_dev.h"
 
@@ -28,25 +28,82 @@ namespace {
 constexpr int kEmbedThreads = 256;
 constexpr int kEmbedRows = 4;  // rows of a lane in flight
 
-template <class OUT>
-__device__ __forceinline__ void store8(OUT *row, int64_t chunk, const float (&f)[8]);
-template <>
-__device__ __forceinline__ void store8<uint16_t>(uint16_t *row, int64_t chunk,
-                                                 const float (&f)[8]) {
-  __builtin_nontemporal_store(pack_bf16x8(f), reinterpret_cast<u32x4 *>(row) + chunk);
+// A thread's eight columns: two runs of four, at the quads a and b of the row.
+// Adjacent when what is read and written is bf16 (16 bytes a lane); else a row's
+// lanes apart, so that a wavefront's 16-byte accesses of floats lie side by side
+// (two stores of 16 bytes, 32 apart, write every line twice).  G: the rows read;
+// OUT: those written.
+struct Cols {
+  int64_t a, b;
+  bool on_b;
+};
+template <class G, class OUT>
+constexpr bool kSplitCols = sizeof(G) == 4 || sizeof(OUT) == 4;
+template <class G, class OUT>
+__device__ __forceinline__ Cols cols_of(int64_t base, int lane, int lanes, int64_t quads) {
+  if (!kSplitCols<G, OUT>) return Cols{base + 2 * lane, base + 2 * lane + 1, true};
+  return Cols{base + lane, base + lane + lanes, base + lane + lanes < quads};
 }
-template <>
-__device__ __forceinline__ void store8<float>(float *row, int64_t chunk, const float (&f)[8]) {
-  f32x4 *q = reinterpret_cast<f32x4 *>(row) + 2 * chunk;
-  q[0] = f32x4{f[0], f[1], f[2], f[3]};
-  q[1] = f32x4{f[4], f[5], f[6], f[7]};
+
+__device__ __forceinline__ void store4(uint16_t *row, int64_t quad, const float *f) {
+  __builtin_nontemporal_store(u32x2{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])},
+                              reinterpret_cast<u32x2 *>(row) + quad);
+}
+__device__ __forceinline__ void store4(float *row, int64_t quad, const float *f) {
+  __builtin_nontemporal_store(f32x4{f[0], f[1], f[2], f[3]},
+                              reinterpret_cast<f32x4 *>(row) + quad);
+}
+
+// Eight values of a row that is read, bf16 (uint16_t) or float; row: its first quad.
+template <class G, bool SPLIT>
+struct RowIn;
+template <bool SPLIT>
+struct RowIn<uint16_t, SPLIT> {
+  static constexpr int kAhead = 8;  // rows in flight
+  typedef u32x4 Raw;
+  static __device__ __forceinline__ Raw load(const void *p, int64_t row, const Cols &c) {
+    if (!SPLIT) return static_cast<const u32x4 *>(p)[(row + c.a) / 2];
+    const u32x2 *q = static_cast<const u32x2 *>(p) + row;
+    const u32x2 x = q[c.a], y = q[c.on_b ? c.b : c.a];
+    return u32x4{x.x, x.y, y.x, y.y};
+  }
+  static __device__ __forceinline__ void unpack(const Raw &r, float (&f)[8]) {
+    unpack_bf16x8(r, f);
+  }
+};
+template <bool SPLIT>
+struct RowIn<float, SPLIT> {
+  static constexpr int kAhead = 4;
+  struct Raw {
+    f32x4 a, b;
+  };
+  static __device__ __forceinline__ Raw load(const void *p, int64_t row, const Cols &c) {
+    const f32x4 *q = static_cast<const f32x4 *>(p) + row;
+    return Raw{q[c.a], q[c.on_b ? c.b : c.a]};
+  }
+  static __device__ __forceinline__ void unpack(const Raw &r, float (&f)[8]) {
+    f[0] = r.a.x; f[1] = r.a.y; f[2] = r.a.z; f[3] = r.a.w;
+    f[4] = r.b.x; f[5] = r.b.y; f[6] = r.b.z; f[7] = r.b.w;
+  }
+};
+
+// Writes a thread's eight values.
+template <class G, class OUT>
+__device__ __forceinline__ void store_cols(OUT *row, const Cols &c, const float (&f)[8]) {
+  if constexpr (!kSplitCols<G, OUT>) {
+    __builtin_nontemporal_store(pack_bf16x8(f), reinterpret_cast<u32x4 *>(row) + c.a / 2);
+  } else {
+    store4(row, c.a, f);
+    if (c.on_b) store4(row, c.b, f + 4);
+  }
 }
 
 template <class OUT>
 __global__ __launch_bounds__(kEmbedThreads) void embed_kernel(
-    const int64_t *__restrict__ tokens, int64_t n, const u32x4 *__restrict__ table,
+    const int64_t *__restrict__ tokens, int64_t n, const void *__restrict__ table,
     int64_t table_rows, int64_t chunks, int lanes, float scale, OUT *__restrict__ out,
     int64_t *err) {
+  typedef RowIn<uint16_t, kSplitCols<uint16_t, OUT>> Row;
   const int slots = kEmbedThreads / lanes;
   const int slot = threadIdx.x / lanes, lane = threadIdx.x % lanes;
   const int64_t first = (int64_t)blockIdx.x * slots * kEmbedRows + slot;
@@ -62,11 +119,16 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_kernel(
     }
   }
   count_errors(bad, err);
-  for (int64_t c = lane; c < chunks; c += lanes) {
+  const int64_t quads = chunks * 2;
+  for (int64_t base = 0; base < quads; base += 2 * lanes) {
+    const Cols c = cols_of<uint16_t, OUT>(base, lane, lanes, quads);
+    if (c.a >= quads) break;
     u32x4 v[kEmbedRows];
 #pragma unroll
-    for (int k = 0; k < kEmbedRows; ++k)
-      v[k] = row[k] >= 0 ? table[row[k] * chunks + c] : u32x4{0u, 0u, 0u, 0u};
+    for (int k = 0; k < kEmbedRows; ++k) {
+      v[k] = u32x4{0u, 0u, 0u, 0u};
+      if (row[k] >= 0) v[k] = Row::load(table, row[k] * quads, c);
+    }
 #pragma unroll
     for (int k = 0; k < kEmbedRows; ++k) {
       const int64_t t = first + k * slots;
@@ -75,7 +137,7 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_kernel(
       unpack_bf16x8(v[k], f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = row[k] >= 0 ? f[e] * scale : 0.0f;
-      store8<OUT>(out + t * chunks * 8, c, f);
+      store_cols<uint16_t, OUT>(out + t * chunks * 8, c, f);
     }
   }
 }
@@ -90,6 +152,7 @@ struct EmbedGradArgs {
   double *partials;  // [walks][2][channels]: of the run that enters, that leaves
   int64_t n, chunks, table_rows;
   int64_t walks, walk_len, walk_blocks;
+  const uint8_t *present;  // [table_rows]: rows with a token (n > 0)
   int lanes, rows_per_block;
   float scale;
   void *out;
@@ -101,21 +164,49 @@ __device__ __forceinline__ bool order_holds(const EmbedGradArgs &g) {
   return g.plan == nullptr || g.plan->stalled == 0;
 }
 
+// Which rows have a token: a block takes kMarkRows rows and looks at every
+// token.
+constexpr int kMarkThreads = 1024, kMarkRows = 4096;
+__device__ __forceinline__ void mark_rows(const int64_t *tokens, int64_t n, int64_t table_rows,
+                                          int64_t first, uint32_t *flags, uint8_t *present) {
+  for (int i = threadIdx.x; i < kMarkRows / 4; i += kMarkThreads) flags[i] = 0u;
+  __syncthreads();
+  for (int64_t j = threadIdx.x; j < n; j += kMarkThreads) {
+    const uint64_t r = (uint64_t)tokens[j] - (uint64_t)first;
+    if (r < (uint64_t)kMarkRows) reinterpret_cast<uint8_t *>(flags)[r] = 1;
+  }
+  __syncthreads();
+  // (the array is padded to whole blocks' rows)
+  for (int i = threadIdx.x; i < kMarkRows / 4; i += kMarkThreads)
+    reinterpret_cast<uint32_t *>(present + first)[i] = flags[i];
+}
+
+__global__ __launch_bounds__(kMarkThreads) void embed_mark_kernel(
+    const int64_t *__restrict__ tokens, int64_t n, int64_t table_rows, uint8_t *present) {
+  __shared__ uint32_t flags[kMarkRows / 4];
+  mark_rows(tokens, n, table_rows, (int64_t)blockIdx.x * kMarkRows, flags, present);
+}
+
 // A few thousand tokens are sorted by counting, in one launch: a token's place
 // is the number of smaller ones, and of equal ones before it.  A block places
 // kRankBlock tokens; its threads are kRankBlock tokens wide and share out the
 // tokens to compare with, four at a time from LDS.  n^2 comparisons over the
 // whole GPU beat the sort's passes, which wait on one another, up to
-// kRankTokens.
-constexpr int kRankThreads = 1024, kRankBlock = 16, kRankParts = kRankThreads / kRankBlock;
+// kRankTokens.  The blocks after rank_blocks mark the rows that have a token.
+constexpr int kRankThreads = kMarkThreads, kRankBlock = 16, kRankParts = kRankThreads / kRankBlock;
 constexpr int64_t kRankTokens = 8192;
 
 __global__ __launch_bounds__(kRankThreads) void embed_rank_kernel(
-    const int64_t *__restrict__ tokens, int n, uint32_t table_rows, uint32_t *keys,
-    uint32_t *vals, int64_t *err) {
+    const int64_t *__restrict__ tokens, int n, uint32_t table_rows, uint32_t rank_blocks,
+    uint32_t *keys, uint32_t *vals, uint8_t *present, int64_t *err) {
   __shared__ u32x4 s_key4[kRankTokens / 4];
   __shared__ uint32_t s_count[kRankParts][kRankBlock];
   uint32_t *s_key = reinterpret_cast<uint32_t *>(s_key4);
+  if (blockIdx.x >= rank_blocks) {
+    mark_rows(tokens, n, table_rows, (int64_t)(blockIdx.x - rank_blocks) * kMarkRows, s_key,
+              present);
+    return;
+  }
   const int i0 = blockIdx.x * kRankBlock;
   int bad = 0;
   for (int j = threadIdx.x; j < ((n + 3) & ~3); j += kRankThreads) {
@@ -160,77 +251,64 @@ __global__ __launch_bounds__(kRankThreads) void embed_rank_kernel(
   vals[place] = (uint32_t)i;
 }
 
-template <class OUT, bool ACCUMULATE>
-__device__ __forceinline__ void write_row(const EmbedGradArgs &g, int64_t row, int64_t c,
+template <class G, class OUT, bool ACCUMULATE>
+__device__ __forceinline__ void write_row(const EmbedGradArgs &g, int64_t row, const Cols &c,
                                           const double (&sum)[8]) {
   OUT *dst = static_cast<OUT *>(g.out) + row * g.chunks * 8;
   float f[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) f[e] = (float)(sum[e] * (double)g.scale);
   if (ACCUMULATE) {
-    const float *old = reinterpret_cast<const float *>(dst) + c * 8;
+    const f32x4 *old = reinterpret_cast<const f32x4 *>(dst);
+    const f32x4 x = old[c.a], y = old[c.on_b ? c.b : c.a];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = old[e] + f[e];
+    for (int e = 0; e < 4; ++e) {
+      f[e] = x[e] + f[e];
+      f[4 + e] = y[e] + f[4 + e];
+    }
   }
-  store8<OUT>(dst, c, f);
+  store_cols<G, OUT>(dst, c, f);
 }
 
+// A row of partial sums, in the thread's own order of columns.
+__device__ __forceinline__ f64x2 *part_at(const EmbedGradArgs &g, int64_t walk, int which,
+                                          int64_t quad) {
+  return reinterpret_cast<f64x2 *>(g.partials + (walk * 2 + which) * g.chunks * 8) + quad * 2;
+}
 __device__ __forceinline__ void write_part(const EmbedGradArgs &g, int64_t walk, int which,
-                                           int64_t c, const double (&sum)[8]) {
-  f64x2 *dst = reinterpret_cast<f64x2 *>(g.partials + ((walk * 2 + which) * g.chunks + c) * 8);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) dst[e] = f64x2{sum[2 * e], sum[2 * e + 1]};
+                                           const Cols &c, const double (&sum)[8]) {
+  f64x2 *x = part_at(g, walk, which, c.a);
+  x[0] = f64x2{sum[0], sum[1]};
+  x[1] = f64x2{sum[2], sum[3]};
+  if (!c.on_b) return;
+  x = part_at(g, walk, which, c.b);
+  x[0] = f64x2{sum[4], sum[5]};
+  x[1] = f64x2{sum[6], sum[7]};
 }
 
 // A walker's chunk [a, b) of the sorted positions: its runs' sums.
-// Eight values of a gradient row, bf16 (uint16_t) or float.
-template <class G>
-struct GradRow;
-template <>
-struct GradRow<uint16_t> {
-  static constexpr int kAhead = 8;  // rows in flight
-  typedef u32x4 Raw;
-  static __device__ __forceinline__ Raw load(const void *p, int64_t chunk) {
-    return static_cast<const u32x4 *>(p)[chunk];
-  }
-  static __device__ __forceinline__ void unpack(const Raw &r, float (&f)[8]) {
-    unpack_bf16x8(r, f);
-  }
-};
-template <>
-struct GradRow<float> {
-  static constexpr int kAhead = 4;
-  struct Raw {
-    f32x4 a, b;
-  };
-  static __device__ __forceinline__ Raw load(const void *p, int64_t chunk) {
-    const f32x4 *q = static_cast<const f32x4 *>(p) + 2 * chunk;
-    return Raw{q[0], q[1]};
-  }
-  static __device__ __forceinline__ void unpack(const Raw &r, float (&f)[8]) {
-    f[0] = r.a.x; f[1] = r.a.y; f[2] = r.a.z; f[3] = r.a.w;
-    f[4] = r.b.x; f[5] = r.b.y; f[6] = r.b.z; f[7] = r.b.w;
-  }
-};
-
 template <class G, class OUT, bool ACCUMULATE>
 __device__ void walk_chunk(const EmbedGradArgs &g, int64_t walk, int lane) {
+  typedef RowIn<G, kSplitCols<G, OUT>> Row;
+  constexpr int kAhead = Row::kAhead;
   const int64_t a = walk * g.walk_len, b = min(a + g.walk_len, g.n);
   const uint32_t before = a > 0 ? g.keys[a - 1] : 0xffffffffu;  // no key (they are smaller)
   const uint32_t after = b < g.n ? g.keys[b] : 0xffffffffu;
-  for (int64_t c = lane; c < g.chunks; c += g.lanes) {
+  const int64_t quads = g.chunks * 2;
+  for (int64_t base = 0; base < quads; base += 2 * g.lanes) {
+    const Cols c = cols_of<G, OUT>(base, lane, g.lanes, quads);
+    if (c.a >= quads) break;
     double sum[8] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
     uint32_t run = g.keys[a];
     bool entered = run == before;
-    constexpr int kAhead = GradRow<G>::kAhead;
     for (int64_t i = a; i < b; i += kAhead) {
       uint32_t key[kAhead];
-      typename GradRow<G>::Raw v[kAhead];
+      typename Row::Raw v[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         const int64_t at = min(i + k, b - 1);
         key[k] = g.keys[at];
-        v[k] = GradRow<G>::load(g.grads, (int64_t)g.vals[at] * g.chunks + c);
+        v[k] = Row::load(g.grads, (int64_t)g.vals[at] * quads, c);
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
@@ -240,7 +318,7 @@ __device__ void walk_chunk(const EmbedGradArgs &g, int64_t walk, int lane) {
             if (entered)
               write_part(g, walk, 0, c, sum);
             else
-              write_row<OUT, ACCUMULATE>(g, run, c, sum);
+              write_row<G, OUT, ACCUMULATE>(g, run, c, sum);
           }
           run = key[k];
           entered = false;
@@ -248,7 +326,7 @@ __device__ void walk_chunk(const EmbedGradArgs &g, int64_t walk, int lane) {
           for (int e = 0; e < 8; ++e) sum[e] = 0.0;
         }
         float f[8];
-        GradRow<G>::unpack(v[k], f);
+        Row::unpack(v[k], f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[e] += f[e];
       }
@@ -259,34 +337,14 @@ __device__ void walk_chunk(const EmbedGradArgs &g, int64_t walk, int lane) {
     else if (run == after)
       write_part(g, walk, 1, c, sum);
     else
-      write_row<OUT, ACCUMULATE>(g, run, c, sum);
+      write_row<G, OUT, ACCUMULATE>(g, run, c, sum);
   }
 }
-
-// The first sorted position in [lo, n) whose key is at least `key` (a
-// wavefront together: 64 probes a step).
-__device__ __forceinline__ int64_t lower_bound(const EmbedGradArgs &g, int64_t lo, int64_t key) {
-  int64_t hi = g.n;
-  while (lo < hi) {
-    const int64_t step = (hi - lo + 63) / 64;
-    const int64_t at = lo + ((int64_t)(threadIdx.x & 63) + 1) * step - 1;
-    const bool below = at < hi && (int64_t)g.keys[at] < key;
-    const int64_t passed = __popcll(__ballot(below));  // probes below are the first ones
-    lo = min(lo + passed * step, hi);
-    // the answer is in [lo, lo + step - 1], or the short last part
-    hi = min(lo + step - 1, hi);
-  }
-  return lo;
-}
-
-constexpr int kMaxRowsPerBlock = 256;
 
 // Blocks below walk_blocks walk the sorted tokens; the others write the zeros
 // of the rows without one.
 template <class G, class OUT, bool ACCUMULATE>
 __global__ __launch_bounds__(kEmbedThreads) void embed_grad_kernel(const EmbedGradArgs g) {
-  __shared__ int64_t bound[2];
-  __shared__ uint32_t present[kMaxRowsPerBlock];
   if (!order_holds(g)) return;
   const int slots = kEmbedThreads / g.lanes;
   const int slot = threadIdx.x / g.lanes, lane = threadIdx.x % g.lanes;
@@ -296,27 +354,12 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_grad_kernel(const EmbedGr
     return;
   }
   const int64_t r0 = ((int64_t)blockIdx.x - g.walk_blocks) * g.rows_per_block;
-  const int64_t rows = min((int64_t)g.rows_per_block, g.table_rows - r0);
-  int64_t lo = 0, hi = 0;
-  if (g.n > 0) {
-    const int wave = threadIdx.x / kWave;
-    if (wave < 2) {
-      const int64_t at = lower_bound(g, 0, r0 + (wave == 0 ? 0 : rows));
-      if ((threadIdx.x & 63) == 0) bound[wave] = at;
-    }
-    __syncthreads();
-    lo = bound[0];
-    hi = bound[1];
-  }
-  if (threadIdx.x < rows) present[threadIdx.x] = 0u;
-  __syncthreads();
-  for (int64_t i = lo + threadIdx.x; i < hi; i += kEmbedThreads) present[g.keys[i] - r0] = 1u;
-  __syncthreads();
+  const int64_t end = min(r0 + g.rows_per_block, g.table_rows);
   // 16 bytes a lane, side by side
   const int64_t words = g.chunks * (int64_t)(sizeof(OUT) / 2);
-  for (int64_t r = slot; r < rows; r += slots) {
-    if (present[r] != 0u) continue;
-    u32x4 *row = reinterpret_cast<u32x4 *>(static_cast<OUT *>(g.out) + (r0 + r) * g.chunks * 8);
+  for (int64_t r = r0 + slot; r < end; r += slots) {
+    if (g.present != nullptr && g.present[r] != 0) continue;
+    u32x4 *row = reinterpret_cast<u32x4 *>(static_cast<OUT *>(g.out) + r * g.chunks * 8);
     for (int64_t c = lane; c < words; c += g.lanes)
       __builtin_nontemporal_store(u32x4{0u, 0u, 0u, 0u}, row + c);
   }
@@ -326,7 +369,7 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_grad_kernel(const EmbedGr
 // parts.  It takes up to 64 chunks of 8 channels; its other threads share the
 // parts out, so a frequent token's hundreds of them are on their way together,
 // and their sums are added in order.
-template <class OUT, bool ACCUMULATE>
+template <class G, class OUT, bool ACCUMULATE>
 __global__ __launch_bounds__(kEmbedThreads) void embed_join_kernel(const EmbedGradArgs g,
                                                                    int64_t col_blocks) {
   __shared__ double sums[kEmbedThreads][9];  // (9: rows in other banks)
@@ -344,16 +387,15 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_join_kernel(const EmbedGr
   }
   const int cols = g.lanes < 64 ? g.lanes : 64, parts = kEmbedThreads / cols;
   const int col = threadIdx.x % cols, part = threadIdx.x / cols;
-  const int64_t c = (blockIdx.x % col_blocks) * cols + col;
-  const bool on = c < g.chunks;
+  const int64_t quads = g.chunks * 2, base = (blockIdx.x % col_blocks) * cols * 2;
+  const Cols c = cols_of<G, OUT>(base, col, cols, quads);
+  const bool on = c.a < quads;
   double sum[8] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
   // part 0 begins with the run's first piece, the one that leaves `walk`
   for (int64_t q = walk + part; on && q <= last; q += parts) {
-    const f64x2 *src = reinterpret_cast<const f64x2 *>(g.partials) +
-                       ((q * 2 + (q == walk ? 1 : 0)) * g.chunks + c) * 4;
-    f64x2 v[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = src[e];
+    const f64x2 *x = part_at(g, q, q == walk ? 1 : 0, c.a);
+    const f64x2 *y = part_at(g, q, q == walk ? 1 : 0, c.on_b ? c.b : c.a);
+    const f64x2 v[4] = {x[0], x[1], y[0], y[1]};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       sum[2 * e] += v[e].x;
@@ -367,22 +409,27 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_join_kernel(const EmbedGr
   for (int q = 1; q < parts; ++q)
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[e] += sums[q * cols + col][e];
-  write_row<OUT, ACCUMULATE>(g, run, c, sum);
+  write_row<G, OUT, ACCUMULATE>(g, run, c, sum);
 }
 
-template <class OUT, bool ACCUMULATE>
-void launch_grad(const EmbedGradArgs &g, bool float_grads, unsigned blocks, hipStream_t s) {
+template <class G, class OUT, bool ACCUMULATE>
+void launch_grad(const EmbedGradArgs &g, unsigned blocks, hipStream_t s) {
   const dim3 block(kEmbedThreads);
-  if (float_grads)
-    hipLaunchKernelGGL((embed_grad_kernel<float, OUT, ACCUMULATE>), dim3(blocks), block, 0, s, g);
-  else
-    hipLaunchKernelGGL((embed_grad_kernel<uint16_t, OUT, ACCUMULATE>), dim3(blocks), block, 0, s,
-                       g);
+  hipLaunchKernelGGL((embed_grad_kernel<G, OUT, ACCUMULATE>), dim3(blocks), block, 0, s, g);
   if (g.walks > 1) {
     const int64_t col_blocks = ceil_div(g.chunks, 64);
-    hipLaunchKernelGGL((embed_join_kernel<OUT, ACCUMULATE>), dim3((unsigned)(g.walks * col_blocks)),
-                       block, 0, s, g, col_blocks);
+    hipLaunchKernelGGL((embed_join_kernel<G, OUT, ACCUMULATE>),
+                       dim3((unsigned)(g.walks * col_blocks)), block, 0, s, g, col_blocks);
   }
+}
+template <class G>
+void launch_grad(const EmbedGradArgs &g, const EmbedGradCall &c, unsigned blocks, hipStream_t s) {
+  if (c.accumulate)
+    launch_grad<G, float, true>(g, blocks, s);
+  else if (c.type == ENGRAM_F32)
+    launch_grad<G, float, false>(g, blocks, s);
+  else
+    launch_grad<G, uint16_t, false>(g, blocks, s);
 }
 
 }  // namespace
@@ -396,14 +443,13 @@ int engram::launch_embed(const int64_t *d_tokens, int64_t n, const void *d_table
   const int64_t blocks = ceil_div(n, (int64_t)(kEmbedThreads / lanes) * kEmbedRows);
   if (!grid_fits(blocks, kEmbedThreads)) return ENGRAM_EINVAL;
   const dim3 grid((unsigned)blocks), block(kEmbedThreads);
-  const u32x4 *table = static_cast<const u32x4 *>(d_table);
   if (out_type == ENGRAM_F32)
     hipLaunchKernelGGL(embed_kernel<float>, grid, block, 0, as_stream(stream), d_tokens, n,
-                       table, table_rows, chunks, lanes, scale, static_cast<float *>(d_out),
+                       d_table, table_rows, chunks, lanes, scale, static_cast<float *>(d_out),
                        d_err_count);
   else
     hipLaunchKernelGGL(embed_kernel<uint16_t>, grid, block, 0, as_stream(stream), d_tokens, n,
-                       table, table_rows, chunks, lanes, scale, static_cast<uint16_t *>(d_out),
+                       d_table, table_rows, chunks, lanes, scale, static_cast<uint16_t *>(d_out),
                        d_err_count);
   return launch_status();
 }
@@ -420,41 +466,49 @@ int engram::launch_embed_grad(const EmbedGradCall &c, const Plan &p, void *d_wor
   g.lanes = embed_row_lanes(c.channels);
   g.scale = c.scale;
   g.out = c.grad_table;
-  // about 128 KB of rows a block of zeros
+  // about 8 KB of rows a block of zeros (blocks that end soon keep the stores
+  // that run together on one stretch of memory: 65,536 x 2048 into float 306 us,
+  // with 16 KB 337, with 32 KB 352)
   const int64_t row_bytes = c.channels * (c.type == ENGRAM_F32 ? 4 : 2);
-  g.rows_per_block = 8;
-  while (g.rows_per_block < kMaxRowsPerBlock && g.rows_per_block * row_bytes < (128 << 10))
+  g.rows_per_block = kEmbedThreads / g.lanes;
+  while (g.rows_per_block < 4096 && g.rows_per_block * row_bytes < (8 << 10))
     g.rows_per_block *= 2;
   g.walk_len = embed_chunk(c.n, c.channels);
   g.walks = ceil_div(c.n, g.walk_len);
   g.walk_blocks = ceil_div(g.walks, kEmbedThreads / g.lanes);
   const int64_t zero_blocks = c.accumulate ? 0 : ceil_div(c.table_rows, g.rows_per_block);
   const int64_t blocks = g.walk_blocks + zero_blocks;
+  const int64_t mark_blocks = c.accumulate ? 0 : ceil_div(c.table_rows, kMarkRows);
+  static_assert(kMarkRows == kEmbedMarkRows, "the workspace pads the marks to whole blocks");
   if (!grid_fits(blocks, kEmbedThreads) ||
+      !grid_fits(mark_blocks + kRankTokens / kRankBlock, kRankThreads) ||
       !grid_fits(g.walks * ceil_div(g.chunks, 64), kEmbedThreads))
     return ENGRAM_EINVAL;
   if (c.n > 0) {
     const Views v = views_of(p, d_workspace);
     g.keys = v.sorted_keys;
     g.vals = v.sorted_vals;
+    g.present = c.present;
     if (c.n <= kRankTokens) {
-      hipLaunchKernelGGL(embed_rank_kernel, dim3((unsigned)ceil_div(c.n, kRankBlock)),
+      const int64_t rank_blocks = ceil_div(c.n, kRankBlock);
+      hipLaunchKernelGGL(embed_rank_kernel, dim3((unsigned)(rank_blocks + mark_blocks)),
                          dim3(kRankThreads), 0, st, c.tokens, (int)c.n, (uint32_t)c.table_rows,
-                         const_cast<uint32_t *>(g.keys), const_cast<uint32_t *>(g.vals), c.err);
+                         (uint32_t)rank_blocks, const_cast<uint32_t *>(g.keys),
+                         const_cast<uint32_t *>(g.vals), c.present, c.err);
     } else {
       g.plan = v.scalars;
       const int rc =
           launch_sort_crowded(c.tokens, c.n, c.table_rows, p, d_workspace, c.err, stream);
       if (rc != ENGRAM_OK) return rc;
+      if (mark_blocks > 0)
+        hipLaunchKernelGGL(embed_mark_kernel, dim3((unsigned)mark_blocks), dim3(kMarkThreads), 0,
+                           st, c.tokens, c.n, c.table_rows, c.present);
     }
     if (c.table_rows == 0) return launch_status();
   }
-  const bool wide = c.grads_type == ENGRAM_F32;
-  if (c.accumulate)
-    launch_grad<float, true>(g, wide, (unsigned)blocks, st);
-  else if (c.type == ENGRAM_F32)
-    launch_grad<float, false>(g, wide, (unsigned)blocks, st);
+  if (c.grads_type == ENGRAM_F32)
+    launch_grad<float>(g, c, (unsigned)blocks, st);
   else
-    launch_grad<uint16_t, false>(g, wide, (unsigned)blocks, st);
+    launch_grad<uint16_t>(g, c, (unsigned)blocks, st);
   return launch_status();
 }

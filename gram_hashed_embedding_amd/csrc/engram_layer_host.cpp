@@ -320,6 +320,10 @@ size_t embed_partials(int64_t n, int64_t channels) {
   return (size_t)ceil_div(n, embed_chunk(n, channels)) * 2 * (size_t)channels * 8;
 }
 
+size_t embed_marks(int64_t table_rows) {
+  return (size_t)(ceil_div(table_rows, kEmbedMarkRows) * kEmbedMarkRows);
+}
+
 }  // namespace
 
 extern "C" int engram_embed(const int64_t *d_tokens, int64_t n, const void *d_table,
@@ -338,7 +342,7 @@ extern "C" size_t engram_embed_grad_workspace(int64_t n, int64_t channels, int64
   Plan p;
   if (!embed_sizes_ok(n, channels, table_rows, ENGRAM_F32) || !embed_plan(n, table_rows, &p))
     return (size_t)-1;
-  return p.total + embed_partials(n, channels);
+  return p.total + embed_partials(n, channels) + embed_marks(table_rows);
 }
 
 extern "C" int engram_embed_grad(const int64_t *d_tokens, int64_t n, const void *d_grads,
@@ -355,12 +359,15 @@ extern "C" int engram_embed_grad(const int64_t *d_tokens, int64_t n, const void 
   if (n > 0 && (d_tokens == nullptr || d_grads == nullptr)) return ENGRAM_EINVAL;
   if (any_misaligned({d_grads, d_grad_table})) return ENGRAM_EALIGN;
   if (n > 0 && (d_workspace == nullptr || !aligned16(d_workspace) ||
-                workspace_bytes < p.total + embed_partials(n, channels)))
+                workspace_bytes < engram_embed_grad_workspace(n, channels, table_rows)))
     return ENGRAM_EWORKSPACE;
   if (n == 0 && (accumulate || table_rows == 0)) return ENGRAM_OK;
   double *partials =
       n > 0 ? reinterpret_cast<double *>(static_cast<char *>(d_workspace) + p.total) : nullptr;
+  uint8_t *present =
+      n > 0 ? reinterpret_cast<uint8_t *>(partials) + embed_partials(n, channels) : nullptr;
   const EmbedGradCall c = {d_tokens,   n,          d_grads,    grads_type,   channels, scale,
-                           table_rows, table_type, accumulate, d_grad_table, partials, d_err_count};
+                           table_rows, table_type, accumulate, d_grad_table, partials, present,
+                           d_err_count};
   return launch_embed_grad(c, p, d_workspace, stream);
 }

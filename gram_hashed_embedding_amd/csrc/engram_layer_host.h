@@ -110,6 +110,8 @@ inline int64_t embed_chunk(int64_t n, int64_t channels) {
   return chunk;
 }
 
+constexpr int64_t kEmbedMarkRows = 4096;
+
 struct EmbedGradCall {
   const int64_t *tokens;
   int64_t n;
@@ -121,6 +123,7 @@ struct EmbedGradCall {
   int32_t type, accumulate;
   void *grad_table;
   double *partials;  // [chunks][2][channels]
+  uint8_t *present;  // [table_rows, rounded up to whole kEmbedMarkRows]
   int64_t *err;
 };
 
