@@ -8,7 +8,11 @@
 //
 // Bound by HBM: the encoder reads 2 bytes and writes 1 a value, the decoder
 // the reverse, with about 10 operations between.  A lane moves one chunk of 8
-// channels of each of kActUnroll rows, all loads before the first use.
+// channels of each of kActUnroll blocks, all loads before the first use.
+// Measured on MI355X: 537M values encoded in 281 us (5.8 TB/s), 33.7M decoded in
+// 17.5 us (5.8 TB/s).  1, 2 and 8 blocks a lane were no faster (331, 291 and 288
+// us); non-temporal code stores gained 1% there but cost a decode that follows
+// soon 20%.
 #include "engram_layer_dev.h"
 
 namespace engram {
