@@ -9,8 +9,8 @@
 // floor is one write of the whole table beside one read of the tokens'
 // gradients, and most rows of a vocabulary have no token in a batch.
 //
-// The gradient.  The tokens are sorted as the hashed rows are (the plan of
-// engram_sort.hip), so a row's terms are one run of the sorted order and no
+// The gradient.  The tokens are sorted (by counting, many of them by the passes
+// of engram_sort.hip), so a row's terms are one run of the sorted order and no
 // atomic is needed: the result does not depend on timing, and each row is
 // written once.  Walkers take equal chunks of the sorted positions, however
 // the tokens crowd: a run inside a chunk is summed and written by its walker;
@@ -22,10 +22,10 @@
 //
 // Measured on MI355X, 151,936 rows, tokens of Zipf exponent 1.1: 65,536 x 2048
 // looked up in 53.7 us (6.0 TB/s; into floats 92 us, 6.4 TB/s); the gradient of
-// as many into floats 309 us, of which the sort takes about 45 us, the walkers
-// and zeros 250 us (6.1 TB/s), the join 11 us; of 4099 x 1024 into bf16 61 us
-// (counting and marks 7, walkers and zeros 45, join 6).  More and shorter chunks
-// were slower (at most 64 positions: 362 us, 32: 388, against 306 then at 128).
+// as many into floats 290 us, of which sorting takes 35, marks 7, the walkers and
+// zeros 228 (7.0 TB/s) and the join 8; of 4099 x 1024 into bf16 59 us (counting
+// and marks 6, walkers and zeros 49, join 5).  More and shorter chunks were
+// slower (at most 64 positions: 362 us, 32: 388, against 306 then at 128).
 #include "engram_layer_dev.h"
 #include "engram_scatter_dev.h"
 
@@ -205,50 +205,61 @@ __device__ __forceinline__ void mark_rows(const int64_t *tokens, int64_t n, int6
     reinterpret_cast<uint32_t *>(present + first)[i] = flags[i];
 }
 
-// A few thousand tokens are sorted by counting, in one launch: a token's place
-// is the number of smaller ones, and of equal ones before it.  A block places
-// kRankBlock tokens; its threads are kRankBlock tokens wide and share out the
-// tokens to compare with, four at a time from LDS.  n^2 comparisons over the
-// whole GPU beat the sort's passes, which wait on one another, up to
-// kRankTokens.  The blocks after rank_blocks mark the rows that have a token.
-constexpr int kRankThreads = kMarkThreads, kRankBlock = 16, kRankParts = kRankThreads / kRankBlock;
-constexpr int64_t kRankTokens = 8192;
+// Tokens are sorted by counting, a piece of at most kRankTokens at a time: a
+// token's place in its piece is the number of smaller ones, and of equal ones
+// before it.  A block places BLOCK tokens; its threads are BLOCK tokens wide and
+// share out the piece's tokens to compare with, four at a time from LDS.  A few
+// thousand tokens are one piece: one launch, in which the blocks after
+// rank_blocks mark the rows that have a token.  More are pieces of kPieceTokens,
+// merged by embed_merge_kernel: up to kMergeTokens the comparisons and searches,
+// spread over the whole GPU, beat the sort's passes, which wait on one another
+// (the whole gradient at 256 channels: 9000 tokens 44 us against 60 with the
+// passes, 20,000 52 and 67, 65,536 81 and 89, 90,000 107 and 86).
+constexpr int kRankThreads = kMarkThreads;
+constexpr int64_t kRankTokens = 8192, kPieceTokens = 2048, kMergeTokens = 65536;
+constexpr int kRankBlock = 16, kPieceBlock = 64;
 
+template <int BLOCK>
 __global__ __launch_bounds__(kRankThreads) void embed_rank_kernel(
-    const int64_t *__restrict__ tokens, int n, uint32_t table_rows, uint32_t rank_blocks,
-    uint32_t *keys, uint32_t *vals, uint8_t *present, int64_t *err) {
+    const int64_t *__restrict__ tokens, int64_t n, int piece, uint32_t table_rows,
+    uint32_t rank_blocks, uint32_t *keys, uint32_t *vals, uint8_t *present, int64_t *err) {
+  constexpr int kParts = kRankThreads / BLOCK;
   __shared__ u32x4 s_key4[kRankTokens / 4];
-  __shared__ uint32_t s_count[kRankParts][kRankBlock];
+  __shared__ uint32_t s_count[kParts][BLOCK];
   uint32_t *s_key = reinterpret_cast<uint32_t *>(s_key4);
   if (blockIdx.x >= rank_blocks) {
     mark_rows(tokens, n, (int64_t)(blockIdx.x - rank_blocks) * kMarkRows, s_key, present);
     return;
   }
-  const int i0 = blockIdx.x * kRankBlock;
+  // this block's piece of the tokens (a whole number of blocks long), and the
+  // first token of the piece that it places
+  const int64_t start = (int64_t)blockIdx.x * BLOCK / piece * piece;
+  const int i0 = (int)((int64_t)blockIdx.x * BLOCK - start);
+  const int len = (int)min((int64_t)piece, n - start);
   int bad = 0;
-  for (int j = threadIdx.x; j < ((n + 3) & ~3); j += kRankThreads) {
+  for (int j = threadIdx.x; j < ((len + 3) & ~3); j += kRankThreads) {
     uint32_t k = 0xffffffffu;  // past the end: above every key
-    if (j < n) {
-      const int64_t t = tokens[j];
+    if (j < len) {
+      const int64_t t = tokens[start + j];
       const bool ok = t >= 0 && t < (int64_t)table_rows;
       k = ok ? (uint32_t)t : table_rows;
-      bad += !ok && t != -1 && j >= i0 && j < i0 + kRankBlock ? 1 : 0;
+      bad += !ok && t != -1 && j >= i0 && j < i0 + BLOCK ? 1 : 0;
     }
     s_key[j] = k;
   }
   count_errors(bad, err);
   __syncthreads();
-  const int lane = threadIdx.x % kRankBlock, part = threadIdx.x / kRankBlock;
+  const int lane = threadIdx.x % BLOCK, part = threadIdx.x / BLOCK;
   const int i = i0 + lane;
-  const uint32_t key = i < n ? s_key[i] : 0u;
-  const int quads = (n + 3) / 4;
+  const uint32_t key = i < len ? s_key[i] : 0u;
+  const int quads = (len + 3) / 4;
   uint32_t count = 0;
-  // the block's own tokens lie in quads [i0 / 4, i0 / 4 + kRankBlock / 4)
-  for (int q = part; q < quads; q += kRankParts) {
+  // the block's own tokens lie in quads [i0 / 4, i0 / 4 + BLOCK / 4)
+  for (int q = part; q < quads; q += kParts) {
     const u32x4 k = s_key4[q];
     if (q < i0 / 4) {
       count += (k.x <= key) + (k.y <= key) + (k.z <= key) + (k.w <= key);
-    } else if (q >= i0 / 4 + kRankBlock / 4) {
+    } else if (q >= i0 / 4 + BLOCK / 4) {
       count += (k.x < key) + (k.y < key) + (k.z < key) + (k.w < key);
     } else {
 #pragma unroll
@@ -260,13 +271,71 @@ __global__ __launch_bounds__(kRankThreads) void embed_rank_kernel(
   }
   s_count[part][lane] = count;
   __syncthreads();
-  if (threadIdx.x >= kRankBlock || i >= n) return;
+  if (threadIdx.x >= BLOCK || i >= len) return;
   uint32_t place = 0;
 #pragma unroll
-  for (int p = 0; p < kRankParts; ++p) place += s_count[p][lane];
-  keys[place] = key;
-  vals[place] = (uint32_t)i;
+  for (int p = 0; p < kParts; ++p) place += s_count[p][lane];
+  keys[start + place] = key;
+  vals[start + place] = (uint32_t)(start + i);
 }
+
+// Sorted pieces into one order: a token's place is its place in its piece, plus
+// the tokens not above it in the pieces before and those below it in the pieces
+// after, by binary search.  A block takes 64 tokens of a piece; its 8 wavefronts
+// share out the other pieces, kMergeAhead searches at a time.
+constexpr int kMergeThreads = 512, kMergeAhead = 4;
+__global__ __launch_bounds__(kMergeThreads) void embed_merge_kernel(
+    const uint32_t *__restrict__ in_keys, const uint32_t *__restrict__ in_vals, int64_t n,
+    uint32_t *keys, uint32_t *vals) {
+  __shared__ uint32_t s_count[kMergeThreads / kWave][kWave];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x / kWave;
+  const int64_t at = (int64_t)blockIdx.x * kWave + lane;
+  const bool on = at < n;
+  const uint32_t key = in_keys[on ? at : 0];
+  const int own = (int)((int64_t)blockIdx.x * kWave / kPieceTokens);
+  const int pieces = (int)((n + kPieceTokens - 1) / kPieceTokens);
+  uint32_t count = 0;
+  for (int p0 = wave * kMergeAhead; p0 < pieces; p0 += kMergeThreads / kWave * kMergeAhead) {
+    uint32_t low[kMergeAhead], size[kMergeAhead];
+    const uint32_t *piece[kMergeAhead];
+    uint32_t bound[kMergeAhead];  // counted are the keys below it
+#pragma unroll
+    for (int k = 0; k < kMergeAhead; ++k) {
+      const int p = p0 + k;
+      const bool other = p < pieces && p != own;
+      const int64_t start = (int64_t)(other ? p : 0) * kPieceTokens;
+      piece[k] = in_keys + start;
+      low[k] = 0;
+      size[k] = other ? (uint32_t)min(kPieceTokens, n - start) : 0u;
+      bound[k] = p < own ? key + 1 : key;  // (keys are below 2^32 - 1)
+    }
+    // halves of [low, low + size) that hold the first key not below the bound
+#pragma unroll 1
+    for (int step = 0; step < 12; ++step) {
+#pragma unroll
+      for (int k = 0; k < kMergeAhead; ++k) {
+        const uint32_t half = size[k] / 2;
+        const bool below = size[k] > 0 && piece[k][low[k] + half] < bound[k];
+        low[k] += below ? half + 1 : 0u;
+        size[k] = below ? size[k] - half - 1 : half;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kMergeAhead; ++k) count += low[k];
+  }
+  s_count[wave][lane] = count;
+  __syncthreads();
+  if (wave != 0 || !on) return;
+  uint32_t place = (uint32_t)(at - (int64_t)own * kPieceTokens);
+#pragma unroll
+  for (int w = 0; w < kMergeThreads / kWave; ++w) place += s_count[w][lane];
+  keys[place] = key;
+  vals[place] = in_vals[at];
+}
+static_assert(kPieceTokens == 1 << 11, "12 halvings empty a piece");
+static_assert(kPieceTokens % kPieceBlock == 0 && kPieceTokens % kWave == 0 &&
+                  kPieceTokens <= kRankTokens && kRankTokens % kRankBlock == 0,
+              "blocks do not straddle pieces");
 
 template <class G, class OUT, bool ACCUMULATE>
 __device__ __forceinline__ void write_row(const EmbedGradArgs &g, int64_t row, const Cols &c,
@@ -407,11 +476,13 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_join_kernel(const EmbedGr
   const int64_t quads = g.chunks * 2, base = (blockIdx.x % col_blocks) * cols * 2;
   const Cols c = cols_of<G, OUT>(base, col, cols, quads);
   const bool on = c.a < quads;
+  const int64_t qa = on ? c.a : 0, qb = on && c.on_b ? c.b : qa;
   double sum[8] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
   // part 0 begins with the run's first piece, the one that leaves `walk`
-  for (int64_t q = walk + part; on && q <= last; q += parts) {
-    const f64x2 *x = part_at(g, q, q == walk ? 1 : 0, c.a);
-    const f64x2 *y = part_at(g, q, q == walk ? 1 : 0, c.on_b ? c.b : c.a);
+#pragma unroll 4
+  for (int64_t q = walk + part; q <= last; q += parts) {
+    const f64x2 *x = part_at(g, q, q == walk ? 1 : 0, qa);
+    const f64x2 *y = part_at(g, q, q == walk ? 1 : 0, qb);
     const f64x2 v[4] = {x[0], x[1], y[0], y[1]};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -507,17 +578,30 @@ int engram::launch_embed_grad(const EmbedGradCall &c, const Plan &p, void *d_wor
     g.keys = v.sorted_keys;
     g.vals = v.sorted_vals;
     g.present = c.present;
+    uint32_t *keys = const_cast<uint32_t *>(g.keys), *vals = const_cast<uint32_t *>(g.vals);
     if (c.n <= kRankTokens) {
       const int64_t rank_blocks = ceil_div(c.n, kRankBlock);
-      hipLaunchKernelGGL(embed_rank_kernel, dim3((unsigned)(rank_blocks + mark_blocks)),
-                         dim3(kRankThreads), 0, st, c.tokens, (int)c.n, (uint32_t)c.table_rows,
-                         (uint32_t)rank_blocks, const_cast<uint32_t *>(g.keys),
-                         const_cast<uint32_t *>(g.vals), c.present, c.err);
+      hipLaunchKernelGGL(embed_rank_kernel<kRankBlock>,
+                         dim3((unsigned)(rank_blocks + mark_blocks)), dim3(kRankThreads), 0, st,
+                         c.tokens, c.n, (int)kRankTokens, (uint32_t)c.table_rows,
+                         (uint32_t)rank_blocks, keys, vals, c.present, c.err);
     } else {
-      g.plan = v.scalars;
-      const int rc =
-          launch_sort_crowded(c.tokens, c.n, c.table_rows, p, d_workspace, c.err, stream);
-      if (rc != ENGRAM_OK) return rc;
+      if (c.n <= kMergeTokens) {
+        uint32_t *piece_keys = keys == v.keys_a ? v.keys_b : v.keys_a;
+        uint32_t *piece_vals = vals == v.vals_a ? v.vals_b : v.vals_a;
+        const int64_t rank_blocks = ceil_div(c.n, kPieceBlock);
+        hipLaunchKernelGGL(embed_rank_kernel<kPieceBlock>, dim3((unsigned)rank_blocks),
+                           dim3(kRankThreads), 0, st, c.tokens, c.n, (int)kPieceTokens,
+                           (uint32_t)c.table_rows, (uint32_t)rank_blocks, piece_keys, piece_vals,
+                           nullptr, c.err);
+        hipLaunchKernelGGL(embed_merge_kernel, dim3((unsigned)ceil_div(c.n, kWave)),
+                           dim3(kMergeThreads), 0, st, piece_keys, piece_vals, c.n, keys, vals);
+      } else {
+        g.plan = v.scalars;
+        const int rc =
+            launch_sort_crowded(c.tokens, c.n, c.table_rows, p, d_workspace, c.err, stream);
+        if (rc != ENGRAM_OK) return rc;
+      }
       if (mark_blocks > 0)
         hipLaunchKernelGGL(embed_mark_kernel,
                            dim3((unsigned)ceil_div(c.table_rows, kEmbedThreads)),

@@ -90,7 +90,7 @@ def test_float_gradients(n, rows, channels, hot, dtype):
     assert np.array_equal(ref.f64(got), want)
 
 
-@pytest.mark.parametrize("n", [128, 1000, 20000, 70000])
+@pytest.mark.parametrize("n", [128, 1000, 8192, 8193, 20000, 65536, 65537, 70000])
 @pytest.mark.parametrize("hot", [0.3, 0.95, 1.0])
 @pytest.mark.parametrize("channels", [8, 264])
 def test_frequent_tokens(n, hot, channels):
