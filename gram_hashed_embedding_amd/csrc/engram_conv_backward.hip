@@ -310,14 +310,11 @@ __global__ __launch_bounds__(kConvBlock) void conv_backward_k4_kernel(const Conv
   int64_t t0 = p.last - T;
   if (p.halo) {  // a few positions: each tile loads its whole window
     for (;; t0 -= T) {
-      XRow xr[T];
+      XRow xr[T] = {};
 #pragma unroll
-      for (int i = 0; i < T + H; ++i)
+      for (int i = 0; i < T + H; ++i) {
         win[i] = (g + min(max(t0 + i, (int64_t)0), a.seq - 1) * a.quads)[p.lane];
-#pragma unroll
-      for (int i = 0; i < T; ++i) {
-        xr[i] = XRow{u32x2{0u, 0u}, 0.0f};
-        if (WANT_W) xr[i] = load_halo(a, p, max(t0 + i, p.first));
+        if (WANT_W && i < T) xr[i] = load_halo(a, p, max(t0 + i, p.first));
       }
       const uint64_t begins = begins_mask(a, load_seg(a, p.b, t0), t0);
       conv_tile<D, T, CODES, WANT_W, kHalo>(a, p, t0, begins, win, xr, w, sum_w, sum_b);
@@ -335,13 +332,12 @@ __global__ __launch_bounds__(kConvBlock) void conv_backward_k4_kernel(const Conv
   // their values are not used.  The next tile's are loaded while one is worked on
   // (after the last, the first rows once more).
   u32x2 next_g[T];
-  XRow next_x[T];
+  XRow next_x[T] = {};
   auto load_tile = [&](int64_t at) {
 #pragma unroll
     for (int i = 0; i < T; ++i) {
       const int64_t t = max(at + i, p.first);
       next_g[i] = (g + t * a.quads)[p.lane];
-      next_x[i] = XRow{u32x2{0u, 0u}, 0.0f};
       if (WANT_W) next_x[i] = load_x<CODES>(a, p, t, scale_at);
     }
   };
@@ -368,7 +364,7 @@ __global__ __launch_bounds__(kConvBlock) void conv_backward_k4_kernel(const Conv
     if (t0 <= p.first) break;
     t0 -= T;
     // the rows ahead of the next tile are this window's first H
-#pragma unroll
+    // (the compiler makes it a move of its own, which it then splits into registers)
     for (int i = H - 1; i >= 0; --i) win[T + i] = win[i];
   }
   if constexpr (WANT_W) store_sums<K>(a, p, sum_w, sum_b);

@@ -139,6 +139,12 @@ int launch_conv_step(const ConvStepCall &c, void *stream);
 int launch_embed(const int64_t *d_tokens, int64_t n, const void *d_table, int64_t table_rows,
                  int64_t channels, float scale, int32_t out_type, void *d_out,
                  int64_t *d_err_count, void *stream);
+// launch_plan's sort for ids that crowd together (a vocabulary's frequent
+// tokens have neighbouring ids): every digit in a pass of its own, none left to
+// buckets of the top digit, which one block would sort nearly whole.  It leaves
+// the sorted keys and positions and the stall flag; no slots, no stamp.
+int launch_sort_crowded(const int64_t *d_row_ids, int64_t n, int64_t table_rows, const Plan &p,
+                        void *d_workspace, int64_t *d_err_count, void *stream);
 int launch_embed_grad(const EmbedGradCall &c, const Plan &p, void *d_workspace, void *stream);
 
 }  // namespace engram

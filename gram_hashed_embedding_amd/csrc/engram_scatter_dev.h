@@ -45,13 +45,6 @@ inline Views views_of(const Plan &p, void *ws) {
   return v;
 }
 
-// launch_plan's sort for ids that crowd together (a vocabulary's frequent
-// tokens have neighbouring ids): every digit in a pass of its own, none left to
-// buckets of the top digit, which one block would sort nearly whole.  It leaves
-// the sorted keys and positions and the stall flag; no slots, no stamp.
-int launch_sort_crowded(const int64_t *d_row_ids, int64_t n, int64_t table_rows, const Plan &p,
-                        void *d_workspace, int64_t *d_err_count, void *stream);
-
 // Add `mark` to *err once (when err is not null).
 __device__ __forceinline__ void add_mark(int64_t *err, int64_t mark) {
   if (err != nullptr)

@@ -36,6 +36,7 @@
 //     and table_rows; the apply checks the stamp (and that no wait of the
 //     plan expired) before it reads the plan.
 #include "engram_hash_dev.h"
+#include "engram_layer_host.h"
 #include "engram_scatter_dev.h"
 
 namespace engram {
@@ -1042,14 +1043,13 @@ void launch_pass(int src, const SortLayout &L, const PassArgs &a, hipStream_t s)
 }  // namespace
 }  // namespace engram
 
-// Plan: sort the row ids and give every distinct row its slot (U and the
-// plan's stamp are left in the workspace scalars).  Needs only the ids: given (ids), or computed
-// from the tokens (hp, when ids is null).
 namespace engram {
 namespace {
 
-// The plan; id_buckets: whether given ids may take the one-pass bucket sort;
-// slots: whether the distinct rows' slots are wanted (and the plan's stamp).
+// Plan: sort the row ids and give every distinct row its slot (U and the
+// plan's stamp are left in the workspace scalars).  Needs only the ids: given (ids), or computed
+// from the tokens (hp, when ids is null).  id_buckets: whether given ids may take
+// the one-pass bucket sort; slots: whether the slots (and the stamp) are wanted.
 int plan_of(const int64_t *ids, const HashParams *hp, int64_t n, int64_t table_rows,
             const Plan &p, void *ws, int64_t *err, void *stream, bool id_buckets, bool slots) {
   hipStream_t s = as_stream(stream);

@@ -245,6 +245,9 @@ int engram_ple_conv_step(const void *d_x, void *d_ring, int64_t ring_count, int6
  *   counted); d_grads [n, channels] of grads_type; d_grad_table [table_rows,
  *   channels] of table_type (accumulate: fp32 only).  table_rows < 2^32 - 1, n < 2^32 - 1.
  *   The workspace holds engram_embed_grad_workspace bytes, 16-byte aligned.
+ *   More than 65,536 tokens are sorted with engram.h's bounded waits: should
+ *   one expire, ENGRAM_ERR_STALLED is added to *d_err_count (when not NULL) and
+ *   nothing is written.
  * Errors: EINVAL, EALIGN, EWORKSPACE.  n == 0 writes zeros (accumulate:
  * nothing).
  */
