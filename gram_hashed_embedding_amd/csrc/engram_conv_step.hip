@@ -39,7 +39,9 @@ __global__ __launch_bounds__(kStepThreads) void conv_step_kernel(const StepArgs 
   if (i >= a.batch * a.chunks) return;
   const int64_t b = i / a.chunks, ch = i - b * a.chunks;
   const int64_t id = a.ring_ids != nullptr ? a.ring_ids[b] : b, pos = a.positions[b];
-  const bool ok = id >= 0 && id < a.ring_count && pos >= 0;
+  // (a position whose tokens would pass the largest number is as invalid)
+  const bool ok =
+      id >= 0 && id < a.ring_count && pos >= 0 && pos <= INT64_MAX - a.tokens;
   if (!ok) {
     if (ch == 0 && id != -1) count_errors(1, a.err);
     if (a.out != nullptr)

@@ -210,10 +210,11 @@ int engram_ple_conv_backward(const void *d_grad_out, const void *d_x, const int8
  *   d_ring bf16 [ring_count, ring_rows, channels], updated in place.
  *     ring_rows >= (K-1)*dilation, and at least 1.  A ring with further rows
  *     can take `tokens` back: positions that have not been overwritten stay.
- *   d_positions int64 [batch]; a negative position is an invalid entry.
+ *   d_positions int64 [batch]; a negative position, or one above INT64_MAX -
+ *     tokens, is an invalid entry.
  *   d_ring_ids int64 [batch], the ring of each sequence, distinct, or NULL
  *     (ring b).  -1 marks an unused entry: its outputs are zero, no ring is
- *     touched.  Any other id outside [0, ring_count), and a negative position,
+ *     touched.  Any other id outside [0, ring_count), and an invalid position,
  *     is treated the same and adds one to *d_err_count (when not NULL).
  *     Repeated ids race on the one ring's contents (in bounds).
  *   d_weight, d_bias, kernel_size, dilation as for engram_ple_conv.

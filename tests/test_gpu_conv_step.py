@@ -84,6 +84,21 @@ def test_slots_positions_and_unused_entries():
         assert torch.equal(ring[s], before[s])
 
 
+@pytest.mark.parametrize("pos", [2 ** 63 - 1, 2 ** 63 - 3, 2 ** 63 - 4, -1, -2 ** 63])
+def test_positions_out_of_range(pos):
+    """Positions whose tokens would pass the largest number touch nothing and are counted; the
+    last ones that do not are as good as any."""
+    x, w, bias = setup(2, 3, 16, 4, 70)
+    ring = garbage(2, 8, 16)
+    err = torch.zeros(1, dtype=torch.int64, device="cuda")
+    at = torch.tensor([pos, 2 ** 63 - 1 - 3], device="cuda")
+    out = L.engram_ple_conv_step(x, ring, w, 2, at, bias=bias, err_count=err)
+    good = pos == 2 ** 63 - 1 - 3
+    assert int(err) == (0 if good else 1)
+    assert bool(torch.isnan(ring[0]).all()) != good and not bool(torch.isnan(ring[1]).all())
+    assert good or bool((out[0] == 0).all())
+
+
 def test_tokens_taken_back():
     """With rows to spare, drafted tokens are overwritten by the accepted ones."""
     B, C, d = 2, 16, 3
