@@ -161,8 +161,25 @@ __device__ __forceinline__ uint64_t begins_mask(const ConvBackArgs &a, const Seg
   return __ballot(pos >= a.seq || (a.seg != nullptr && pos > -a.halo_len && s.here != s.before));
 }
 
+// The first position after `at` (of the slice's last position) where a segment
+// begins or the row ends, or one past `reach` positions ahead if none does
+// before; 64 positions a step, the same in every lane of the wave.
+__device__ __forceinline__ int64_t run_end(const ConvBackArgs &a, const int64_t *seg, int64_t at,
+                                           int64_t reach) {
+  const int64_t end = min(a.seq, at + reach + 1);
+  if (seg == nullptr) return end;
+  for (int64_t from = at + 1; from < end; from += kWave) {
+    const int64_t pos = from + (threadIdx.x & 63);
+    const int64_t at_most = min(pos, end - 1);
+    const uint64_t begins = __ballot(pos < end && seg[at_most] != seg[at_most - 1]);
+    if (begins != 0) return from + __builtin_ctzll(begins);
+  }
+  return end;
+}
+
 // Any K up to kConvMaxKernel and any dilation: the same walk, each row of g
-// read from memory and each pair tested against the segment ids.
+// read from memory.  `limit` is where the pairs of a position end: the next
+// place a segment begins, which only moves down as the walk does.
 template <bool CODES>
 __global__ __launch_bounds__(kConvBlock) void conv_backward_generic_kernel(const ConvBackArgs a) {
   const uint32_t unit = blockIdx.x * kConvWaves + threadIdx.x / kWave;
@@ -173,17 +190,15 @@ __global__ __launch_bounds__(kConvBlock) void conv_backward_generic_kernel(const
       a.seg != nullptr ? a.seg + p.b * (a.halo_len + a.seq) + a.halo_len : nullptr;
   const int64_t quad = p.quad0 + p.lane;
   const u32x2 *g = a.g + p.b * a.seq * a.quads + quad;
-  // one tap at a time for the weight's sums, so that K stays a run-time number
+  const int64_t end = run_end(a, seg, p.last - 1, (int64_t)(a.K - 1) * a.dil);
   float sum_b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  int64_t limit = end;
   for (int64_t t = p.last - 1; t >= p.first; --t) {
+    if (seg != nullptr && t + 1 < p.last && seg[t + 1] != seg[t]) limit = t + 1;
     float dx[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    int64_t reach = t;  // pairs up to here have been tested
     for (int j = 0; j < a.K; ++j) {
       const int64_t q = t + (int64_t)j * a.dil;
-      if (q >= a.seq) break;
-      bool ok = true;
-      for (; ok && seg != nullptr && reach < q; ++reach) ok = seg[reach] == seg[reach + 1];
-      if (!ok) break;
+      if (q >= limit) break;
       if (q < 0) continue;
       float v[4];
       unpack4(g[q * a.quads], v);
@@ -198,15 +213,15 @@ __global__ __launch_bounds__(kConvBlock) void conv_backward_generic_kernel(const
   if (a.partials == nullptr) return;
   f32x4 *dst = reinterpret_cast<f32x4 *>(a.partials) +
                (p.b * a.s.slices + p.slice) * (a.K + 1) * a.quads + quad;
+  // one tap at a time for the weight's sums, so that K stays a run-time number
   for (int j = 0; j < a.K && a.want_w; ++j) {
     const int64_t back = (int64_t)j * a.dil;
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    limit = end;
     for (int64_t t = p.last - 1; t >= p.first; --t) {
+      if (seg != nullptr && t + 1 < p.last && seg[t + 1] != seg[t]) limit = t + 1;
       const int64_t q = t + back;
-      if (q >= a.seq || q < 0) continue;
-      bool ok = true;
-      for (int64_t r = t; ok && seg != nullptr && r < q; ++r) ok = seg[r] == seg[r + 1];
-      if (!ok) continue;
+      if (q >= limit || q < 0) continue;
       float v[4], x[4];
       unpack4(g[q * a.quads], v);
       unpack_x<CODES>(p.halo ? load_halo(a, p, t) : load_x<CODES>(a, p, t, scale_at), p.halo, x);
@@ -461,7 +476,7 @@ int engram::launch_conv_backward(const ConvBackwardCall &c, void *stream) {
     const bool codes = c.codes != nullptr;
     // the register-window kernel sums the weight's gradient with the bias's: a
     // bias alone (no x given) takes the plain one
-    if (c.K == 4 && c.dilation <= 8 && (a.want_w || !sums)) {
+    if (conv_windowed(c.K, c.dilation) && (a.want_w || !sums)) {
       if (!sums)
         launch_k4<false, false>(a, grid, st);
       else if (codes)

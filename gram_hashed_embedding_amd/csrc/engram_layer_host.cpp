@@ -61,13 +61,14 @@ ConvBackwardShape conv_backward_shape(int64_t batch, int64_t seq, int64_t halo_l
   s.quads = channels / 4;
   s.groups = ceil_div(s.quads, 64);
   // about 2048 waves, as many as stay on 256 CUs at a time (8 each); a slice not
-  // so short that the rows it reads past its end outweigh its own
+  // so short that the rows it reads past its end (the register window's) outweigh
+  // its own, nor so long that its fp32 sums lose bits
   const int64_t want = ceil_div(2048, (batch > 0 ? batch : 1) * s.groups);
-  const int64_t least = 32 > 2 * (int64_t)(K - 1) * dilation ? 32 : 2 * (int64_t)(K - 1) * dilation;
+  const int64_t ahead = conv_windowed(K, dilation) ? (int64_t)(K - 1) * dilation : 0;
+  const int64_t least = 2 * ahead > 32 ? 2 * ahead : 32;
   s.slice = ceil_div(seq > 0 ? seq : 1, want);
   if (s.slice < least) s.slice = least;
-  // nor so long that its fp32 sums lose bits
-  if (s.slice > kConvMaxSlice && least <= kConvMaxSlice) s.slice = kConvMaxSlice;
+  if (s.slice > kConvMaxSlice) s.slice = kConvMaxSlice;
   s.halo_slices = ceil_div(halo_len, s.slice);
   s.slices = s.halo_slices + ceil_div(seq, s.slice);
   return s;

@@ -58,6 +58,8 @@ inline int64_t norm_partial_floats(const NormShape &s) { return s.rowblocks * 2 
 // halo_slices slices) or of its sequence.  Each leaves kernel_size + 1 fp32
 // sums a channel.
 constexpr int64_t kConvMaxSlice = 1024;
+// The shapes of the register-window kernel.
+inline bool conv_windowed(int32_t K, int32_t dilation) { return K == 4 && dilation <= 8; }
 struct ConvBackwardShape {
   int64_t quads, groups, slice, halo_slices, slices;  // slices: a row's, the halo's included
 };

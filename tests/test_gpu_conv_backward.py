@@ -83,6 +83,14 @@ def test_other_kernel_sizes(K, d, codes):
     check(2, 60, 16, K, d, K * 31 + d, halo_len=5, seg_mean=9, codes=codes)
 
 
+@pytest.mark.parametrize("K,d,S,halo_len,seg_mean", [(3, 300, 1500, 0, 700), (2, 70, 2300, 90, 90),
+                                                     (4, 9, 1200, 27, 40), (3, 2000, 1500, 0, 300),
+                                                     (2, 1, 70, 200, None)])
+def test_other_shapes_over_many_slices(K, d, S, halo_len, seg_mean):
+    """Taps that reach past slices and boundaries, and a halo of several slices."""
+    check(1, S, 8, K, d, K + d, halo_len=halo_len, seg_mean=seg_mean)
+
+
 @pytest.mark.parametrize("C,width", [(512, 64), (400, 200), (1024, 256)])
 def test_codes_of_groups(C, width):
     """Codes made group by group (as the norm before the convolution makes them)."""
