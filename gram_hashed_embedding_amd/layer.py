@@ -182,6 +182,8 @@ def engram_residual_norm(residual, y=None, *, gate=None, w_post=None, scale=None
     yc = ys = nc = ns = None
     if y is not None:
         y_p = _tensor(y, bf, n, "y", index)
+        if y.shape != residual.shape:
+            raise ValueError("y must have the residual's shape")
         if out is None:
             out = torch.empty_like(residual)
         out_p = _tensor(out, rt, n, "out", index)
@@ -236,6 +238,8 @@ def engram_residual_norm_backward(grad_out, grad_next=None, *, out=None, rstd_po
     out_p = dn_p = rnext_p = post_p = y_p = yc_p = ys_p = 0
     if w_next is not None:
         dn_p = _tensor(grad_next, bf, n, "grad_next", index)
+        if grad_next.shape != like.shape:
+            raise ValueError("grad_next must have the shape of grad_out (or of out)")
         out_p = _tensor(out, rt, n, "out", index)
         rnext_p = _tensor(rstd_next, f32, stats, "rstd_next", index)
     branch = y is not None or y_codes is not None

@@ -21,6 +21,9 @@ REFUSED = [
     lambda: L.engram_residual_norm(z(4, 64)[:, :32], w_next=z(32)),
     lambda: L.engram_residual_norm(z(4, 32), z(4, 24), w_next=z(32)),
     lambda: L.engram_residual_norm(z(4, 32), z(4, 32).float()),
+    lambda: L.engram_residual_norm(z(4, 32), z(8, 16)),
+    lambda: L.engram_residual_norm_backward(z(4, 32), z(8, 16), out=z(4, 32), w_next=z(32),
+                                            rstd_next=z(4, 1, dtype=torch.float32)),
     lambda: L.engram_residual_norm(z(4, 32), z(4, 32), gate=z(4, 5)),
     lambda: L.engram_residual_norm(z(4, 32), z(4, 32), gate=z(3, 32)),
     lambda: L.engram_residual_norm(z(4, 32), z(4, 32), eps=0.0),
