@@ -559,7 +559,10 @@ int engram::launch_embed_grad(const EmbedGradCall &c, const Plan &p, void *d_wor
   // with 16 KB 337, with 32 KB 352)
   const int64_t row_bytes = c.channels * (c.type == ENGRAM_F32 ? 4 : 2);
   g.rows_per_block = kEmbedThreads / g.lanes;
-  while (g.rows_per_block < 4096 && g.rows_per_block * row_bytes < (8 << 10))
+  // (and not more blocks than a launch holds, for tables past 64 GB)
+  while (g.rows_per_block < (1 << 28) &&
+         ((g.rows_per_block < 4096 && g.rows_per_block * row_bytes < (8 << 10)) ||
+          ceil_div(c.table_rows, g.rows_per_block) > (1 << 23)))
     g.rows_per_block *= 2;
   g.walk_len = embed_chunk(c.n, c.channels);
   g.walks = ceil_div(c.n, g.walk_len);
