@@ -348,8 +348,8 @@ extern "C" size_t engram_embed_grad_workspace(int64_t n, int64_t channels, int64
 
 extern "C" int engram_embed_grad(const int64_t *d_tokens, int64_t n, const void *d_grads,
                                  int32_t grads_type, int64_t channels, float scale,
-                                 int64_t table_rows, int32_t table_type, int32_t accumulate, void *d_grad_table,
-                                 void *d_workspace, size_t workspace_bytes,
+                                 int64_t table_rows, int32_t table_type, int32_t accumulate,
+                                 void *d_grad_table, void *d_workspace, size_t workspace_bytes,
                                  int64_t *d_err_count, void *stream) {
   Plan p;
   if (!embed_sizes_ok(n, channels, table_rows, table_type) || !embed_plan(n, table_rows, &p))

@@ -169,7 +169,7 @@ struct Row<float> {
 };
 
 // A sum over a group's lanes: within a wavefront, or over a block through
-// LDS (kWide: `part` has one slot a wavefront; consecutive calls alternate
+// LDS (`part` has one slot a wavefront; consecutive calls alternate
 // between two sets, so one barrier a call is enough).
 template <int LANES>
 __device__ __forceinline__ float group_sum(float v, float (*part)[16], int set) {
