@@ -169,12 +169,16 @@ struct Row<float> {
 };
 
 // A sum over a group's lanes: within a wavefront, or over a block through
-// LDS (`part` has one slot a wavefront; consecutive calls alternate
-// between two sets, so one barrier a call is enough).
+// LDS (`part` has one slot a wavefront).  One barrier a call is enough because
+// each call takes the other set than the call before it, whichever means the
+// rows have (`set`, alike in the whole block, is carried from call to call and
+// from row to row): a set is written again after the barrier of the call
+// between, which every wavefront reaches after its reads of that set.
 template <int LANES>
-__device__ __forceinline__ float group_sum(float v, float (*part)[16], int set) {
+__device__ __forceinline__ float group_sum(float v, float (*part)[16], int &set) {
   if (LANES <= 64) return lanes_sum<(LANES <= 64 ? LANES : 64)>(v);
   v = lanes_sum<64>(v);
+  set ^= 1;
   if ((threadIdx.x & 63) == 0) part[set][threadIdx.x >> 6] = v;
   __syncthreads();
   float s = 0.0f;
@@ -287,6 +291,7 @@ __device__ __forceinline__ Place place_of(const NormShape &s) {
 template <class RT, int LANES, int ITEMS, int THREADS>
 __global__ __launch_bounds__(THREADS) void norm_forward_kernel(const NormArgs a) {
   __shared__ float part[2][16];
+  int set = 0;  // of part, the last one written
   const Place p = place_of<LANES, THREADS>(a.s);
   const int n = (int)a.s.chunks * 8;
   const int64_t g0 = p.group * n;  // the group's first channel
@@ -336,7 +341,7 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(const NormArgs a)
 #pragma unroll
         for (int e = 0; e < 8; ++e) sq += f[e] * f[e];
       }
-      const float u = 1.0f / sqrtf(group_sum<LANES>(sq, part, 0) * a.inv_n + a.eps);
+      const float u = 1.0f / sqrtf(group_sum<LANES>(sq, part, set) * a.inv_n + a.eps);
       float ag = 1.0f, unused;
       if (a.gate_kind == 1) sigmoid(zg, ag, unused);
       const float ua = u * ag;
@@ -371,7 +376,7 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(const NormArgs a)
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           sq += (e < 4 ? sp[i].on_a : sp[i].on_b) ? o[i][e] * o[i][e] : 0.0f;
-      const float v = 1.0f / sqrtf(group_sum<LANES>(sq, part, 1) * a.inv_n + a.eps);
+      const float v = 1.0f / sqrtf(group_sum<LANES>(sq, part, set) * a.inv_n + a.eps);
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i) {
         float w[8];
@@ -394,6 +399,7 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(const NormArgs a)
 template <class RT, int LANES, int ITEMS, int THREADS>
 __global__ __launch_bounds__(THREADS) void norm_backward_kernel(const NormArgs a) {
   __shared__ float part[2][16];
+  int set = 0;  // of part, the last one written
   __shared__ float sums[THREADS == LANES ? 1 : THREADS * ITEMS * 8];
   const Place p = place_of<LANES, THREADS>(a.s);
   const int n = (int)a.s.chunks * 8;
@@ -458,7 +464,7 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(const NormArgs a
           sum_n[i][e] += g[e] * xh;
         }
       }
-      const float m = group_sum<LANES>(s, part, 0) * a.inv_n;
+      const float m = group_sum<LANES>(s, part, set) * a.inv_n;
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i) {
         float w[8], g[8], x[8];
@@ -509,7 +515,7 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(const NormArgs a
           s += q[i][e] * yh[i][e];
         }
       }
-      s = group_sum<LANES>(s, part, 1);
+      s = group_sum<LANES>(s, part, set);
       const float m = s * a.inv_n;
       if (a.grad_y != nullptr) {
 #pragma unroll
