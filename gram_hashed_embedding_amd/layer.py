@@ -469,7 +469,10 @@ def engram_embed_grad(tokens, grads, table_rows, scale=1.0, grad_table=None,
                       grad_dtype=torch.float32, accumulate=False, workspace=None, err_count=None):
     """The gradient of engram_embed, from grads bf16 or fp32 [..., channels], into the whole
     table [table_rows, channels] (grad_dtype: fp32 or bf16): rows without a token get zeros;
-    with accumulate (fp32, grad_table given) the sums are added to the rows that have tokens."""
+    with accumulate (fp32, grad_table given) the sums are added to the rows that have tokens.
+    Should a bounded wait of the sort (of more than 65,536 tokens) expire, err_count receives
+    ERR_STALLED and the gradient is NaN; accumulated, the table is left as it was, and only
+    err_count tells."""
     device, index = _device_of(grads, "grads")
     n = tokens.numel()
     channels = grads.shape[-1] if grads.dim() else 0

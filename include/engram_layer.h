@@ -247,8 +247,9 @@ int engram_ple_conv_step(const void *d_x, void *d_ring, int64_t ring_count, int6
  *   channels] of table_type (accumulate: fp32 only).  table_rows < 2^32 - 1, n < 2^32 - 1.
  *   The workspace holds engram_embed_grad_workspace bytes, 16-byte aligned.
  *   More than 65,536 tokens are sorted with engram.h's bounded waits: should
- *   one expire, ENGRAM_ERR_STALLED is added to *d_err_count (when not NULL) and
- *   nothing is written.
+ *   one expire, ENGRAM_ERR_STALLED is added to *d_err_count (when not NULL), and
+ *   every value of the table is NaN (accumulate: the table is left as it was,
+ *   so only the counter tells).
  * Errors: EINVAL, EALIGN, EWORKSPACE.  n == 0 writes zeros (accumulate:
  * nothing).
  */

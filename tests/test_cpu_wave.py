@@ -44,3 +44,13 @@ def test_shapes_of_several_rows_a_block(tmp_path):
                                  capture_output=True, text=True).stdout
             lanes, at_once, blocks = map(int, out.split())
             assert lanes > 64 and at_once * blocks < rows, (way, rows, channels, out)
+
+
+def test_embedding_gradient_of_a_stalled_sort(tmp_path):
+    """A sort whose wait expired leaves NaN in a gradient, not what the memory held, whether or
+    not the caller counts errors."""
+    exe = build(tmp_path, "embed_stall", os.path.join(CSRC, "engram_host.cpp"),
+                os.path.join(ROOT, "tests", "host_launch_stub.cpp"))
+    res = subprocess.run([exe], capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0, res.stdout + res.stderr
+    assert res.stdout.count(": ok") == 6
