@@ -56,6 +56,19 @@ def _optional(t, dtype, numel, what, index):
     return 0 if t is None else _tensor(t, dtype, numel, what, index)
 
 
+def _check_rows(t, lead, widths, what):
+    """Raises when `t`, which has the right number of values, has them in another order of axes:
+    it keeps the axes `lead` in front, or is flattened to rows of one of `widths` or to one axis
+    (or the rows of `lead` are one axis themselves).  Axes of one do not count."""
+    have, want = ([d for d in axes if d != 1] for axes in (t.shape, lead))
+    if have[:len(want)] == want or len(have) <= 1:
+        return
+    if have[-1] in widths and (len(have) == 2 or len(want) <= 1):
+        return
+    raise ValueError(f"{what} must have the leading axes {tuple(lead)}, or be flattened to rows; "
+                     f"has the shape {tuple(t.shape)}")
+
+
 def _device_of(t, what):
     """(device, its index) of a device tensor."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -148,14 +161,18 @@ def _norm_shape(like, groups):
     return like.numel() // channels, channels, kind
 
 
-def _gate_of(gate, rows, channels, groups, index):
-    """(width, address) of a gate [..., groups] or [..., channels], or of none."""
+def _gate_of(gate, like, rows, channels, groups, index):
+    """(width, address) of a gate [..., groups] or [..., channels] of the rows of `like`, or of
+    none."""
     if gate is None:
         return 0, 0
     width = gate.shape[-1] if gate.dim() else 0
     if width != groups and width != channels:
         raise ValueError("gate must be [..., groups] or [..., channels]")
-    return width, _tensor(gate, torch.bfloat16, rows * width, "gate", index)
+    address = _tensor(gate, torch.bfloat16, rows * width, "gate", index)
+    if gate.dim() > 2:  # (of two axes the first is the rows)
+        _check_rows(gate, like.shape[:-1], (width,), "gate")
+    return width, address
 
 
 def _codes(rows, channels, groups, device):
@@ -177,7 +194,7 @@ def engram_residual_norm(residual, y=None, *, gate=None, w_post=None, scale=None
     device, index = _device_of(residual, "residual")
     rows, channels, kind = _norm_shape(residual, groups)
     n, stats, rt, bf = rows * channels, rows * groups, residual.dtype, torch.bfloat16
-    width, gate_p = _gate_of(gate, rows, channels, groups, index)
+    width, gate_p = _gate_of(gate, residual, rows, channels, groups, index)
     y_p = out_p = post_p = next_p = rnext_p = yc_p = ys_p = nc_p = ns_p = 0
     yc = ys = nc = ns = None
     if y is not None:
@@ -232,7 +249,7 @@ def engram_residual_norm_backward(grad_out, grad_next=None, *, out=None, rstd_po
     rows, channels, kind = _norm_shape(like, groups)
     n, stats, rt = rows * channels, rows * groups, like.dtype
     bf, f32 = torch.bfloat16, torch.float32
-    width, gate_p = _gate_of(gate, rows, channels, groups, index)
+    width, gate_p = _gate_of(gate, like, rows, channels, groups, index)
     if (w_next is None) != (grad_next is None):
         raise ValueError("grad_next goes with w_next")
     out_p = dn_p = rnext_p = post_p = y_p = yc_p = ys_p = 0
@@ -241,12 +258,18 @@ def engram_residual_norm_backward(grad_out, grad_next=None, *, out=None, rstd_po
         if grad_next.shape != like.shape:
             raise ValueError("grad_next must have the shape of grad_out (or of out)")
         out_p = _tensor(out, rt, n, "out", index)
+        if out.shape != like.shape:
+            _check_rows(out, like.shape[:-1], (channels,), "out")
         rnext_p = _tensor(rstd_next, f32, stats, "rstd_next", index)
     branch = y is not None or y_codes is not None
     if branch:
         post_p = _tensor(rstd_post, f32, stats, "rstd_post", index)
         y_p = _optional(y, bf, n, "y", index)
+        if y is not None and y.shape != like.shape:
+            _check_rows(y, like.shape[:-1], (channels,), "y")
         yc_p = _optional(y_codes, torch.int8, n, "y_codes", index)
+        if y_codes is not None:
+            _check_rows(y_codes, like.shape[:-1], (channels, channels // groups), "y_codes")
         ys_p = _optional(y_scales, f32, stats * code_blocks(channels // groups), "y_scales",
                          index)
     if grad_residual is None:

@@ -1,0 +1,64 @@
+"""Arguments of the layer operators that have the right number of values in another
+order of axes are refused: they would be read as other rows.  Flattened ones are not."""
+import pytest
+import torch
+
+from gram_hashed_embedding_amd import workloads
+from tests.gpu_helpers import needs_gpu
+
+pytestmark = needs_gpu
+L = pytest.importorskip("gram_hashed_embedding_amd.layer")
+
+B, S, C, G = 2, 6, 64, 4
+N = C // G
+F32, I8, I64 = torch.float32, torch.int8, torch.int64
+
+
+def z(*shape, dtype=torch.bfloat16):
+    return torch.zeros(shape, dtype=dtype, device="cuda")
+
+
+def draw(*shape):
+    return workloads.make_bf16(shape, sum(shape), "cuda")
+
+
+# ------------------------------------------------------------- residual norm --
+@pytest.mark.parametrize("name,shape", [("y", (S, B, C)), ("y", (C, B * S)), ("out", (S, B, C)),
+                                        ("gate", (S, B, G)), ("gate", (S, B, C)),
+                                        ("y_codes", (S, B, C)), ("y_codes", (C, B * S)),
+                                        ("y_codes", (S, B, G, N))])
+def test_norm_backward_refuses(name, shape):
+    args = dict(out=z(B, S, C), rstd_post=z(B * S, G, dtype=F32), rstd_next=z(B * S, G, dtype=F32),
+                y=z(B, S, C), gate=z(B, S, G), w_next=z(C), groups=G)
+    if name == "y_codes":
+        args.update(y=None, y_scales=z(B * S, G, dtype=F32), y_codes=z(*shape, dtype=I8))
+    else:
+        args[name] = z(*shape)
+    with pytest.raises(ValueError):
+        L.engram_residual_norm_backward(z(B, S, C), z(B, S, C), **args)
+
+
+@pytest.mark.parametrize("shape", [(S, B, G), (S, B, C)])
+def test_norm_refuses_a_gate(shape):
+    with pytest.raises(ValueError):
+        L.engram_residual_norm(z(B, S, C), z(B, S, C), gate=z(*shape), groups=G)
+
+
+def test_norm_takes_flattened_rows():
+    """Codes and gates of rows [B * S, ...], as the forward and a product of rows leave them;
+    and every argument flattened, or only the rows that the shape is taken of."""
+    r, y, gate, d = draw(B, S, C), draw(B, S, C), draw(B, S, G), draw(B, S, C)
+    f, flat = (L.engram_residual_norm(r, y, gate=g, groups=G, save_codes=True)
+               for g in (gate, gate.view(-1, G)))
+    assert torch.equal(f.out, flat.out) and f.y_codes.shape == (B * S, C)
+    stats = dict(rstd_post=f.rstd_post, groups=G)
+    codes = [L.engram_residual_norm_backward(dd, y_codes=c, y_scales=f.y_scales, gate=g, **stats)
+             for c in (f.y_codes, f.y_codes.view(B, S, C), f.y_codes.view(-1, N),
+                       f.y_codes.view(B, S, G, N), f.y_codes.view(-1))
+             for g in (gate, gate.view(-1, G)) for dd in (d, d.view(-1, C))]
+    plain = [L.engram_residual_norm_backward(dd, y=yy, gate=gate, **stats)
+             for dd in (d, d.view(-1, C)) for yy in (y, y.view(-1, C))]
+    for results in (codes, plain):
+        for b in results[1:]:
+            for k in ("y", "residual", "gate"):
+                assert torch.equal(getattr(b, k).view(-1), getattr(results[0], k).view(-1))
