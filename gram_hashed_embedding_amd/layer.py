@@ -387,16 +387,21 @@ def engram_ple_conv_backward(grad_out, weight, dilation, x=None, x_codes=None, x
         halo_len = halo.shape[1]
         hp = _tensor(halo, torch.bfloat16, batch * halo_len * channels, "halo", index)
     ids = _optional(seq_ids, torch.int64, batch * (halo_len + seq), "seq_ids", index)
+    if seq_ids is not None and seq_ids.shape != (batch, halo_len + seq):
+        _check_rows(seq_ids, (batch, halo_len + seq), (), "seq_ids")
     xp = cp = sp = None
     if need_weight:
         if (x is None) == (x_codes is None):
             raise ValueError("the weight's gradient needs x, or x_codes and x_scales")
         xp = _optional(x, torch.bfloat16, n, "x", index)
+        if x is not None and x.shape != grad_out.shape:
+            _check_rows(x, (batch, seq), (channels,), "x")
         cp = _optional(x_codes, torch.int8, n, "x_codes", index)
         if x_codes is not None:
             width = code_width or channels
             if width < 1 or channels % width:
                 raise ValueError("code_width must divide channels")
+            _check_rows(x_codes, (batch, seq), (channels, width), "x_codes")
             sp = _tensor(x_scales, torch.float32,
                          batch * seq * (channels // width) * code_blocks(width), "x_scales", index)
     gx = torch.empty_like(grad_out) if need_x else None

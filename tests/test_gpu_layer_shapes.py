@@ -62,3 +62,41 @@ def test_norm_takes_flattened_rows():
         for b in results[1:]:
             for k in ("y", "residual", "gate"):
                 assert torch.equal(getattr(b, k).view(-1), getattr(results[0], k).view(-1))
+
+
+# --------------------------------------------------------------- convolution --
+def conv_backward(**other):
+    return L.engram_ple_conv_backward(z(B, S, C), z(C, 4), 1, **{"x": z(B, S, C), **other})
+
+
+@pytest.mark.parametrize("shape", [(S, B, C), (B, C, S), (C, B * S)])
+def test_conv_backward_refuses_x(shape):
+    with pytest.raises(ValueError):
+        conv_backward(x=z(*shape))
+
+
+@pytest.mark.parametrize("shape,width", [((S, B, C), 0), ((C, B * S), 0), ((S, B, G, N), N),
+                                         ((B * S * G // 2, 2 * N), N)])
+def test_conv_backward_refuses_codes(shape, width):
+    with pytest.raises(ValueError):
+        conv_backward(x=None, x_codes=z(*shape, dtype=I8), code_width=width,
+                      x_scales=z(B * S * (G if width else 1), dtype=F32))
+
+
+def test_conv_backward_refuses_segment_ids():
+    with pytest.raises(ValueError):
+        conv_backward(seq_ids=z(S, B, dtype=I64))
+
+
+def test_conv_backward_takes_flattened_rows():
+    x, g, w = draw(B, S, C), draw(B, S, C), draw(C, 4)
+    ids = torch.tensor([[0, 0, 1, 1, 1, 2], [3, 3, 3, 3, 4, 4]], device="cuda")
+    codes, scales = L.engram_act_encode(x.view(-1, N))
+    kept = [dict(x_codes=c, x_scales=scales, code_width=N)
+            for c in (codes, codes.view(B, S, C), codes.view(B * S, C), codes.view(B, S, G, N),
+                      codes.view(-1))]
+    for forms in (kept, [dict(x=x), dict(x=x.view(-1, C))]):
+        results = [L.engram_ple_conv_backward(g, w, 2, seq_ids=i, **k)
+                   for k in forms for i in (ids, ids.view(-1))]
+        for b in results[1:]:
+            assert torch.equal(b.weight, results[0].weight) and torch.equal(b.x, results[0].x)
