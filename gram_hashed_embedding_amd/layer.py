@@ -510,6 +510,8 @@ def engram_embed_grad(tokens, grads, table_rows, scale=1.0, grad_table=None,
     if grads.dtype not in _TYPES:
         raise TypeError(f"grads must be bfloat16 or float32, is {grads.dtype}")
     gp = _tensor(grads, grads.dtype, n * channels, "grads", index)
+    if grads.dim() > 2 and tokens.dim() > 1 and grads.shape[:-1] != tokens.shape:
+        _check_rows(grads, tokens.shape, (channels,), "grads")
     if grad_table is None:
         if accumulate:
             raise ValueError("accumulate needs grad_table")
@@ -517,6 +519,8 @@ def engram_embed_grad(tokens, grads, table_rows, scale=1.0, grad_table=None,
     if grad_table.dtype not in _TYPES:
         raise TypeError(f"grad_table must be bfloat16 or float32, is {grad_table.dtype}")
     op = _tensor(grad_table, grad_table.dtype, table_rows * channels, "grad_table", index)
+    if grad_table.dim() == 2 and grad_table.shape[1] != channels:
+        raise ValueError("grad_table must be [table_rows, channels]")
     ep = _optional(err_count, torch.int64, 1, "err_count", index)
     need = _lib.engram_embed_grad_workspace(n, channels, table_rows)
     workspace = _bytes(workspace, need, device, index, "engram_embed_grad_workspace")

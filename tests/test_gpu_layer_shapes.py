@@ -100,3 +100,25 @@ def test_conv_backward_takes_flattened_rows():
                    for k in forms for i in (ids, ids.view(-1))]
         for b in results[1:]:
             assert torch.equal(b.weight, results[0].weight) and torch.equal(b.x, results[0].x)
+
+
+# ----------------------------------------------------------------- embedding --
+@pytest.mark.parametrize("tokens,grads", [((S, B), (B, S, C)), ((B, S), (S, B, C))])
+def test_embed_grad_refuses_other_axes(tokens, grads):
+    with pytest.raises(ValueError):
+        L.engram_embed_grad(z(*tokens, dtype=I64), z(*grads), 9)
+
+
+def test_embed_grad_refuses_a_table_of_other_rows():
+    with pytest.raises(ValueError):
+        L.engram_embed_grad(z(B, S, dtype=I64), z(B, S, C), 9, grad_table=z(C, 9, dtype=F32))
+
+
+def test_embed_grad_takes_flattened_rows():
+    t, g = torch.arange(B * S, device="cuda").view(B, S) % 7, draw(B, S, C)
+    want = L.engram_embed_grad(t, g, 9)
+    for a in (t, t.view(-1), t.view(-1, 1)):
+        for b in (g, g.view(-1, C)):
+            assert torch.equal(L.engram_embed_grad(a, b, 9), want)
+    table = torch.empty((9 * C,), device="cuda")
+    assert torch.equal(L.engram_embed_grad(t, g, 9, grad_table=table).view(9, C), want)
