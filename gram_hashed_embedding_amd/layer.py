@@ -5,7 +5,7 @@ single-token form, the scaled token embedding and its gradient.
 
 As ``engram.py``: argument marshalling only, every step in the library's HIP
 kernels, asynchronous on the current stream of the tensors' device, or on the
-stream passed as ``stream``.  Outputs and workspaces are torch tensors, allocated when
+stream of that device passed as ``stream``.  Outputs and workspaces are torch tensors, allocated when
 they are not passed in.  What each call computes stands in the header.
 
 A tensor that is freed while work on another stream still reads it has to be
@@ -112,6 +112,12 @@ def _streamed(call):
     def on_stream(*args, stream=None, **kwargs):
         if stream is None:
             return call(*args, **kwargs)
+        # (a stream of another device would leave the call on its tensors' device's own stream)
+        for t in (*args, *kwargs.values()):
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                if t.get_device() != stream.device.index:
+                    raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+                break
         with torch.cuda.stream(stream):
             return call(*args, **kwargs)
     return on_stream
