@@ -361,6 +361,15 @@ def engram_act_decode(codes, scales, out=None):
 
 
 # --------------------------------------------------------------- convolution --
+def _taps(weight, dilation):
+    """(kernel_size, dilation) as the 32-bit numbers of the call, which would take a larger
+    one's low half."""
+    kernel, dilation = weight.shape[1], int(dilation)
+    if not -1 << 31 <= dilation < 1 << 31 or kernel >= 1 << 31:
+        raise ValueError("kernel_size and dilation must fit 32 bits")
+    return kernel, dilation
+
+
 class ConvGrads(NamedTuple):
     """The gradients engram_ple_conv_backward wrote."""
     x: Optional[torch.Tensor]
@@ -382,7 +391,7 @@ def engram_ple_conv_backward(grad_out, weight, dilation, x=None, x_codes=None, x
     batch, seq, channels = grad_out.shape
     if weight.dim() != 2 or weight.shape[0] != channels:
         raise ValueError("weight must be [channels, kernel_size]")
-    kernel = weight.shape[1]
+    kernel, dilation = _taps(weight, dilation)
     n, halo_len = grad_out.numel(), 0
     gp = _tensor(grad_out, torch.bfloat16, n, "grad_out", index)
     wp = _tensor(weight, torch.bfloat16, channels * kernel, "weight", index)
@@ -420,7 +429,7 @@ def engram_ple_conv_backward(grad_out, weight, dilation, x=None, x_codes=None, x
     size = 0
     if need_weight or need_bias:
         need = _lib.engram_ple_conv_backward_workspace(batch, seq, halo_len, channels, kernel,
-                                                       int(dilation))
+                                                       dilation)
         workspace = _bytes(workspace, need, device, index, "engram_ple_conv_backward_workspace")
         size = workspace.numel()
 
@@ -428,7 +437,7 @@ def engram_ple_conv_backward(grad_out, weight, dilation, x=None, x_codes=None, x
         return None if t is None else t.data_ptr()
 
     _run(index, "engram_ple_conv_backward", gp, xp, cp, sp, code_width,
-         hp if halo_len else None, halo_len, ids, wp, batch, seq, channels, kernel, int(dilation),
+         hp if halo_len else None, halo_len, ids, wp, batch, seq, channels, kernel, dilation,
          ptr(gx), ptr(gh), ptr(gw), ptr(gb), ptr(workspace) if size else None, size,
          _stream_of(index))
     if need_x and halo is not None and gh is None:
@@ -455,7 +464,8 @@ def engram_ple_conv_step(x, ring, weight, dilation, positions, slots=None, bias=
         raise ValueError("ring must be [ring_count, ring_rows, channels]")
     if weight.dim() != 2 or weight.shape[0] != channels:
         raise ValueError("weight must be [channels, kernel_size]")
-    kernel, n = weight.shape[1], batch * tokens * channels
+    kernel, dilation = _taps(weight, dilation)
+    n = batch * tokens * channels
     xp = _tensor(x, torch.bfloat16, n, "x", index)
     rp = _tensor(ring, torch.bfloat16, ring.numel(), "ring", index)
     wp = _tensor(weight, torch.bfloat16, channels * kernel, "weight", index)
@@ -471,7 +481,7 @@ def engram_ple_conv_step(x, ring, weight, dilation, positions, slots=None, bias=
     elif out is not None:
         raise ValueError("write_only computes no out")
     _run(index, "engram_ple_conv_step", xp, rp, ring.shape[0], ring.shape[1], ip, pp, wp, bp,
-         batch, tokens, channels, kernel, int(dilation), op, ep, _stream_of(index))
+         batch, tokens, channels, kernel, dilation, op, ep, _stream_of(index))
     return out
 
 

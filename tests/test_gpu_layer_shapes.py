@@ -122,3 +122,21 @@ def test_embed_grad_takes_flattened_rows():
             assert torch.equal(L.engram_embed_grad(a, b, 9), want)
     table = torch.empty((9 * C,), device="cuda")
     assert torch.equal(L.engram_embed_grad(t, g, 9, grad_table=table).view(9, C), want)
+
+
+# --------------------------------------------------------------------- sizes --
+@pytest.mark.parametrize("dilation", [2 ** 32 + 1, 2 ** 31, -2 ** 32 + 1])
+def test_dilations_past_32_bits_are_refused(dilation):
+    """Their low halves are dilations."""
+    with pytest.raises(ValueError):
+        L.engram_ple_conv_backward(z(1, 3, 8), z(8, 4), dilation, x=z(1, 3, 8))
+    with pytest.raises(ValueError):
+        L.engram_ple_conv_step(z(1, 8), z(1, 3, 8), z(8, 4), dilation, z(1, dtype=I64))
+
+
+def test_the_largest_dilation():
+    """No tap but a position's own lies inside the row."""
+    g, x, w = draw(1, 5, 8), draw(1, 5, 8), draw(8, 4)
+    b = L.engram_ple_conv_backward(g, w, 2 ** 31 - 1, x=x)
+    assert torch.equal(b.x, (g.float() * w[:, 3].float()).to(torch.bfloat16))
+    assert bool((b.weight[:, :3] == 0).all()) and bool((b.weight[:, 3] != 0).any())
