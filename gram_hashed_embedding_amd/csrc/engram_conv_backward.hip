@@ -25,12 +25,16 @@
 // A tile's loads are straight-line code, at clamped addresses, and go out while
 // the tile before is worked on: behind branches, even wave-uniform ones, each
 // was waited for on its own (985 us for the encoding and the gradients below,
-// 780 us so).  Registers bound the waves to two a SIMD; as many slices as such
-// waves (2048) were faster than twice as many (780 and 817 us), tiles of 8
-// positions than tiles of 4 (801 us).  Measured on MI355X, [8, 8192, 8192],
-// dilation 4, packed segments, x from its checkpoint: 500 us (5.4 TB/s; 540
-// under the profiler), its sums joined in 7 us.  [2, 2053, 1032] with a halo:
-// 23 us, bound by latency (about 14 of them for a wave's four tiles alone).
+// 780 us so).  Registers bound the waves to two a SIMD up to dilation 4 (5 with x in
+// bf16), and to one beyond (256 registers and accumulation registers).  As many
+// slices as two a SIMD (2048 waves) were faster than twice as many (780 and 817 us),
+// tiles of 8 positions than tiles of 4 (801 us), both at dilation 4.  Measured on
+// MI355X, [8, 8192, 8192], packed segments: from the checkpoint at dilation 4 500 us
+// (5.4 TB/s; 540 under the profiler), its sums joined in 7 us, at dilations 5, 6 and
+// 8 584, 681 and 740; from bf16 at dilations 4 and 5 610 us (5.3 TB/s), at 6 and 8
+// 648 and 717.  [2, 2053, 1032] with a halo: 23 us, bound by latency (about 14 of
+// them for a wave's four tiles alone).  The kernel for other shapes reads every row
+// of g K times for each of the two sums: 6.1 ms for [8, 8192, 8192] with 3 taps.
 #include "engram_layer_dev.h"
 
 namespace engram {

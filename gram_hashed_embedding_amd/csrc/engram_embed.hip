@@ -24,8 +24,11 @@
 // looked up in 53.7 us (6.0 TB/s; into floats 92 us, 6.4 TB/s); the gradient of
 // as many into floats 290 us, of which sorting takes 35, marks 7, the walkers and
 // zeros 228 (7.0 TB/s) and the join 8; of 4099 x 1024 into bf16 59 us (counting
-// and marks 6, walkers and zeros 49, join 5).  More and shorter chunks were
-// slower (at most 64 positions: 362 us, 32: 388, against 306 then at 128).
+// and marks 6, walkers and zeros 49, join 5).  From float gradients the 65,536 x 2048
+// take 391 us (4.5 TB/s: four rows of a lane in flight, not eight); accumulated into
+// the rows with tokens alone 215 us from bf16 and 252 from floats, where no zeros hide
+// the sort and the walkers' waits.  More and shorter chunks were slower (at most 64
+// positions: 362 us, 32: 388, against 306 then at 128).
 #include "engram_layer_dev.h"
 #include "engram_scatter_dev.h"
 
@@ -225,7 +228,8 @@ __device__ __forceinline__ void mark_rows(const int64_t *tokens, int64_t n, int6
 // merged by embed_merge_kernel: up to kMergeTokens the comparisons and searches,
 // spread over the whole GPU, beat the sort's passes, which wait on one another
 // (the whole gradient at 256 channels: 9000 tokens 44 us against 60 with the
-// passes, 20,000 52 and 67, 65,536 81 and 89, 90,000 107 and 86).
+// passes, 20,000 52 and 67, 65,536 81 and 89, 90,000 107 and 86; where the two
+// cross between the last two was not looked for).
 constexpr int kRankThreads = kMarkThreads;
 constexpr int64_t kRankTokens = 8192, kPieceTokens = 2048, kMergeTokens = 65536;
 constexpr int kRankBlock = 16, kPieceBlock = 64;

@@ -60,9 +60,10 @@ ConvBackwardShape conv_backward_shape(int64_t batch, int64_t seq, int64_t halo_l
   ConvBackwardShape s = {};
   s.quads = channels / 4;
   s.groups = ceil_div(s.quads, 64);
-  // about 2048 waves, as many as stay on 256 CUs at a time (8 each); a slice not
-  // so short that the rows it reads past its end (the register window's) outweigh
-  // its own, nor so long that its fp32 sums lose bits
+  // about 2048 waves, as many as stay on 256 CUs at a time (8 each; 4 each where the
+  // window's registers leave one wave a SIMD, from dilation 5 or 6 on: those run in two
+  // rounds); a slice not so short that the rows it reads past its end (the register
+  // window's) outweigh its own, nor so long that its fp32 sums lose bits
   const int64_t want = ceil_div(2048, (batch > 0 ? batch : 1) * s.groups);
   const int64_t ahead = conv_windowed(K, dilation) ? (int64_t)(K - 1) * dilation : 0;
   const int64_t least = 2 * ahead > 32 ? 2 * ahead : 32;

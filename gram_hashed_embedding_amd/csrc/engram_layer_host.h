@@ -36,8 +36,14 @@ constexpr int kNormForwardItems = 4;
 constexpr int kNormBackwardItems = 2;
 // The forward: a block takes a few rows and ends, so that the blocks that run
 // together stay together in memory (65,536 x 6144: 32,768 blocks 943 us, 4096
-// 1040, one for each row 960).  The backward: as many blocks as stay on the GPU
-// together, since each leaves sums (768 blocks 1236 us, 1536 1274, 3072 1291).
+// 1040, one for each row 960).  The backward: as many blocks of 256 threads as
+// stay on the GPU together where a lane holds one chunk (3 wavefronts a SIMD),
+// since each leaves sums (65,536 x 6144 in 24 groups: 768 blocks 1236 us, 1536
+// 1274, 3072 1291).  That shape is where the count was measured.  Kernels of two
+// chunks a lane keep 2 wavefronts a SIMD, so 768 of their blocks run in one and a
+// half rounds; blocks of 1024 threads are scaled to 192, fewer than the 256 CUs
+// ([16384, 4096] as one group takes 192 us against a floor of 124, [8192, 6144]
+// 213 against 140).
 constexpr int64_t kNormForwardBlocks = 32768;
 constexpr int64_t kNormBackwardBlocks = 768;
 // Most rows a lane sums in fp32 before the sums go on in fp64.

@@ -18,7 +18,12 @@
 // by latency.  Measured on MI355X, 65,536 rows of 24 groups of 256, float
 // stream, one gate a group, 8-bit checkpoint of y: forward 945 us (5.6 TB/s),
 // backward 1236 us (5.5 TB/s), where a streaming copy reaches 6.5 TB/s.  8 rows
-// of one group of 6144: 5.2 us.
+// of one group of 6144: 5.2 us.  One group a row: [8192, 6144] forward 120 us (5.0
+// TB/s), backward 213 (4.2 TB/s); the norm alone of [16384, 4096] in bf16 54 and 125
+// us.  Two to four chunks a lane take 128 to 246 registers, which leaves 2 or 3
+// wavefronts a SIMD; the 1024-thread backward of two chunks (groups past 8192
+// channels) spills 290 to 390 bytes a lane ([2048, 16384]: 276 us, 1.5 TB/s), that of
+// one chunk with a float stream 20.
 //
 // Layout.  A lane holds chunks of 8 adjacent channels (16 bytes of bf16); a
 // group of up to 512 channels is a power of two of lanes of one wavefront, so
