@@ -169,3 +169,42 @@ def declare_layer(lib):
         f = getattr(lib, name)
         f.restype, f.argtypes = result, args
     return lib
+
+
+DISTILL_MAX_TOP = 1024            # ENGRAM_DISTILL_MAX_TOP
+BEAM_MAX = 64                     # ENGRAM_BEAM_MAX
+FORK_MAX_POOLS = 8                # ENGRAM_FORK_MAX_POOLS
+
+
+class EngramDistillArgs(ctypes.Structure):
+    """struct engram_distill_args of include/engram_vocab.h, field for field."""
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("vocab", ctypes.c_int64), ("top", ctypes.c_int64),
+        ("logits_stride", ctypes.c_int64), ("grad_stride", ctypes.c_int64),
+        ("temperature", ctypes.c_float), ("logits_type", ctypes.c_int32),
+        ("teacher_type", ctypes.c_int32), ("rest", ctypes.c_int32),
+        ("d_logits", _vp), ("d_ids", _vp), ("d_teacher", _vp), ("d_teacher_lse", _vp),
+        ("d_grad_loss", _vp), ("d_loss", _vp), ("d_lse", _vp), ("d_lse_rest", _vp),
+        ("d_grad", _vp), ("d_err_count", _vp), ("d_workspace", _vp),
+        ("workspace_bytes", ctypes.c_size_t), ("stream", _vp),
+    ]
+
+
+def declare_vocab(lib):
+    """declare() for the entry points of include/engram_vocab.h."""
+    i64, i32, size = ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+    distill = _vp  # an EngramDistillArgs by reference, or its bytes
+    for name, result, args in [
+        ("engram_distill_workspace", size, [i64, i64]),
+        ("engram_distill", ctypes.c_int, [distill]),
+        ("engram_distill_backward", ctypes.c_int, [distill]),
+        ("engram_beam_select_workspace", size, [i64, i64, i64]),
+        ("engram_beam_select", ctypes.c_int,
+         [_vp, i32, i64, _vp, _vp, i64, i64, i64, i64, i64, _vp, _vp, _vp, _vp, _vp, size, _vp]),
+        ("engram_beam_fork", ctypes.c_int,
+         [_vp, _vp, i64, i64, ctypes.POINTER(_vp), _i64p, i32, i64, _vp, _vp, _vp, i64, _vp, i64,
+          _vp, _vp]),
+    ]:
+        f = getattr(lib, name)
+        f.restype, f.argtypes = result, args
+    return lib

@@ -1,0 +1,370 @@
+// engram_beam.hip -- beam search: the selection over beams and vocabulary, and
+// the reordering of the decoding states after it, for gfx950.  What is computed
+// is stated with engram_beam_select and engram_beam_fork in include/
+// engram_vocab.h.
+//
+// Selection.  One pass over the logits (beam_scan_kernel) leaves each segment's
+// sum of exponentials and the largest logit of every kBeamGroup adjacent
+// values.  The `count` best candidates lie in the `count` best groups (by their
+// largest value, equal ones by place: the candidate before which `count` others
+// come cannot be one of the first `count`), so beam_choose_kernel, a block to a
+// sequence, finds those among 1/128 of the values, reads them again and takes
+// the best of `count` times 128 candidates.  Both choices are exact in fp64.
+//
+// Reordering.  A new beam that is the first child of its parent keeps the
+// parent's slot; only the others' states are copied, into slots of beams that
+// ended.  Every block works the order out for itself from one wavefront's
+// ballots, so one launch does all of it and nothing is read that is written.
+#include "engram_vocab_dev.h"
+
+namespace engram {
+namespace {
+
+// ------------------------------------------------------------------- scan --
+struct ScanArgs {
+  const void *logits;
+  int64_t vocab, stride, segs, seg_len, groups;
+  float c;
+  const float *scores;
+  const uint8_t *finished;
+  ScanPart *parts;
+  float *maxima;
+};
+
+// Whether a beam's logits are needed.
+__device__ __forceinline__ bool beam_live(const float *scores, const uint8_t *finished,
+                                          int64_t row) {
+  return __builtin_isfinite(scores[row]) && (finished == nullptr || finished[row] == 0);
+}
+
+// The maximum over aligned groups of 16 lanes, by DPP.
+__device__ __forceinline__ float max16(float v) {
+  const auto op = [](uint32_t a, uint32_t b) {
+    return __float_as_uint(max3(__uint_as_float(a), __uint_as_float(b), kNegInf));
+  };
+  return __uint_as_float(lanes_reduce<16>(__float_as_uint(v), op));
+}
+
+template <class T>
+__global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(const ScanArgs a) {
+  __shared__ RowSum sums[kScanThreads / kWave];
+  const int64_t row = blockIdx.x / a.segs, seg = blockIdx.x - row * a.segs;
+  if (!beam_live(a.scores, a.finished, row)) return;
+  const int64_t lo = seg * a.seg_len, hi = lo + a.seg_len < a.vocab ? lo + a.seg_len : a.vocab;
+  const T *z = static_cast<const T *>(a.logits) + row * a.stride;
+  float *maxima = a.maxima + row * a.groups;
+  constexpr int U = sizeof(T) == 2 ? 4 : 2;
+  Running run;
+  each_chunks<T, U>(z, lo, hi, [&](int64_t at, float (&z)[U][8]) {
+    float m = run.max;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float own = max8(kNegInf, z[u]);
+      m = max3(m, own, kNegInf);
+      const float most = max16(own);
+      const int64_t i = at + u * kScanTile + 8 * threadIdx.x;
+      if (threadIdx.x % 16 == 0 && i < hi) maxima[i / kBeamGroup] = most;
+    }
+    const float ref = run.raise(m, a.c);
+#pragma unroll
+    for (int u = 0; u < U; ++u) run.add(z[u], a.c, ref);
+  });
+  const RowSum s = block_join<kScanThreads>(RowSum{run.max, (double)run.sum}, a.c, sums);
+  if (threadIdx.x == 0) a.parts[row * a.segs + seg] = {s.sum, s.max, 0u};
+}
+
+// ----------------------------------------------------------------- choice --
+constexpr int kChooseThreads = 1024;
+constexpr int kChooseList = 2048;
+
+// A candidate: its value, and its place among all of them.
+struct Candidate {
+  double value;
+  int64_t at;
+};
+__device__ __forceinline__ bool before(const Candidate &x, const Candidate &y) {
+  return x.value > y.value || (x.value == y.value && x.at < y.at);
+}
+constexpr double kNone = -__builtin_inf();
+
+struct ChooseLds {
+  Candidate list[kChooseList];
+  Candidate best[ENGRAM_BEAM_MAX];  // the answer, in order
+  double row_best[kChooseThreads / 16];
+  Candidate wave_best[kChooseThreads / kWave];
+  double threshold;
+  int listed, taken;
+};
+
+// The first `count` of the candidates 0 .. n-1 (get(i), value kNone where there is
+// none), in order, in l.best[0 .. l.taken).
+//
+// A threshold first: of the largest values of 64 rows of 16 threads, the count-th
+// largest has at least `count` values at or above it.  What reaches it is listed and
+// ranked by counting.  More than the list holds (long runs of equal values) are taken
+// one at a time instead, each the first after the one before.
+template <class GET>
+__device__ void choose(ChooseLds &l, int64_t n, int count, GET get) {
+  const int t = threadIdx.x;
+  double mine = kNone;
+  for (int64_t i = t; i < n; i += kChooseThreads) mine = fmax(mine, get(i).value);
+#pragma unroll
+  for (int d = 1; d < 16; d *= 2) mine = fmax(mine, __shfl_xor(mine, d));
+  if (t % 16 == 0) l.row_best[t / 16] = mine;
+  if (t == 0) l.listed = 0;
+  __syncthreads();
+  if (t < kWave) {
+    const double v = l.row_best[t];
+    int ahead = 0;
+#pragma unroll 8
+    for (int k = 0; k < kWave; ++k) {
+      const double o = l.row_best[k];
+      ahead += o > v || (o == v && k < t);
+    }
+    if (ahead == count - 1) l.threshold = v;
+  }
+  __syncthreads();
+  const double least = l.threshold;
+  for (int64_t i = t; i < n; i += kChooseThreads) {
+    const Candidate c = get(i);
+    if (c.value > kNone && c.value >= least) {
+      const int k = atomicAdd(&l.listed, 1);
+      if (k < kChooseList) l.list[k] = c;
+    }
+  }
+  __syncthreads();
+  const int listed = l.listed;
+  if (listed <= kChooseList) {
+    for (int k = t; k < listed; k += kChooseThreads) {
+      const Candidate c = l.list[k];
+      int ahead = 0;
+      for (int o = 0; o < listed; ++o) ahead += before(l.list[o], c);
+      if (ahead < count) l.best[ahead] = c;
+    }
+    if (t == 0) l.taken = listed < count ? listed : count;
+    __syncthreads();
+    return;
+  }
+  // (at least `count` candidates there)
+  Candidate last = {__builtin_inf(), -1};
+  for (int r = 0; r < count; ++r) {
+    Candidate m = {kNone, INT64_MAX};
+    for (int64_t i = t; i < n; i += kChooseThreads) {
+      const Candidate c = get(i);
+      if (c.value > kNone && before(last, c) && before(c, m)) m = c;
+    }
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) {
+      const Candidate o = {__shfl_xor(m.value, d), __shfl_xor(m.at, d)};
+      if (before(o, m)) m = o;
+    }
+    if (t % kWave == 0) l.wave_best[t / kWave] = m;
+    __syncthreads();
+    last = l.wave_best[0];
+    for (int w = 1; w < kChooseThreads / kWave; ++w)
+      if (before(l.wave_best[w], last)) last = l.wave_best[w];
+    if (t == 0) l.best[r] = last;
+    __syncthreads();
+  }
+  if (t == 0) l.taken = count;
+  __syncthreads();
+}
+
+struct ChooseArgs {
+  BeamCall c;
+  int64_t segs, groups;
+  float log2e;
+};
+
+template <class T>
+__global__ __launch_bounds__(kChooseThreads) void beam_choose_kernel(const ChooseArgs a) {
+  __shared__ ChooseLds l;
+  __shared__ double lse[ENGRAM_BEAM_MAX];    // NaN: no candidate but a finished beam's
+  __shared__ double score[ENGRAM_BEAM_MAX];
+  __shared__ int64_t group_at[ENGRAM_BEAM_MAX];
+  const BeamCall &c = a.c;
+  const int64_t b = blockIdx.x, first_row = b * c.beams;
+  const int t = threadIdx.x, beams = (int)c.beams, count = (int)c.count;
+  // each beam's lse, a wavefront to a beam
+  for (int w = t / kWave; w < beams; w += kChooseThreads / kWave) {
+    const int64_t row = first_row + w;
+    double v = __builtin_nan("");
+    if (beam_live(c.scores, c.finished, row)) {
+      RowSum s = {kNegInf, 0.0};
+      for (int64_t i = t % kWave; i < a.segs; i += kWave) {
+        const ScanPart p = c.parts[row * a.segs + i];
+        s = join_sums(s, RowSum{p.max, p.sum}, a.log2e);
+      }
+      s = wave_join(s, a.log2e);
+      v = log_sum(s, 1.0, a.log2e);
+      if (!__builtin_isfinite(v)) v = __builtin_nan("");
+    }
+    if (t % kWave == 0) {
+      lse[w] = v;
+      score[w] = c.scores[row];
+    }
+  }
+  __syncthreads();
+  // the best groups; a finished beam's candidate is a group of its own (its first)
+  const int64_t groups = a.groups;
+  const auto value_of = [&](int w, float z) {
+    const double v = score[w] + ((double)z - lse[w]);
+    return v == v ? v : kNone;
+  };
+  const auto finished = [&](int w) {
+    return c.finished != nullptr && c.finished[first_row + w] != 0 &&
+           __builtin_isfinite(c.scores[first_row + w]);
+  };
+  choose(l, beams * groups, count, [&](int64_t i) {
+    const int w = (int)(i / groups);
+    const int64_t g = i - w * groups;
+    double v = kNone;
+    if (lse[w] == lse[w])
+      v = value_of(w, c.maxima[(first_row + w) * groups + g]);
+    else if (g == 0 && finished(w))
+      v = score[w];
+    return Candidate{v, i};
+  });
+  const int chosen = l.taken;
+  if (t < chosen) group_at[t] = l.best[t].at;
+  __syncthreads();
+  choose(l, chosen * kBeamGroup, count, [&](int64_t i) {
+    const int64_t place = group_at[i / kBeamGroup];
+    const int w = (int)(place / groups);
+    const int64_t v = (place - w * groups) * kBeamGroup + i % kBeamGroup;
+    if (lse[w] == lse[w]) {
+      if (v >= c.vocab) return Candidate{kNone, INT64_MAX};
+      const T *z = static_cast<const T *>(c.logits) + (first_row + w) * c.stride;
+      return Candidate{value_of(w, Chunk<T>::one(z[v])), w * c.vocab + v};
+    }
+    return i % kBeamGroup == 0 ? Candidate{score[w], w * c.vocab + c.eos}
+                               : Candidate{kNone, INT64_MAX};
+  });
+  if (t < count) {
+    const bool there = t < l.taken;
+    const Candidate best = l.best[there ? t : 0];
+    const int64_t w = there ? best.at / c.vocab : -1, v = there ? best.at - w * c.vocab : -1;
+    const int64_t o = b * count + t;
+    c.out_scores[o] = there ? (float)best.value : kNegInf;
+    c.out_parents[o] = w;
+    c.out_tokens[o] = v;
+    if (c.out_finished != nullptr)
+      c.out_finished[o] = there && (v == c.eos || finished((int)w));
+  }
+}
+
+// ------------------------------------------------------------- reordering --
+constexpr int kForkThreads = 256;
+constexpr int kForkSteps = 4;
+constexpr int64_t kForkChunk = (int64_t)kForkThreads * kForkSteps * 16;  // bytes a block copies
+
+// Blocks: `chunks` of every new beam (the pools' slots one after another); the first
+// of them also writes the beam's slot and history.
+__global__ __launch_bounds__(kForkThreads) void beam_fork_kernel(const ForkCall c,
+                                                                 const int64_t chunks) {
+  const int64_t entry = blockIdx.x / chunks;
+  int64_t chunk = blockIdx.x - entry * chunks;
+  const int64_t b = entry / c.beams;
+  const int j = (int)(entry - b * c.beams), lane = threadIdx.x % kWave;
+  const int beams = (int)c.beams;
+  int64_t raw = -1, slot = -1;  // a lane to a beam
+  if (lane < beams) {
+    raw = c.parents[b * beams + lane];
+    slot = c.slots != nullptr ? c.slots[b * beams + lane] : b * beams + lane;
+  }
+  const bool valid = raw >= 0 && raw < beams;
+  const int parent = valid ? (int)raw : -1;
+  uint64_t keeps = 0, bare = 0;  // first children; old beams without a child
+  for (int w = 0; w < beams; ++w) {
+    const uint64_t children = __ballot(parent == w);
+    if (children != 0)
+      keeps |= children & -children;
+    else
+      bare |= uint64_t(1) << w;
+  }
+  const int from = __shfl(parent, j);
+  const int64_t source = from >= 0 ? __shfl(slot, from) : -1;
+  int to = from;
+  if (!(keeps >> j & 1)) {
+    // as many new beams before j keep nothing as bare beams come before its own
+    int skip = __popcll(~keeps & ((uint64_t(1) << j) - 1));
+    uint64_t left = bare;
+    while (skip-- > 0) left &= left - 1;
+    to = __ffsll((unsigned long long)left) - 1;
+  }
+  const int64_t target = __shfl(slot, to);
+  if (chunk == 0) {
+    if (threadIdx.x == 0) c.new_slots[entry] = target;
+    if (threadIdx.x < kWave && lane == j) {
+      const int bad = (!valid && raw != -1) + (c.pool_count > 0 && slot != -1 &&
+                                               (slot < 0 || slot >= c.slot_count));
+      count_errors(bad, c.err);
+    }
+    if (c.new_history != nullptr) {
+      const int64_t row = b * beams + (from >= 0 ? from : j);
+      const int64_t drop = c.history_len + 1 - c.new_len;
+      for (int64_t i = threadIdx.x; i < c.new_len; i += kForkThreads)
+        c.new_history[entry * c.new_len + i] =
+            i + 1 == c.new_len ? c.tokens[entry] : c.history[row * c.history_len + drop + i];
+    }
+  }
+  if (source < 0 || source >= c.slot_count || target < 0 || target >= c.slot_count ||
+      source == target)
+    return;
+  for (int p = 0; p < c.pool_count; ++p) {
+    const int64_t bytes = c.slot_bytes[p], mine = (bytes + kForkChunk - 1) / kForkChunk;
+    if (chunk >= mine) {
+      chunk -= mine;
+      continue;
+    }
+    const u32x4 *in = reinterpret_cast<const u32x4 *>(static_cast<char *>(c.pools[p]) +
+                                                      source * bytes);
+    u32x4 *out = reinterpret_cast<u32x4 *>(static_cast<char *>(c.pools[p]) + target * bytes);
+    const int64_t n = bytes / 16, at = chunk * (kForkChunk / 16) + threadIdx.x;
+    u32x4 v[kForkSteps];
+#pragma unroll
+    for (int k = 0; k < kForkSteps; ++k)
+      if (at + k * kForkThreads < n) v[k] = in[at + k * kForkThreads];
+#pragma unroll
+    for (int k = 0; k < kForkSteps; ++k)
+      if (at + k * kForkThreads < n) out[at + k * kForkThreads] = v[k];
+    return;
+  }
+}
+
+}  // namespace
+}  // namespace engram
+
+int engram::launch_beam_select(const BeamCall &c, void *stream) {
+  const int64_t rows = c.batch * c.beams;
+  const ScanShape shape = beam_shape(rows, c.vocab);
+  if (!grid_fits(rows * shape.segs, kScanThreads) || !grid_fits(c.batch, kChooseThreads))
+    return ENGRAM_EINVAL;
+  const float log2e = 1.44269504088896340736f;
+  const int64_t groups = ceil_div(c.vocab, kBeamGroup);
+  const ScanArgs s = {c.logits, c.vocab, c.stride, shape.segs, shape.seg_len, groups, log2e,
+                      c.scores, c.finished, c.parts, c.maxima};
+  const ChooseArgs a = {c, shape.segs, groups, log2e};
+  const dim3 grid((unsigned)(rows * shape.segs)), block(kScanThreads);
+  const dim3 sequences((unsigned)c.batch), wide(kChooseThreads);
+  if (c.type == ENGRAM_BF16) {
+    hipLaunchKernelGGL(beam_scan_kernel<uint16_t>, grid, block, 0, as_stream(stream), s);
+    hipLaunchKernelGGL(beam_choose_kernel<uint16_t>, sequences, wide, 0, as_stream(stream), a);
+  } else {
+    hipLaunchKernelGGL(beam_scan_kernel<float>, grid, block, 0, as_stream(stream), s);
+    hipLaunchKernelGGL(beam_choose_kernel<float>, sequences, wide, 0, as_stream(stream), a);
+  }
+  return launch_status();
+}
+
+int engram::launch_beam_fork(const ForkCall &c, void *stream) {
+  int64_t chunks = 0;
+  for (int p = 0; p < c.pool_count; ++p) chunks += ceil_div(c.slot_bytes[p], kForkChunk);
+  if (chunks < 1) chunks = 1;
+  const int64_t entries = c.batch * c.beams;
+  if (!mul_fits(entries, chunks, kMaxGridItems) || !grid_fits(entries * chunks, kForkThreads))
+    return ENGRAM_EINVAL;
+  hipLaunchKernelGGL(beam_fork_kernel, dim3((unsigned)(entries * chunks)), dim3(kForkThreads), 0,
+                     as_stream(stream), c, chunks);
+  return launch_status();
+}

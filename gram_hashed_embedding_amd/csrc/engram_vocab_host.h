@@ -1,0 +1,100 @@
+// engram_vocab_host.h -- the host side of the operators at the vocabulary's
+// end (include/engram_vocab.h) in plain C++: how rows of logits are cut, the
+// workspaces, and the launchers of the HIP sources.
+#pragma once
+
+#include "engram_layer_host.h"
+#include "engram_vocab.h"
+
+namespace engram {
+
+// A row of logits is read in chunks of 8 values, a lane to a chunk, by blocks
+// of kScanThreads lanes; a block's step takes kScanSteps chunks a lane.
+constexpr int kScanThreads = 256;
+constexpr int64_t kScanTile = 8 * kScanThreads;  // values
+constexpr int64_t kMaxVocab = int64_t(1) << 30;
+
+// Rows are cut into `segs` segments of seg_len values (a multiple of
+// kScanTile), a block to each.
+struct ScanShape {
+  int64_t segs, seg_len;
+};
+// At least `blocks` blocks where the rows are long enough, and segments of at
+// most `most` values.
+inline ScanShape scan_shape(int64_t rows, int64_t vocab, int64_t blocks, int64_t most) {
+  const int64_t tiles = ceil_div(vocab, kScanTile);
+  int64_t want = ceil_div(blocks, rows > 0 ? rows : 1);
+  if (want > tiles) want = tiles;
+  int64_t per = ceil_div(tiles, want);
+  if (per * kScanTile > most) per = most / kScanTile;
+  return {ceil_div(tiles, per), per * kScanTile};
+}
+
+// The sum of exp((z - max) / temperature) over a segment, beside its max.
+struct ScanPart {
+  double sum;
+  float max;
+  uint32_t pad;
+};
+
+// ------------------------------------------------------------ distillation --
+// One bit a value marks the ids that a teacher's row names, in LDS: 32 KB.
+constexpr int64_t kDistillMaxSeg = int64_t(1) << 18;
+constexpr int64_t kDistillBlocks = 1024;
+inline ScanShape distill_shape(int64_t rows, int64_t vocab) {
+  return scan_shape(rows, vocab, kDistillBlocks, kDistillMaxSeg);
+}
+// The parts of every segment, then the two fp32 statistics of each row for the
+// gradient; nothing where a block takes a whole row.
+inline size_t distill_workspace(int64_t rows, int64_t vocab) {
+  const ScanShape s = distill_shape(rows, vocab);
+  if (rows == 0 || s.segs == 1) return 0;
+  return (size_t)rows * (size_t)s.segs * sizeof(ScanPart) + (size_t)rows * 8;
+}
+
+// --------------------------------------------------------------- selection --
+// The scan leaves the largest logit of every kBeamGroup values.
+constexpr int64_t kBeamGroup = 128;
+constexpr int64_t kBeamBlocks = 1024;
+inline ScanShape beam_shape(int64_t rows, int64_t vocab) {
+  return scan_shape(rows, vocab, kBeamBlocks, kMaxVocab);
+}
+struct BeamCall {
+  const void *logits;
+  int32_t type;
+  int64_t stride;
+  const float *scores;
+  const uint8_t *finished;
+  int64_t eos, batch, beams, vocab, count;
+  float *out_scores;
+  int64_t *out_parents, *out_tokens;
+  uint8_t *out_finished;
+  ScanPart *parts;  // [batch * beams][segs]
+  float *maxima;    // [batch * beams][groups]
+};
+inline size_t beam_parts_bytes(int64_t rows, int64_t vocab) {
+  return (size_t)rows * (size_t)beam_shape(rows, vocab).segs * sizeof(ScanPart);
+}
+
+struct ForkCall {
+  const int64_t *parents, *slots;
+  int64_t batch, beams;
+  void *pools[ENGRAM_FORK_MAX_POOLS];
+  int64_t slot_bytes[ENGRAM_FORK_MAX_POOLS];
+  int32_t pool_count;
+  int64_t slot_count;
+  int64_t *new_slots;
+  const int64_t *tokens, *history;
+  int64_t history_len;
+  int64_t *new_history;
+  int64_t new_len;
+  int64_t *err;
+};
+
+// -------------------------------------------------------------- launchers --
+int launch_distill(const engram_distill_args &a);
+int launch_distill_backward(const engram_distill_args &a);
+int launch_beam_select(const BeamCall &c, void *stream);
+int launch_beam_fork(const ForkCall &c, void *stream);
+
+}  // namespace engram
