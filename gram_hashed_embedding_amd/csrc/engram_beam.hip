@@ -47,7 +47,7 @@ __device__ __forceinline__ float max16(float v) {
 
 template <class T>
 __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(const ScanArgs a) {
-  __shared__ RowSum sums[kScanThreads / kWave];
+  __shared__ double part[kScanThreads / kWave];
   const int64_t row = blockIdx.x / a.segs, seg = blockIdx.x - row * a.segs;
   if (!beam_live(a.scores, a.finished, row)) return;
   const int64_t lo = seg * a.seg_len, hi = lo + a.seg_len < a.vocab ? lo + a.seg_len : a.vocab;
@@ -67,9 +67,9 @@ __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(const ScanArgs 
     }
     const float ref = run.raise(m, a.c);
 #pragma unroll
-    for (int u = 0; u < U; ++u) run.add(z[u], a.c, ref);
+    for (int u = 0; u < U; ++u) run.add(z[u], ref, a.c);
   });
-  const RowSum s = block_join<kScanThreads>(RowSum{run.max, (double)run.sum}, a.c, sums);
+  const RowSum s = block_join<kScanThreads>(run, a.c, part);
   if (threadIdx.x == 0) a.parts[row * a.segs + seg] = {s.sum, s.max, 0u};
 }
 
@@ -96,20 +96,29 @@ struct ChooseLds {
   int listed, taken;
 };
 
-// The first `count` of the candidates 0 .. n-1 (get(i), value kNone where there is
-// none), in order, in l.best[0 .. l.taken).
+// The first `count` of the candidates 0 .. n-1 (value_at(i), kNone where there is none, and
+// place_at(i)), in order, in l.best[0 .. l.taken).
 //
 // A threshold first: of the largest values of 64 rows of 16 threads, the count-th
 // largest has at least `count` values at or above it.  What reaches it is listed and
 // ranked by counting.  More than the list holds (long runs of equal values) are taken
-// one at a time instead, each the first after the one before.
-template <class GET>
-__device__ void choose(ChooseLds &l, int64_t n, int count, GET get) {
+// one at a time instead, each the first after the one before.  A thread keeps its
+// first kKeep values; their loads go out together.
+constexpr int kKeep = 12;
+template <class VALUE, class PLACE>
+__device__ void choose(ChooseLds &l, int n, int count, VALUE value_at, PLACE place_at) {
   const int t = threadIdx.x;
-  double mine = kNone;
-  for (int64_t i = t; i < n; i += kChooseThreads) mine = fmax(mine, get(i).value);
+  double kept[kKeep], mine = kNone;
 #pragma unroll
-  for (int d = 1; d < 16; d *= 2) mine = fmax(mine, __shfl_xor(mine, d));
+  for (int k = 0; k < kKeep; ++k) {
+    const int i = t + k * kChooseThreads;
+    kept[k] = i < n ? value_at(i) : kNone;
+  }
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k) mine = fmax(mine, kept[k]);
+  for (int i = t + kKeep * kChooseThreads; i < n; i += kChooseThreads)
+    mine = fmax(mine, value_at(i));
+  mine = lanes_reduce<16>(mine, [](double a, double b) { return fmax(a, b); });
   if (t % 16 == 0) l.row_best[t / 16] = mine;
   if (t == 0) l.listed = 0;
   __syncthreads();
@@ -125,19 +134,22 @@ __device__ void choose(ChooseLds &l, int64_t n, int count, GET get) {
   }
   __syncthreads();
   const double least = l.threshold;
-  for (int64_t i = t; i < n; i += kChooseThreads) {
-    const Candidate c = get(i);
-    if (c.value > kNone && c.value >= least) {
+  const auto list = [&](int i, double v) {
+    if (v > kNone && v >= least) {
       const int k = atomicAdd(&l.listed, 1);
-      if (k < kChooseList) l.list[k] = c;
+      if (k < kChooseList) l.list[k] = {v, place_at(i)};
     }
-  }
+  };
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k) list(t + k * kChooseThreads, kept[k]);
+  for (int i = t + kKeep * kChooseThreads; i < n; i += kChooseThreads) list(i, value_at(i));
   __syncthreads();
   const int listed = l.listed;
   if (listed <= kChooseList) {
     for (int k = t; k < listed; k += kChooseThreads) {
       const Candidate c = l.list[k];
       int ahead = 0;
+#pragma unroll 4
       for (int o = 0; o < listed; ++o) ahead += before(l.list[o], c);
       if (ahead < count) l.best[ahead] = c;
     }
@@ -149,9 +161,12 @@ __device__ void choose(ChooseLds &l, int64_t n, int count, GET get) {
   Candidate last = {__builtin_inf(), -1};
   for (int r = 0; r < count; ++r) {
     Candidate m = {kNone, INT64_MAX};
-    for (int64_t i = t; i < n; i += kChooseThreads) {
-      const Candidate c = get(i);
-      if (c.value > kNone && before(last, c) && before(c, m)) m = c;
+    for (int i = t; i < n; i += kChooseThreads) {
+      const double v = value_at(i);
+      if (v > kNone && v <= last.value && v >= m.value) {
+        const Candidate c = {v, place_at(i)};
+        if (before(last, c) && before(c, m)) m = c;
+      }
     }
 #pragma unroll
     for (int d = 1; d < kWave; d *= 2) {
@@ -173,6 +188,7 @@ __device__ void choose(ChooseLds &l, int64_t n, int count, GET get) {
 struct ChooseArgs {
   BeamCall c;
   int64_t segs, groups;
+  uint32_t per_group;  // 2^32 / groups, rounded down
   float log2e;
 };
 
@@ -181,7 +197,8 @@ __global__ __launch_bounds__(kChooseThreads) void beam_choose_kernel(const Choos
   __shared__ ChooseLds l;
   __shared__ double lse[ENGRAM_BEAM_MAX];    // NaN: no candidate but a finished beam's
   __shared__ double score[ENGRAM_BEAM_MAX];
-  __shared__ int64_t group_at[ENGRAM_BEAM_MAX];
+  __shared__ int64_t group_at[ENGRAM_BEAM_MAX];  // of each chosen group: its first value
+  __shared__ int group_beam[ENGRAM_BEAM_MAX];
   const BeamCall &c = a.c;
   const int64_t b = blockIdx.x, first_row = b * c.beams;
   const int t = threadIdx.x, beams = (int)c.beams, count = (int)c.count;
@@ -190,13 +207,7 @@ __global__ __launch_bounds__(kChooseThreads) void beam_choose_kernel(const Choos
     const int64_t row = first_row + w;
     double v = __builtin_nan("");
     if (beam_live(c.scores, c.finished, row)) {
-      RowSum s = {kNegInf, 0.0};
-      for (int64_t i = t % kWave; i < a.segs; i += kWave) {
-        const ScanPart p = c.parts[row * a.segs + i];
-        s = join_sums(s, RowSum{p.max, p.sum}, a.log2e);
-      }
-      s = wave_join(s, a.log2e);
-      v = log_sum(s, 1.0, a.log2e);
+      v = log_sum(wave_join(c.parts + row * a.segs, a.segs, a.log2e), 1.0);
       if (!__builtin_isfinite(v)) v = __builtin_nan("");
     }
     if (t % kWave == 0) {
@@ -206,40 +217,49 @@ __global__ __launch_bounds__(kChooseThreads) void beam_choose_kernel(const Choos
   }
   __syncthreads();
   // the best groups; a finished beam's candidate is a group of its own (its first)
-  const int64_t groups = a.groups;
+  const int groups = (int)a.groups;
   const auto value_of = [&](int w, float z) {
     const double v = score[w] + ((double)z - lse[w]);
     return v == v ? v : kNone;
   };
   const auto finished = [&](int w) {
     return c.finished != nullptr && c.finished[first_row + w] != 0 &&
-           __builtin_isfinite(c.scores[first_row + w]);
+           __builtin_isfinite(score[w]);
   };
-  choose(l, beams * groups, count, [&](int64_t i) {
-    const int w = (int)(i / groups);
-    const int64_t g = i - w * groups;
-    double v = kNone;
-    if (lse[w] == lse[w])
-      v = value_of(w, c.maxima[(first_row + w) * groups + g]);
-    else if (g == 0 && finished(w))
-      v = score[w];
-    return Candidate{v, i};
-  });
+  // i / groups by the whole part of 2^32 / groups, which is at most one too small
+  const auto beam_of = [&](uint32_t i) {
+    const uint32_t w = __umulhi(i, a.per_group);
+    return (int)(i - w * groups >= (uint32_t)groups ? w + 1 : w);
+  };
+  choose(
+      l, beams * groups, count,
+      [&](int i) {
+        const int w = beam_of(i);
+        if (lse[w] == lse[w]) return value_of(w, c.maxima[first_row * groups + i]);
+        return i == w * groups && finished(w) ? score[w] : kNone;
+      },
+      [&](int i) { return (int64_t)i; });
   const int chosen = l.taken;
-  if (t < chosen) group_at[t] = l.best[t].at;
+  if (t < chosen) {
+    const int at = (int)l.best[t].at, w = beam_of(at);
+    group_beam[t] = w;
+    group_at[t] = (int64_t)(at - w * groups) * kBeamGroup;
+  }
   __syncthreads();
-  choose(l, chosen * kBeamGroup, count, [&](int64_t i) {
-    const int64_t place = group_at[i / kBeamGroup];
-    const int w = (int)(place / groups);
-    const int64_t v = (place - w * groups) * kBeamGroup + i % kBeamGroup;
-    if (lse[w] == lse[w]) {
-      if (v >= c.vocab) return Candidate{kNone, INT64_MAX};
-      const T *z = static_cast<const T *>(c.logits) + (first_row + w) * c.stride;
-      return Candidate{value_of(w, Chunk<T>::one(z[v])), w * c.vocab + v};
-    }
-    return i % kBeamGroup == 0 ? Candidate{score[w], w * c.vocab + c.eos}
-                               : Candidate{kNone, INT64_MAX};
-  });
+  choose(
+      l, chosen * (int)kBeamGroup, count,
+      [&](int i) {
+        const int w = group_beam[i / kBeamGroup], k = i % kBeamGroup;
+        const int64_t v = group_at[i / kBeamGroup] + k;
+        if (lse[w] != lse[w]) return k == 0 ? score[w] : kNone;
+        if (v >= c.vocab) return kNone;
+        const T *z = static_cast<const T *>(c.logits) + (first_row + w) * c.stride;
+        return value_of(w, Chunk<T>::one(z[v]));
+      },
+      [&](int i) {
+        const int w = group_beam[i / kBeamGroup];
+        return w * c.vocab + (lse[w] != lse[w] ? c.eos : group_at[i / kBeamGroup] + i % kBeamGroup);
+      });
   if (t < count) {
     const bool there = t < l.taken;
     const Candidate best = l.best[there ? t : 0];
@@ -344,7 +364,9 @@ int engram::launch_beam_select(const BeamCall &c, void *stream) {
   const int64_t groups = ceil_div(c.vocab, kBeamGroup);
   const ScanArgs s = {c.logits, c.vocab, c.stride, shape.segs, shape.seg_len, groups, log2e,
                       c.scores, c.finished, c.parts, c.maxima};
-  const ChooseArgs a = {c, shape.segs, groups, log2e};
+  const ChooseArgs a = {c, shape.segs, groups,
+                        groups > 1 ? (uint32_t)((uint64_t(1) << 32) / groups) : 0xffffffffu,
+                        log2e};
   const dim3 grid((unsigned)(rows * shape.segs)), block(kScanThreads);
   const dim3 sequences((unsigned)c.batch), wide(kChooseThreads);
   if (c.type == ENGRAM_BF16) {

@@ -2,13 +2,17 @@
 // every row, its gradient, or both, for gfx950.  What is computed is stated
 // with engram_distill in include/engram_vocab.h.
 //
-// The vocabulary's part is one pass over a row's logits for the sum of their
-// exponentials, and one that writes the gradient.  With r (the teacher's mass
-// on the ids it does not name) the first pass leaves the named ids out: s and
-// the sum of all are then sums of positive terms, and s - r, which the
-// gradient of the others is made of, keeps its digits when s is near r.  The
-// second pass treats every id as unnamed; the few named ones are written
-// after it.
+// With N the ids that a row's teacher names and R the others, the sums
+//     S_R = sum over R of exp(z / T),  S_N the same over N
+// are kept apart: S_R is the pass over the vocabulary, in fp32 terms, S_N a few
+// terms in fp64.  The named ids are where a row's large terms lie, so lse =
+// log(S_R + S_N) keeps its digits, and so do s = S_R / (S_R + S_N) and s - r,
+// which the gradient of the unnamed ids is made of.  The gradient is written
+// for every id as if it were unnamed; the few named ones are written after it.
+//
+// A block holds its whole row in registers between the two passes, so a row is
+// read once (distill_hold_kernel); rows that no block can hold are read again
+// for the gradient.
 #include "engram_vocab_dev.h"
 
 namespace engram {
@@ -17,7 +21,7 @@ namespace {
 struct DistillArgs {
   int64_t vocab, top, stride, grad_stride, segs, seg_len;
   float temperature, c;  // c = log2(e) / temperature
-  int rest;
+  int teacher_type, rest;
   const void *logits;
   const int64_t *ids;
   const void *teacher;
@@ -28,21 +32,42 @@ struct DistillArgs {
   ScanPart *parts;
 };
 
-// What a block keeps of the teacher's row in LDS, `top` values each.
+// What a block keeps of the teacher's row in LDS, `top` values each, and behind
+// them one bit a value of its part of the vocabulary: whether it is named.
 struct Entries {
-  double *p;     // the entry's probability; after merge(), its id's
-  int32_t *ids;  // -1: unused; after merge(), also where an earlier entry has the id
-  float *z;      // the student's logit
+  double *p;      // the probability of the entry, then of its id; where there is one
+  int32_t *ids;   // -1: unused, or an earlier entry has the id
+  float *z;       // the student's logit
+  uint32_t *bits;
   __device__ Entries(char *lds, int64_t top)
       : p(reinterpret_cast<double *>(lds)), ids(reinterpret_cast<int32_t *>(p + top)),
-        z(reinterpret_cast<float *>(ids + top)) {}
+        z(reinterpret_cast<float *>(ids + top)), bits(reinterpret_cast<uint32_t *>(z + top)) {}
 };
 constexpr size_t kEntryBytes = 16;
 
-template <class T>
-__device__ __forceinline__ float teacher_value(const void *p, int64_t i) {
-  return Chunk<T>::one(static_cast<const T *>(p)[i]);
-}
+// An entry as it is loaded; a lane has up to kMost of them.
+template <int THREADS>
+struct RawEntries {
+  static constexpr int kMost = ENGRAM_DISTILL_MAX_TOP / THREADS;
+  int64_t id[kMost];
+  float y[kMost], lse, weight;
+  __device__ __forceinline__ void load(const DistillArgs &a, int64_t row) {
+    lse = a.teacher_lse != nullptr ? a.teacher_lse[row] : 0.0f;
+    weight = a.grad_loss != nullptr ? a.grad_loss[row] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) {
+      const int64_t j = threadIdx.x + k * THREADS;
+      id[k] = -1;
+      y[k] = kNegInf;
+      if (j < a.top) {
+        id[k] = a.ids[row * a.top + j];
+        y[k] = a.teacher_type == ENGRAM_BF16
+                   ? bf16_lo(static_cast<const uint16_t *>(a.teacher)[row * a.top + j])
+                   : static_cast<const float *>(a.teacher)[row * a.top + j];
+      }
+    }
+  }
+};
 
 // The teacher's row: m, r, and whether it has a target at all.
 struct Target {
@@ -50,316 +75,446 @@ struct Target {
   bool none;
 };
 
-template <class Y>
-__device__ Target read_target(const DistillArgs &a, int64_t row, Entries e, double *part,
+// Fills e.ids and e.p; with `words` of bits, marks the ids that lie in [lo, hi).
+// Entries of one id become one, the first, with their sum in their order.
+template <int THREADS>
+__device__ __forceinline__ Target read_target(const DistillArgs &a, int64_t row, const RawEntries<THREADS> &raw,
+                              int64_t lo, int64_t hi, int words, Entries e, double *part,
                               int64_t *err) {
+  constexpr int kMost = RawEntries<THREADS>::kMost;
+  __shared__ int flags;  // 1: an entry is used, 2: an id may repeat
   const double T = a.temperature;
+  const int top = (int)a.top;
+  if (threadIdx.x == 0) flags = words > 0 ? 0 : 2;
+  for (int i = threadIdx.x; i < words; i += THREADS) e.bits[i] = 0u;
   double most = -__builtin_inf();
-  int used = 0, bad = 0;
-  for (int64_t j = threadIdx.x; j < a.top; j += kScanThreads) {
-    const int64_t id = a.ids[row * a.top + j];
-    const bool ok = id >= 0 && id < a.vocab;
-    bad += !ok && id != -1;
-    used |= ok;
-    const double y = ok ? teacher_value<Y>(a.teacher, row * a.top + j) / T : -__builtin_inf();
-    e.ids[j] = ok ? (int32_t)id : -1;
-    e.p[j] = y;
-    most = fmax(most, y);
+  int bad = 0, seen = 0;
+#pragma unroll
+  for (int k = 0; k < kMost; ++k) {
+    const int j = threadIdx.x + k * THREADS;
+    if (j < top) {
+      const int64_t id = raw.id[k];
+      const bool ok = id >= 0 && id < a.vocab;
+      bad += !ok && id != -1;
+      seen |= ok;
+      const double y = ok ? raw.y[k] / T : -__builtin_inf();
+      e.ids[j] = ok ? (int32_t)id : -1;
+      e.p[j] = y;
+      most = fmax(most, y);
+    }
   }
   count_errors(bad, err);
   double ref;
   if (a.teacher_lse != nullptr) {
-    ref = a.teacher_lse[row];
+    ref = raw.lse;
+    __syncthreads();
   } else {
-    ref = block_max<kScanThreads>(most, part);
+    ref = block_max<THREADS>(most, part);
     if (ref == -__builtin_inf()) ref = 0.0;
   }
   double sum = 0.0;
-  for (int64_t j = threadIdx.x; j < a.top; j += kScanThreads) {
-    const double p = e.ids[j] >= 0 ? exp(e.p[j] - ref) : 0.0;
+  for (int j = threadIdx.x; j < top; j += THREADS) {
+    const int32_t id = e.ids[j];
+    const double p = id >= 0 ? exp64(e.p[j] - ref) : 0.0;
     e.p[j] = p;
     sum += p;
+    if (words > 0 && id >= lo && id < hi) {
+      const uint32_t bit = 1u << ((id - lo) & 31);
+      if (atomicOr(&e.bits[(id - lo) >> 5], bit) & bit) seen |= 2;
+    }
   }
-  sum = block_sum<kScanThreads>(sum, part);
-  Target t = {sum, 0.0, __syncthreads_or(used) == 0};
+  if (seen != 0) atomicOr(&flags, seen);
+  sum = block_sum<THREADS>(sum, part);
+  Target t = {sum, 0.0, (flags & 1) == 0};
   if (a.teacher_lse == nullptr) {
     t.none |= sum == 0.0;
-    for (int64_t j = threadIdx.x; j < a.top; j += kScanThreads)
-      if (sum != 0.0) e.p[j] /= sum;
+    if (sum != 0.0)
+      for (int j = threadIdx.x; j < top; j += THREADS) e.p[j] /= sum;
     t.m = sum == 0.0 ? 0.0 : sum / sum;
   } else if (a.rest) {
     // (a smaller difference from 1 is what rounding teacher_lse to fp32 leaves)
     const double r = 1.0 - sum;
     t.r = !t.none && r >= 0x1p-20 ? r : 0.0;
   }
+  if ((flags & 2) != 0) {
+    __syncthreads();
+    double p[kMost];
+    bool first[kMost];
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) {
+      const int j = threadIdx.x + k * THREADS;
+      const int32_t id = j < top ? e.ids[j] : -1;
+      double total = 0.0;
+      bool least = true;
+      if (id >= 0)
+        for (int i = 0; i < top; ++i)
+          if (e.ids[i] == id) {
+            total += e.p[i];
+            least &= i >= j;
+          }
+      p[k] = total;
+      first[k] = least;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) {
+      const int j = threadIdx.x + k * THREADS;
+      if (j < top) {
+        e.p[j] = p[k];
+        if (!first[k]) e.ids[j] = -1;
+      }
+    }
+  }
   __syncthreads();
   return t;
 }
 
-// Entries of one id become one: the first has their sum, in their order.
-__device__ void merge(int64_t top, Entries e) {
-  constexpr int kMost = ENGRAM_DISTILL_MAX_TOP / kScanThreads;
-  double p[kMost];
-  bool first[kMost];
+// -inf in the place of a chunk's named values.
+__device__ __forceinline__ void leave_out(float (&z)[8], uint32_t named) {
+  if (named != 0u)
 #pragma unroll
-  for (int k = 0; k < kMost; ++k) {
-    const int64_t j = threadIdx.x + k * kScanThreads;
-    p[k] = 0.0;
-    first[k] = true;
-    if (j >= top) continue;
-    const int32_t id = e.ids[j];
-    if (id < 0) continue;
-    for (int64_t i = 0; i < top; ++i)
-      if (e.ids[i] == id) {
-        p[k] += e.p[i];
-        first[k] &= i >= j;
-      }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < kMost; ++k) {
-    const int64_t j = threadIdx.x + k * kScanThreads;
-    if (j >= top) continue;
-    e.p[j] = p[k];
-    if (!first[k]) e.ids[j] = -1;
-  }
-  __syncthreads();
+    for (int k = 0; k < 8; ++k)
+      if (named >> k & 1u) z[k] = kNegInf;
 }
 
-// One bit a value of the segment [lo, hi) that the teacher names.
-__device__ void mark_named(uint32_t *bits, int64_t words, const int64_t *ids, int64_t top,
-                           int64_t lo, int64_t hi) {
-  for (int64_t i = threadIdx.x; i < words; i += kScanThreads) bits[i] = 0u;
-  __syncthreads();
-  for (int64_t j = threadIdx.x; j < top; j += kScanThreads) {
-    const int64_t id = ids[j] - lo;
-    if (id >= 0 && id < hi - lo) atomicOr(&bits[id >> 5], 1u << (id & 31));
-  }
-  __syncthreads();
-}
-
-// The sum over a segment, the named values left out with REST.
-template <class T, bool REST>
-__device__ __forceinline__ RowSum scan_segment(const T *row, int64_t lo, int64_t hi, float c,
-                                               const uint8_t *bits, RowSum *part) {
-  constexpr int U = sizeof(T) == 2 ? 4 : 2;
-  Running run;
-  each_chunks<T, U>(row, lo, hi, [&](int64_t at, float (&z)[U][8]) {
-    if (REST) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t i = at + u * kScanTile + 8 * threadIdx.x;
-        const uint32_t named = i < hi ? bits[(i - lo) >> 3] : 0u;
-        if (named != 0u)
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (named >> k & 1u) z[u][k] = kNegInf;
-      }
-    }
-    float m = run.max;
-#pragma unroll
-    for (int u = 0; u < U; ++u) m = max8(m, z[u]);
-    const float ref = run.raise(m, c);
-#pragma unroll
-    for (int u = 0; u < U; ++u) run.add(z[u], c, ref);
-  });
-  return block_join<kScanThreads>(RowSum{run.max, (double)run.sum}, c, part);
-}
-
-struct RowStats {
-  double lse, lse_rest;
+// The sum over both sides, taken from the larger maximum, and the unnamed side's share in
+// it (none in an empty sum).
+struct Whole {
+  RowSum all;
+  double s;
 };
-
-// log(q) of a value, log(s): with no finite logit at all every q is 0.
-__device__ __forceinline__ double log_share(double x, double lse) {
-  return lse == -__builtin_inf() ? lse : x - lse;
+__device__ __forceinline__ Whole both(const RowSum &rest, const RowSum &named, double T) {
+  const bool up = rest.max >= named.max;
+  const double d = up ? (double)named.max - (double)rest.max
+                      : (double)rest.max - (double)named.max;
+  const double w = rest.max == named.max ? 1.0 : exp64(d / T);  // (two empty sides are level)
+  const double a = up ? rest.sum : rest.sum * w, b = up ? named.sum * w : named.sum;
+  const double sum = a + b;
+  return {{up ? rest.max : named.max, sum}, sum == 0.0 ? 0.0 : a / sum};
 }
 
-// The row's statistics from its sum (of the unnamed values with REST) and its loss.
-template <class T, bool REST>
-__device__ RowStats finish_row(const DistillArgs &a, int64_t row, const RowSum &sum, Entries e,
-                               const Target &t, double *part) {
-  const double T_ = a.temperature;
-  const T *z = static_cast<const T *>(a.logits) + row * a.stride;
-  for (int64_t j = threadIdx.x; j < a.top; j += kScanThreads)
-    e.z[j] = e.ids[j] >= 0 ? Chunk<T>::one(z[e.ids[j]]) : kNegInf;
-  RowStats s;
-  s.lse = s.lse_rest = log_sum(sum, T_, a.c);
-  if (REST) {
-    double most = -__builtin_inf(), named = 0.0;
-    for (int64_t j = threadIdx.x; j < a.top; j += kScanThreads)
-      most = fmax(most, e.z[j] / T_);
-    most = block_max<kScanThreads>(most, part);
-    const double ref = most == -__builtin_inf() ? 0.0 : most;
-    for (int64_t j = threadIdx.x; j < a.top; j += kScanThreads)
-      if (e.ids[j] >= 0) named += exp(e.z[j] / T_ - ref);
-    named = block_sum<kScanThreads>(named, part);
-    // log(exp(lse_rest) + named * exp(ref)), from the larger of the two
-    const double ln = ref + log(named);
-    if (named == 0.0)
-      s.lse = s.lse_rest;
-    else if (s.lse_rest > ln)
-      s.lse = s.lse_rest + log1p(exp(ln - s.lse_rest));
-    else
-      s.lse = ln + log1p(exp(s.lse_rest - ln));
+// The named logits' sum, in fp64, over the block; e.z is read by its own lanes.
+template <int THREADS>
+__device__ __forceinline__ RowSum sum_named(const DistillArgs &a, Entries e, double *part) {
+  const int top = (int)a.top;
+  float m = kNegInf;
+  for (int j = threadIdx.x; j < top; j += THREADS) m = max3(m, e.z[j], kNegInf);
+  m = block_max<THREADS>(m, reinterpret_cast<float *>(part));
+  double sum = 0.0;
+  for (int j = threadIdx.x; j < top; j += THREADS)
+    if (e.ids[j] >= 0) sum += exp64(((double)e.z[j] - (double)ref_of(m)) / a.temperature);
+  return {m, block_sum<THREADS>(sum, part)};
+}
+
+// Loss and statistics of a row, written.
+template <int THREADS>
+__device__ __forceinline__ void write_row(const DistillArgs &a, int64_t row, const RowSum &rest,
+                          const RowSum &all, Entries e, const Target &t, double *part) {
+  const double T = a.temperature;
+  const double none = -__builtin_inf();
+  const int top = (int)a.top;
+  double loss = 0.0, lse = 0.0;
+  if (threadIdx.x < (unsigned)top) {  // (the first lane is one of them)
+    lse = log_sum(all, T);
+    if (a.loss != nullptr)
+      for (int j = threadIdx.x; j < top; j += THREADS) {
+        const double p = e.p[j];
+        if (e.ids[j] >= 0 && p != 0.0)
+          // (where no logit is finite every q is 0)
+          loss += p * (log(p) - (lse == none ? none : e.z[j] / T - lse));
+      }
   }
+  if (a.loss != nullptr) loss = block_sum<THREADS>(loss, part);
+  if (threadIdx.x != 0) return;
+  if (a.lse != nullptr) a.lse[row] = (float)lse;
+  const double lse_rest = a.rest ? log_sum(rest, T) : 0.0;
+  if (a.rest && a.lse_rest != nullptr) a.lse_rest[row] = (float)lse_rest;
   if (a.loss != nullptr) {
-    double loss = 0.0;
-    for (int64_t j = threadIdx.x; j < a.top; j += kScanThreads)
-      if (e.ids[j] >= 0 && e.p[j] != 0.0)
-        loss += e.p[j] * (log(e.p[j]) - log_share(e.z[j] / T_, s.lse));
-    loss = block_sum<kScanThreads>(loss, part);
-    if (REST && t.r != 0.0) loss += t.r * (log(t.r) - log_share(s.lse_rest, s.lse));
-    if (threadIdx.x == 0) a.loss[row] = t.none ? 0.0f : (float)loss;
+    if (t.r != 0.0) loss += t.r * (log(t.r) - (lse_rest == none ? none : lse_rest - lse));
+    a.loss[row] = t.none ? 0.0f : (float)loss;
   }
-  if (threadIdx.x == 0) {
-    if (a.lse != nullptr) a.lse[row] = (float)s.lse;
-    if (REST && a.lse_rest != nullptr) a.lse_rest[row] = (float)s.lse_rest;
-  }
-  return s;
 }
 
-// Stores of eight values, or of the last ones before hi.
-__device__ __forceinline__ void store8(uint16_t *p, const float (&v)[8], int64_t left) {
+// ------------------------------------------------------------ held rows --
+__device__ __forceinline__ void store8(uint16_t *p, const float (&v)[8]) {
   const u32x4 w = pack_bf16x8(v);
-  if (left >= 8) {
-    __builtin_memcpy(p, &w, 16);
-  } else {
-    const uint32_t h[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < left) p[e] = (uint16_t)(h[e / 2] >> (16 * (e % 2)));
-  }
+  __builtin_memcpy(p, &w, 16);
 }
-__device__ __forceinline__ void store8(float *p, const float (&v)[8], int64_t left) {
-  if (left >= 8) {
-    __builtin_memcpy(p, v, 32);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < left) p[e] = v[e];
-  }
+__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
+  __builtin_memcpy(p, v, 32);
 }
 __device__ __forceinline__ void store1(uint16_t *p, float v) { *p = (uint16_t)pack_bf16(v, 0.0f); }
 __device__ __forceinline__ void store1(float *p, float v) { *p = v; }
 
-// The gradient of the values [lo, hi) of a row.  Every value is first written as
-// an unnamed one,
-//     factor * exp(z / temperature - base),
-// base the log of the sum of all (of the unnamed with REST, whose share s makes
-// factor = g / temperature * ((m + r) s - r)): one subtraction, product, v_exp_f32
-// and product.  The named ones follow.
-template <class T, bool REST>
-__device__ void write_gradient(const DistillArgs &a, int64_t row, int64_t lo, int64_t hi,
-                               const RowStats &s, Entries e, const Target &t) {
-  const double T_ = a.temperature;
-  const T *zrow = static_cast<const T *>(a.logits) + row * a.stride;
-  T *grow = static_cast<T *>(a.grad) + row * a.grad_stride;
-  const float g = a.grad_loss[row];
-  constexpr int U = sizeof(T) == 2 ? 4 : 2;
-  if (g == 0.0f || t.none) {
-    const float zero[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t i = lo + 8 * threadIdx.x; i < hi; i += kScanTile) store8(grow + i, zero, hi - i);
-    return;
+// The n >= 8 values of a row that start at `row`, in the registers of a block: chunk k
+// of a lane starts at 8 * (k * THREADS + lane).  A chunk that would pass the end is the
+// last eight values instead, of which those before its start are not its own, so
+// every load is made, in a row, at an address inside.
+template <class T, int THREADS, int N>
+struct Held {
+  Chunk<T> r[N];
+  // whether any lane has values in chunk k; whether all have eight (uniform)
+  __device__ static __forceinline__ bool any(int n, int k) { return 8 * k * THREADS < n; }
+  __device__ static __forceinline__ bool full(int n, int k) { return 8 * (k + 1) * THREADS <= n; }
+  // the lane, hidden from the compiler, which would keep the places of the loads in
+  // registers for the next use
+  __device__ static __forceinline__ int own_lane() {
+    int lane = threadIdx.x;
+    asm volatile("" : "+v"(lane));
+    return lane;
   }
-  const double gt = g / T_, base = REST ? s.lse_rest : s.lse;
-  const bool empty = base == -__builtin_inf();
-  const float r0 = empty || base != base ? 0.0f : (float)(base * T_);
-  double f = gt * t.m;
-  if (REST) f = gt * ((t.m + t.r) * (empty ? 0.0 : exp(s.lse_rest - s.lse)) - t.r);
-  const float factor = empty ? 0.0f : (float)(f * exp(r0 / T_ - base));
-  each_chunks<T, U>(zrow, lo, hi, [&](int64_t at, float (&z)[U][8]) {
+  // the address of a value: a uniform base and 32 bits of a lane's own
+  __device__ static __forceinline__ const T *value(const T *row, uint32_t at) {
+    return reinterpret_cast<const T *>(reinterpret_cast<const char *>(row) +
+                                       (uint32_t)(at * sizeof(T)));
+  }
+  // where the eight values of a lane's chunk lie; its own start `first` (at most 8) later
+  __device__ static __forceinline__ uint32_t place(int n, int k, int lane) {
+    const int at = 8 * (k * THREADS + lane);
+    return (uint32_t)(at + 8 <= n ? at : n - 8);
+  }
+  __device__ static __forceinline__ int first(int n, int k, int lane) {
+    const int over = 8 * (k * THREADS + lane) + 8 - n;
+    return over <= 0 ? 0 : over < 8 ? over : 8;
+  }
+  __device__ __forceinline__ void load(const T *row, int n) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t i = at + u * kScanTile + 8 * threadIdx.x;
+    for (int k = 0; k < N; ++k) r[k].load(value(row, place(n, k, threadIdx.x)));
+  }
+
+  // The running sum of the unnamed values.
+  __device__ __forceinline__ void sum(int n, float c, const uint32_t *bits, Running &run) const {
+    const uint8_t *bytes = reinterpret_cast<const uint8_t *>(bits);
+    constexpr int G = sizeof(T) == 2 ? 2 : 1;
+    static_assert(N % G == 0, "whole groups");
+    const int lane = own_lane();
 #pragma unroll
-      for (int k = 0; k < 8; ++k) z[u][k] = factor * exp2_fast((z[u][k] - r0) * a.c);
-      if (i < hi) store8(grow + i, z[u], hi - i);
+    for (int g = 0; g < N; g += G) {
+      if (full(n, g + G - 1)) {
+        float z[G][8], m = run.max;
+#pragma unroll
+        for (int u = 0; u < G; ++u) {
+          r[g + u].values(z[u]);
+          leave_out(z[u], bytes[(g + u) * THREADS + lane]);
+          m = max8(m, z[u]);
+        }
+        const float ref = run.raise(m, c);
+#pragma unroll
+        for (int u = 0; u < G; ++u) run.add(z[u], ref, c);
+      } else {
+#pragma unroll
+      for (int u = 0; u < G; ++u)
+        if (any(n, g + u)) {
+          float z[8];
+          r[g + u].values(z);
+          const int from = first(n, g + u, lane);
+          const uint32_t at = place(n, g + u, lane);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i < from || (bits[(at + i) >> 5] >> ((at + i) & 31) & 1u)) z[i] = kNegInf;
+          run.add(z, run.raise(max8(run.max, z), c), c);
+        }
+      }
     }
-  });
-  __syncthreads();
-  for (int64_t j = threadIdx.x; j < a.top; j += kScanThreads) {
+  }
+
+  // factor * exp((z - ref) / T) in the place of every value.  (The values are unpacked
+  // and placed anew: kept from the sum they would take twice the registers.)
+  __device__ __forceinline__ void write(T *row, int n, float factor, float ref, float c) {
+    const int lane = own_lane();
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      if (any(n, k)) {
+        r[k].renew();
+        float z[8];
+        r[k].values(z);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] = factor * exp2_fast((z[i] - ref) * c);
+        T *to = const_cast<T *>(value(row, place(n, k, lane)));
+        const int from = full(n, k) ? 0 : first(n, k, lane);
+        if (from == 0) {
+          store8(to, z);
+        } else {
+#pragma unroll
+          for (int i = 1; i < 8; ++i)
+            if (i >= from) store1(to + i, z[i]);
+        }
+      }
+    }
+  }
+};
+
+template <class T>
+__device__ __forceinline__ void write_zeros(T *row, int64_t lo, int64_t hi, int threads) {
+  const float zero[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  for (int64_t i = lo + 8 * threadIdx.x; i < hi; i += 8 * threads) {
+    if (i + 8 <= hi)
+      store8(row + i, zero);
+    else
+      for (int64_t j = i; j < hi; ++j) store1(row + j, 0.0f);
+  }
+}
+
+// The gradient of the named values in [lo, hi): q by q_of(z).
+template <class T, int THREADS, class Q>
+__device__ __forceinline__ void write_named(const DistillArgs &a, T *row, int64_t lo, int64_t hi,
+                                            double gt, Entries e, const Target &t, Q q_of) {
+  for (int j = threadIdx.x; j < (int)a.top; j += THREADS) {
     const int32_t id = e.ids[j];
-    if (id < lo || id >= hi) continue;
-    const double q = s.lse == -__builtin_inf() ? 0.0 : exp(e.z[j] / T_ - s.lse);
-    store1(grow + id, (float)(gt * ((t.m + t.r) * q - e.p[j])));
+    if (id >= lo && id < hi)
+      store1(row + id, (float)(gt * ((t.m + t.r) * q_of(e.z[j]) - e.p[j])));
   }
 }
 
 extern __shared__ __align__(16) char lds[];
 
-// A block to a row: the loss and, with GRAD, the gradient.
-template <class T, class Y, bool REST, bool GRAD>
-__global__ __launch_bounds__(kScanThreads) void distill_row_kernel(const DistillArgs a) {
-  __shared__ RowSum sums[kScanThreads / kWave];
-  __shared__ double part[kScanThreads / kWave];
+// A block to a row that its registers hold: the loss and, with GRAD, the gradient.
+// The row's loads go out first and arrive behind the work on the teacher's entries.
+template <class T, int THREADS, bool GRAD>
+__global__ __launch_bounds__(THREADS, 4) void distill_hold_kernel(const DistillArgs a) {
+  constexpr int N = distill_held(sizeof(T));
+  __shared__ double part[THREADS / kWave];
   const int64_t row = blockIdx.x;
-  Entries e(lds, a.top);
-  uint32_t *bits = reinterpret_cast<uint32_t *>(lds + a.top * kEntryBytes);
-  const Target t = read_target<Y>(a, row, e, part, a.err);
-  if (REST)
-    mark_named(bits, a.seg_len / 32, a.ids + row * a.top, a.top, 0, a.vocab);
-  merge(a.top, e);
   const T *z = static_cast<const T *>(a.logits) + row * a.stride;
-  const RowSum sum = scan_segment<T, REST>(z, 0, a.vocab, a.c,
-                                           reinterpret_cast<const uint8_t *>(bits), sums);
-  const RowStats s = finish_row<T, REST>(a, row, sum, e, t, part);
+  const double T_ = a.temperature;
+  RawEntries<THREADS> raw;
+  raw.load(a, row);
+  Held<T, THREADS, N> held;
+  held.load(z, (int)a.vocab);
+  Entries e(lds, a.top);
+  const Target t = read_target<THREADS>(a, row, raw, 0, a.vocab, (int)(a.vocab + 31) / 32, e,
+                                        part, a.err);
+  for (int j = threadIdx.x; j < (int)a.top; j += THREADS)
+    e.z[j] = e.ids[j] >= 0 ? Chunk<T>::one(z[e.ids[j]]) : kNegInf;
+  Running run;
+  held.sum((int)a.vocab, a.c, e.bits, run);
+  const RowSum rest = block_join<THREADS>(run, a.c, part);
+  const RowSum named = sum_named<THREADS>(a, e, part);
+  const Whole whole = both(rest, named, T_);
+  const RowSum &all = whole.all;
   if (GRAD) {
-    __syncthreads();  // (the logits of the named ids are read before any is overwritten)
-    write_gradient<T, REST>(a, row, 0, a.vocab, s, e, t);
+    // (every lane has read its named logits, before the barriers of the sums)
+    T *grad = static_cast<T *>(a.grad) + row * a.grad_stride;
+    const float g = raw.weight;
+    if (g == 0.0f || t.none) {
+      write_zeros(grad, 0, a.vocab, THREADS);
+    } else {
+      const double gt = g / T_;
+      const float factor =
+          rest.sum == 0.0 ? 0.0f : (float)(gt * ((t.m + t.r) * whole.s - t.r) / rest.sum);
+      held.write(grad, (int)a.vocab, factor, ref_of(rest.max), a.c);
+      __syncthreads();
+      write_named<T, THREADS>(a, grad, 0, a.vocab, gt, e, t, [&](float x) {
+        return all.sum == 0.0
+                   ? 0.0
+                   : exp64(((double)x - (double)ref_of(all.max)) / T_) / all.sum;
+      });
+    }
   }
+  write_row<THREADS>(a, row, rest, all, e, t, part);
 }
 
-// A block to a segment of a row: its sum.
-template <class T, bool REST>
+// A block to a segment of a row: the sum of its unnamed values.
+template <class T>
 __global__ __launch_bounds__(kScanThreads) void distill_scan_kernel(const DistillArgs a) {
-  __shared__ RowSum sums[kScanThreads / kWave];
+  __shared__ double part[kScanThreads / kWave];
   const int64_t row = blockIdx.x / a.segs, seg = blockIdx.x - row * a.segs;
   const int64_t lo = seg * a.seg_len, hi = lo + a.seg_len < a.vocab ? lo + a.seg_len : a.vocab;
   uint32_t *bits = reinterpret_cast<uint32_t *>(lds);
-  if (REST) mark_named(bits, a.seg_len / 32, a.ids + row * a.top, a.top, lo, hi);
+  for (int i = threadIdx.x; i < (int)(a.seg_len / 32); i += kScanThreads) bits[i] = 0u;
+  __syncthreads();
+  for (int64_t j = threadIdx.x; j < a.top; j += kScanThreads) {
+    const int64_t id = a.ids[row * a.top + j];
+    if (id >= lo && id < hi) atomicOr(&bits[(id - lo) >> 5], 1u << ((id - lo) & 31));
+  }
+  __syncthreads();
+  const uint8_t *bytes = reinterpret_cast<const uint8_t *>(bits);
   const T *z = static_cast<const T *>(a.logits) + row * a.stride;
-  const RowSum s = scan_segment<T, REST>(z, lo, hi, a.c,
-                                         reinterpret_cast<const uint8_t *>(bits), sums);
+  constexpr int U = sizeof(T) == 2 ? 4 : 2;
+  Running run;
+  each_chunks<T, U>(z, lo, hi, [&](int64_t at, float (&v)[U][8]) {
+    float m = run.max;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = at + u * kScanTile + 8 * threadIdx.x;
+      leave_out(v[u], i < hi ? bytes[(i - lo) >> 3] : 0u);
+      m = max8(m, v[u]);
+    }
+    const float ref = run.raise(m, a.c);
+#pragma unroll
+    for (int u = 0; u < U; ++u) run.add(v[u], ref, a.c);
+  });
+  const RowSum s = block_join<kScanThreads>(run, a.c, part);
   if (threadIdx.x == 0) a.parts[row * a.segs + seg] = {s.sum, s.max, 0u};
 }
 
 // A block to a row: the segments' sums joined, the row's statistics and loss.
-template <class T, class Y, bool REST>
+template <class T>
 __global__ __launch_bounds__(kScanThreads) void distill_finish_kernel(const DistillArgs a) {
-  __shared__ RowSum sums[kScanThreads / kWave];
   __shared__ double part[kScanThreads / kWave];
   const int64_t row = blockIdx.x;
+  const T *z = static_cast<const T *>(a.logits) + row * a.stride;
+  RawEntries<kScanThreads> raw;
+  raw.load(a, row);
   Entries e(lds, a.top);
-  const Target t = read_target<Y>(a, row, e, part, a.err);
-  merge(a.top, e);
-  RowSum v = {kNegInf, 0.0};
-  for (int64_t i = threadIdx.x; i < a.segs; i += kScanThreads) {
-    const ScanPart p = a.parts[row * a.segs + i];
-    v = join_sums(v, RowSum{p.max, p.sum}, a.c);
-  }
-  v = block_join<kScanThreads>(v, a.c, sums);
-  finish_row<T, REST>(a, row, v, e, t, part);
+  const Target t = read_target<kScanThreads>(a, row, raw, 0, a.vocab, 0, e, part, a.err);
+  for (int j = threadIdx.x; j < (int)a.top; j += kScanThreads)
+    e.z[j] = e.ids[j] >= 0 ? Chunk<T>::one(z[e.ids[j]]) : kNegInf;
+  const RowSum rest = wave_join(a.parts + row * a.segs, a.segs, a.c);
+  const RowSum named = sum_named<kScanThreads>(a, e, part);
+  write_row<kScanThreads>(a, row, rest, both(rest, named, a.temperature).all, e, t,
+                          part);
 }
 
 // A block to a segment of a row: its gradient, from the statistics that were kept.
-template <class T, class Y, bool REST>
+// SHORT: a vocabulary of less than eight values.
+template <class T, bool SHORT>
 __global__ __launch_bounds__(kScanThreads) void distill_backward_kernel(const DistillArgs a) {
+  constexpr int N = distill_held_backward(sizeof(T));
   __shared__ double part[kScanThreads / kWave];
   const int64_t row = blockIdx.x / a.segs, seg = blockIdx.x - row * a.segs;
-  const int64_t lo = seg * a.seg_len, hi = lo + a.seg_len < a.vocab ? lo + a.seg_len : a.vocab;
-  Entries e(lds, a.top);
-  const Target t = read_target<Y>(a, row, e, part, seg == 0 ? a.err : nullptr);
-  merge(a.top, e);
+  // (whole chunks are shared out, so that every segment has eight values or more)
+  const int64_t chunks = a.vocab / 8, lo = chunks * seg / a.segs * 8;
+  const int64_t hi = seg + 1 == a.segs ? a.vocab : chunks * (seg + 1) / a.segs * 8;
   const T *z = static_cast<const T *>(a.logits) + row * a.stride;
-  // (other segments may be overwritten already)
-  for (int64_t j = threadIdx.x; j < a.top; j += kScanThreads) {
+  T *grad = static_cast<T *>(a.grad) + row * a.grad_stride;
+  const double T_ = a.temperature;
+  RawEntries<kScanThreads> raw;
+  raw.load(a, row);
+  Held<T, kScanThreads, N> held;
+  if (!SHORT) held.load(z + lo, (int)(hi - lo));
+  Entries e(lds, a.top);
+  const Target t = read_target<kScanThreads>(a, row, raw, lo, hi, (int)(hi - lo + 31) / 32, e,
+                                             part, seg == 0 ? a.err : nullptr);
+  const float g = raw.weight;
+  if (g == 0.0f || t.none) {
+    write_zeros(grad, lo, hi, kScanThreads);
+    return;
+  }
+  // (other segments' logits may be overwritten already)
+  for (int j = threadIdx.x; j < (int)a.top; j += kScanThreads) {
     const int32_t id = e.ids[j];
     e.z[j] = id >= lo && id < hi ? Chunk<T>::one(z[id]) : kNegInf;
   }
+  // the unnamed: factor * exp(z / T - base), base the log of their own sum (of the whole
+  // sum without a class for the rest)
+  const double lse = a.lse[row], base = a.rest ? a.lse_rest[row] : lse, gt = g / T_;
+  const bool empty = base == -__builtin_inf();
+  const float ref = empty || base != base ? 0.0f : (float)(base * T_);
+  double f = gt * t.m;
+  if (a.rest) f = gt * ((t.m + t.r) * (empty ? 0.0 : exp64(base - lse)) - t.r);
+  const float factor = empty ? 0.0f : (float)(f * exp64(ref / T_ - base));
+  float one = kNegInf;
+  if (SHORT && threadIdx.x < a.vocab) one = Chunk<T>::one(z[threadIdx.x]);
   __syncthreads();
-  const RowStats s = {a.lse[row], REST ? a.lse_rest[row] : 0.0};
-  write_gradient<T, REST>(a, row, lo, hi, s, e, t);
+  if (!SHORT)
+    held.write(grad + lo, (int)(hi - lo), factor, ref, a.c);
+  else if (threadIdx.x < a.vocab)
+    store1(grad + threadIdx.x, factor * exp2_fast((one - ref) * a.c));
+  __syncthreads();
+  write_named<T, kScanThreads>(a, grad, lo, hi, gt, e, t, [&](float x) {
+    return lse == -__builtin_inf() ? 0.0 : exp64(x / T_ - lse);
+  });
 }
 
 DistillArgs device_args(const engram_distill_args &h, const ScanShape &shape) {
@@ -372,6 +527,7 @@ DistillArgs device_args(const engram_distill_args &h, const ScanShape &shape) {
   a.seg_len = shape.seg_len;
   a.temperature = h.temperature;
   a.c = (float)(1.4426950408889634 / (double)h.temperature);
+  a.teacher_type = h.teacher_type;
   a.rest = h.rest;
   a.logits = h.d_logits;
   a.ids = h.d_ids;
@@ -386,57 +542,51 @@ DistillArgs device_args(const engram_distill_args &h, const ScanShape &shape) {
   return a;
 }
 
-// Calls f with the types and the switch as template arguments.
-template <class F>
-void with_types(const engram_distill_args &h, F f) {
-  const auto rest = [&](auto t, auto y) {
-    if (h.rest)
-      f(t, y, std::true_type{});
-    else
-      f(t, y, std::false_type{});
-  };
-  const auto teacher = [&](auto t) {
-    if (h.teacher_type == ENGRAM_BF16)
-      rest(t, uint16_t{});
-    else
-      rest(t, float{});
-  };
-  if (h.logits_type == ENGRAM_BF16)
-    teacher(uint16_t{});
+size_t lds_bytes(int64_t top, int64_t values) {
+  return (size_t)top * kEntryBytes + (size_t)ceil_div(values, 32) * 4;
+}
+
+template <class T, int THREADS>
+void enqueue_hold(const DistillArgs &a, int64_t rows, hipStream_t stream) {
+  const dim3 grid((unsigned)rows), block(THREADS);
+  const size_t bytes = lds_bytes(a.top, a.vocab);
+  if (a.grad != nullptr)
+    hipLaunchKernelGGL((distill_hold_kernel<T, THREADS, true>), grid, block, bytes, stream, a);
   else
-    teacher(float{});
+    hipLaunchKernelGGL((distill_hold_kernel<T, THREADS, false>), grid, block, bytes, stream, a);
 }
 
-void enqueue_backward(const engram_distill_args &h, const DistillArgs &a, hipStream_t stream) {
+template <class T>
+int enqueue_backward(const engram_distill_args &h, DistillArgs a) {
+  const int64_t most = kScanThreads * distill_held_backward(sizeof(T));
+  // (a segment of a row's chunks, and what is left of the last)
+  a.segs = h.vocab < 8 ? 1 : ceil_div(h.vocab / 8, most - 1);
+  if (!grid_fits(h.rows * a.segs, kScanThreads)) return ENGRAM_EINVAL;
   const dim3 grid((unsigned)(h.rows * a.segs)), block(kScanThreads);
-  const size_t entries = (size_t)h.top * kEntryBytes;
-  with_types(h, [&](auto t, auto y, auto rest) {
-    hipLaunchKernelGGL((distill_backward_kernel<decltype(t), decltype(y), rest.value>), grid,
-                       block, entries, stream, a);
-  });
+  const size_t bytes = lds_bytes(h.top, most * 8);
+  const hipStream_t stream = as_stream(h.stream);
+  if (h.vocab < 8)
+    hipLaunchKernelGGL((distill_backward_kernel<T, true>), grid, block, bytes, stream, a);
+  else
+    hipLaunchKernelGGL((distill_backward_kernel<T, false>), grid, block, bytes, stream, a);
+  return launch_status();
 }
 
-}  // namespace
-}  // namespace engram
-
-int engram::launch_distill(const engram_distill_args &h) {
+template <class T>
+int enqueue(const engram_distill_args &h) {
   const ScanShape shape = distill_shape(h.rows, h.vocab);
-  if (!grid_fits(h.rows * shape.segs, kScanThreads)) return ENGRAM_EINVAL;
   DistillArgs a = device_args(h, shape);
   const hipStream_t stream = as_stream(h.stream);
-  const size_t entries = (size_t)h.top * kEntryBytes, bits = h.rest ? shape.seg_len / 8 : 0;
-  const dim3 rows((unsigned)h.rows), block(kScanThreads);
-  if (shape.segs == 1) {
-    with_types(h, [&](auto t, auto y, auto rest) {
-      using T = decltype(t);
-      using Y = decltype(y);
-      if (h.d_grad != nullptr)
-        hipLaunchKernelGGL((distill_row_kernel<T, Y, rest.value, true>), rows, block,
-                           entries + bits, stream, a);
-      else
-        hipLaunchKernelGGL((distill_row_kernel<T, Y, rest.value, false>), rows, block,
-                           entries + bits, stream, a);
-    });
+  const int threads = distill_threads(h.vocab, sizeof(T));
+  if (!grid_fits(h.rows, 1024) || !grid_fits(h.rows * shape.segs, kScanThreads))
+    return ENGRAM_EINVAL;
+  if (threads != 0) {
+    if (threads == 256)
+      enqueue_hold<T, 256>(a, h.rows, stream);
+    else if (threads == 512)
+      enqueue_hold<T, 512>(a, h.rows, stream);
+    else
+      enqueue_hold<T, 1024>(a, h.rows, stream);
     return launch_status();
   }
   a.parts = static_cast<ScanPart *>(h.d_workspace);
@@ -445,24 +595,24 @@ int engram::launch_distill(const engram_distill_args &h) {
     if (a.lse == nullptr) a.lse = kept;
     if (a.lse_rest == nullptr) a.lse_rest = kept + h.rows;
   }
-  with_types(h, [&](auto t, auto y, auto rest) {
-    using T = decltype(t);
-    using Y = decltype(y);
-    hipLaunchKernelGGL((distill_scan_kernel<T, rest.value>),
-                       dim3((unsigned)(h.rows * shape.segs)), block, bits, stream, a);
-    hipLaunchKernelGGL((distill_finish_kernel<T, Y, rest.value>), rows, block, entries, stream,
-                       a);
-  });
-  if (h.d_grad != nullptr) {
-    a.err = nullptr;  // counted already
-    enqueue_backward(h, a, stream);
-  }
-  return launch_status();
+  hipLaunchKernelGGL(distill_scan_kernel<T>, dim3((unsigned)(h.rows * shape.segs)),
+                     dim3(kScanThreads), (size_t)shape.seg_len / 8, stream, a);
+  hipLaunchKernelGGL(distill_finish_kernel<T>, dim3((unsigned)h.rows), dim3(kScanThreads),
+                     lds_bytes(h.top, 0), stream, a);
+  if (h.d_grad == nullptr) return launch_status();
+  a.err = nullptr;  // counted already
+  return enqueue_backward<T>(h, a);
+}
+
+}  // namespace
+}  // namespace engram
+
+int engram::launch_distill(const engram_distill_args &h) {
+  return h.logits_type == ENGRAM_BF16 ? enqueue<uint16_t>(h) : enqueue<float>(h);
 }
 
 int engram::launch_distill_backward(const engram_distill_args &h) {
-  const ScanShape shape = distill_shape(h.rows, h.vocab);
-  if (!grid_fits(h.rows * shape.segs, kScanThreads)) return ENGRAM_EINVAL;
-  enqueue_backward(h, device_args(h, shape), as_stream(h.stream));
-  return launch_status();
+  const DistillArgs a = device_args(h, ScanShape{});
+  return h.logits_type == ENGRAM_BF16 ? enqueue_backward<uint16_t>(h, a)
+                                      : enqueue_backward<float>(h, a);
 }

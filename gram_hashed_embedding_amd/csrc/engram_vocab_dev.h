@@ -3,11 +3,11 @@
 // joins over lanes, segments and rows.
 //
 // A lane keeps the largest logit it has seen and the sum of
-//     2^(z c - M),  c = log2(e) / temperature,  M = round(max c)
-// (one fma and one v_exp_f32 a value); a new maximum scales the sum by
-// 2^(M_old - M_new).  Sums leave the lane in fp64.  The logarithm is taken in
-// fp64 at the end: lse = max / temperature + ln(sum) + (M - max c) ln 2, so
-// that M's rounding is no error.
+//     exp((z - max) / temperature) = 2^((z - max) c),  c = log2(e) / temperature
+// (a subtraction, a product and a v_exp_f32 a value).  One fma, z c - (max c), would
+// do, but max c overflows for a row whose logits are all a mask's lowest value;
+// the difference is exact there.  Sums leave the lane in fp64, where the
+// logarithm is taken too.
 #pragma once
 
 #include "engram_layer_dev.h"
@@ -36,6 +36,8 @@ struct Chunk<uint16_t> {
   __device__ __forceinline__ void load(const uint16_t *p) { __builtin_memcpy(&r, p, 16); }
   __device__ __forceinline__ void values(float (&z)[8]) const { unpack_bf16x8(r, z); }
   __device__ static __forceinline__ float one(uint16_t v) { return bf16_lo(v); }
+  // hides where the bits came from, so that nothing made of them is kept
+  __device__ __forceinline__ void renew() { asm volatile("" : "+v"(r)); }
 };
 template <>
 struct Chunk<float> {
@@ -49,6 +51,7 @@ struct Chunk<float> {
     z[4] = b.x; z[5] = b.y; z[6] = b.z; z[7] = b.w;
   }
   __device__ static __forceinline__ float one(float v) { return v; }
+  __device__ __forceinline__ void renew() { asm volatile("" : "+v"(a), "+v"(b)); }
 };
 
 __device__ __forceinline__ float max8(float m, const float (&z)[8]) {
@@ -56,99 +59,158 @@ __device__ __forceinline__ float max8(float m, const float (&z)[8]) {
 }
 
 // ---------------------------------------------------- running softmax sum --
-// The exponent's reference of a maximum: 0 while there is none, so that no
-// difference of infinities arises.
-__device__ __forceinline__ float ref_of(float max, float c) {
-  return max == kNegInf ? 0.0f : __fmul_rn(max, c);
-}
+// The point that exponents are taken from: the maximum, or 0 while there is none,
+// so that no difference of infinities arises.
+__device__ __forceinline__ float ref_of(float max) { return max == kNegInf ? 0.0f : max; }
 
 struct Running {
   float max = kNegInf, sum = 0.0f;
-  // raises the maximum to at least m, and gives the exponent's reference
+  // raises the maximum to at least m, and gives the point that exponents are taken from
   __device__ __forceinline__ float raise(float m, float c) {
-    const float ref = ref_of(m, c);
-    sum *= exp2_fast(__fmul_rn(max, c) - ref);  // (2^-inf while there was none)
+    const float ref = ref_of(m);
+    sum *= exp2_fast((max - ref) * c);  // (2^-inf while there was none)
     max = m;
     return ref;
   }
-  __device__ __forceinline__ void add(const float (&z)[8], float c, float ref) {
+  __device__ __forceinline__ void add(const float (&z)[8], float ref, float c) {
     float e[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = exp2_fast(__builtin_fmaf(z[i], c, -ref));
+    for (int i = 0; i < 8; ++i) e[i] = exp2_fast((z[i] - ref) * c);
     sum += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
   }
 };
 
-// A sum with its maximum, of a lane, a segment or a row.
+// exp in fp64 by its series around 0 (|r| <= ln(2) / 2: the 11th power's term is
+// 2e-13), in few registers.
+__device__ __forceinline__ double exp64(double x) {
+  x = x < -800.0 ? -800.0 : x;  // (0; a NaN stays one)
+  const double n = rint(x * 1.44269504088896340736);
+  const double r = fma(-n, 0.693147180559945309417, x);
+  double p = 1.0 / 3628800.0;
+  p = fma(p, r, 1.0 / 362880.0);
+  p = fma(p, r, 1.0 / 40320.0);
+  p = fma(p, r, 1.0 / 5040.0);
+  p = fma(p, r, 1.0 / 720.0);
+  p = fma(p, r, 1.0 / 120.0);
+  p = fma(p, r, 1.0 / 24.0);
+  p = fma(p, r, 1.0 / 6.0);
+  p = fma(p, r, 0.5);
+  p = fma(p, r, 1.0);
+  p = fma(p, r, 1.0);
+  return ldexp(p, (int)n);
+}
+
+// ----------------------------------------------- reductions over wavefronts --
+template <int LANES>
+__device__ __forceinline__ float lanes_max_of(float v) {
+  return __uint_as_float(lanes_reduce<LANES>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(max3(__uint_as_float(a), __uint_as_float(b), kNegInf));
+  }));
+}
+__device__ __forceinline__ float wave_max(float v) { return lanes_max_of<kWave>(v); }
+__device__ __forceinline__ double double_of(uint32_t lo, uint32_t hi) {
+  return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+__device__ __forceinline__ uint32_t low_of(double v) {
+  return (uint32_t)__double_as_longlong(v);
+}
+__device__ __forceinline__ uint32_t high_of(double v) {
+  return (uint32_t)((uint64_t)__double_as_longlong(v) >> 32);
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_move(double v) {
+  return double_of(dpp_move<CTRL>(low_of(v)), dpp_move<CTRL>(high_of(v)));
+}
+// A commutative op over aligned groups of LANES lanes, left in each of them.
+template <int LANES, class OP>
+__device__ __forceinline__ double lanes_reduce(double v, OP op) {
+  if (LANES >= 2) v = op(v, dpp_move<kDppXor1>(v));
+  if (LANES >= 4) v = op(v, dpp_move<kDppXor2>(v));
+  if (LANES >= 8) v = op(v, dpp_move<kDppHalfMirror>(v));
+  if (LANES >= 16) v = op(v, dpp_move<kDppMirror>(v));
+  if (LANES >= 32) {
+    const uint32_t l = low_of(v), h = high_of(v);
+    const auto x = __builtin_amdgcn_permlane16_swap(l, l, false, false);
+    const auto y = __builtin_amdgcn_permlane16_swap(h, h, false, false);
+    v = op(double_of(x[0], y[0]), double_of(x[1], y[1]));
+  }
+  if (LANES >= 64) {
+    const uint32_t l = low_of(v), h = high_of(v);
+    const auto x = __builtin_amdgcn_permlane32_swap(l, l, false, false);
+    const auto y = __builtin_amdgcn_permlane32_swap(h, h, false, false);
+    v = op(double_of(x[0], y[0]), double_of(x[1], y[1]));
+  }
+  return v;
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  return lanes_reduce<kWave>(v, [](double a, double b) { return a + b; });
+}
+__device__ __forceinline__ double wave_max(double v) {
+  return lanes_reduce<kWave>(v, [](double a, double b) { return fmax(a, b); });
+}
+
+// Over a block, in the same order for every row; `part` holds a slot a wavefront, which
+// each wavefront's lanes read one to a lane.
+template <int THREADS, class V>
+__device__ __forceinline__ V wave_of(const V *part) {
+  return part[threadIdx.x % (THREADS / kWave)];
+}
+template <int THREADS>
+__device__ __forceinline__ double block_sum(double v, double *part) {
+  v = wave_sum(v);
+  if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = v;
+  __syncthreads();
+  v = wave_of<THREADS>(part);
+  __syncthreads();
+  return lanes_reduce<THREADS / kWave>(v, [](double a, double b) { return a + b; });
+}
+template <int THREADS>
+__device__ __forceinline__ double block_max(double v, double *part) {
+  v = wave_max(v);
+  if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = v;
+  __syncthreads();
+  v = wave_of<THREADS>(part);
+  __syncthreads();
+  return lanes_reduce<THREADS / kWave>(v, [](double a, double b) { return fmax(a, b); });
+}
+template <int THREADS>
+__device__ __forceinline__ float block_max(float v, float *part) {
+  v = wave_max(v);
+  if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = v;
+  __syncthreads();
+  v = wave_of<THREADS>(part);
+  __syncthreads();
+  return lanes_max_of<THREADS / kWave>(v);
+}
+
+// A sum of exponentials with its maximum: of exp((z - max) / temperature).
 struct RowSum {
   float max;
   double sum;
 };
-__device__ __forceinline__ RowSum join_sums(const RowSum &a, const RowSum &b, float c) {
-  // (a NaN maximum is one of a NaN sum)
-  const float m = a.max > b.max ? a.max : b.max;
-  const float ref = ref_of(m, c);
-  // the terms of an empty side are 0, whatever its reference
-  const double sa = a.max == kNegInf ? a.sum : a.sum * (double)exp2_fast(ref_of(a.max, c) - ref);
-  const double sb = b.max == kNegInf ? b.sum : b.sum * (double)exp2_fast(ref_of(b.max, c) - ref);
-  return {m, sa + sb};
+// s, taken from max, as taken from ref.
+__device__ __forceinline__ double moved(double s, float max, float ref, float c) {
+  return max == kNegInf ? s : s * (double)exp2_fast((max - ref) * c);
 }
-
-// Joined over a wavefront, left in every lane: the order is the same for every row.
-__device__ __forceinline__ RowSum wave_join(RowSum v, float c) {
-#pragma unroll
-  for (int d = 1; d < kWave; d *= 2) {
-    const RowSum o = {__shfl_xor(v.max, d), __shfl_xor(v.sum, d)};
-    // the lower lane's side first in both
-    v = (threadIdx.x & d) ? join_sums(o, v, c) : join_sums(v, o, c);
-  }
-  return v;
-}
-
-// Joined over a block; `part` holds a slot a wavefront.  Left in every lane.
+// The lanes' running sums over a block.
 template <int THREADS>
-__device__ __forceinline__ RowSum block_join(RowSum v, float c, RowSum *part) {
-  v = wave_join(v, c);
-  if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = v;
-  __syncthreads();
-  v = part[0];
-#pragma unroll
-  for (int w = 1; w < THREADS / kWave; ++w) v = join_sums(v, part[w], c);
-  __syncthreads();
-  return v;
+__device__ __forceinline__ RowSum block_join(const Running &run, float c, double *part) {
+  const float m = block_max<THREADS>(run.max, reinterpret_cast<float *>(part));
+  return {m, block_sum<THREADS>(moved(run.sum, run.max, ref_of(m), c), part)};
 }
-
-// log of the sum of exp(z / temperature).
-__device__ __forceinline__ double log_sum(const RowSum &v, double temperature, float c) {
-  if (v.max == kNegInf && v.sum == 0.0) return -__builtin_inf();
-  const double m = v.max;
-  return m / temperature + log(v.sum) +
-         ((double)ref_of(v.max, c) - m * (double)c) * 0.693147180559945309417;
+// The sums of a row's segments, joined by a wavefront.
+__device__ __forceinline__ RowSum wave_join(const ScanPart *parts, int64_t n, float c) {
+  float m = kNegInf;
+  for (int64_t i = threadIdx.x % kWave; i < n; i += kWave) m = max3(m, parts[i].max, kNegInf);
+  m = wave_max(m);
+  double s = 0.0;
+  for (int64_t i = threadIdx.x % kWave; i < n; i += kWave)
+    s += moved(parts[i].sum, parts[i].max, ref_of(m), c);
+  return {m, wave_sum(s)};
 }
-
-template <int THREADS>
-__device__ __forceinline__ double block_sum(double v, double *part) {
-#pragma unroll
-  for (int d = 1; d < kWave; d *= 2) v += __shfl_xor(v, d);
-  if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = v;
-  __syncthreads();
-  v = part[0];
-#pragma unroll
-  for (int w = 1; w < THREADS / kWave; ++w) v += part[w];
-  __syncthreads();
-  return v;
-}
-template <int THREADS>
-__device__ __forceinline__ double block_max(double v, double *part) {
-#pragma unroll
-  for (int d = 1; d < kWave; d *= 2) v = fmax(v, __shfl_xor(v, d));
-  if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = v;
-  __syncthreads();
-  v = part[0];
-#pragma unroll
-  for (int w = 1; w < THREADS / kWave; ++w) v = fmax(v, part[w]);
-  __syncthreads();
-  return v;
+// log of the sum of exp(z / temperature): -inf for none.
+__device__ __forceinline__ double log_sum(const RowSum &v, double temperature) {
+  return ref_of(v.max) / temperature + log(v.sum);
 }
 
 // -------------------------------------------------------- reading a segment --

@@ -4,8 +4,6 @@
 // CPU alone.  Every check runs before anything is enqueued.
 #include "engram_vocab_host.h"
 
-#include <cmath>
-
 using namespace engram;
 
 namespace {
@@ -21,9 +19,10 @@ bool rows_ok(int64_t rows, int64_t vocab, int64_t stride) {
 }  // namespace
 
 // ------------------------------------------------------------ distillation --
-extern "C" size_t engram_distill_workspace(int64_t rows, int64_t vocab) {
-  if (!rows_ok(rows, vocab, vocab)) return (size_t)-1;
-  return distill_workspace(rows, vocab);
+extern "C" size_t engram_distill_workspace(int64_t rows, int64_t vocab,
+                                          int32_t logits_type) {
+  if (!rows_ok(rows, vocab, vocab) || !type_ok(logits_type)) return (size_t)-1;
+  return distill_workspace(rows, vocab, logits_type);
 }
 
 namespace {
@@ -35,7 +34,7 @@ int check_distill(const engram_distill_args *a) {
   if (!mul_fits(a->rows, a->top * 8, INT64_MAX / 16)) return ENGRAM_EINVAL;
   if (!type_ok(a->logits_type) || !type_ok(a->teacher_type)) return ENGRAM_EINVAL;
   if (a->rest != 0 && a->rest != 1) return ENGRAM_EINVAL;
-  if (!(a->temperature > 0.0f) || !std::isfinite(a->temperature)) return ENGRAM_EINVAL;
+  if (!(a->temperature >= 0x1p-64f && a->temperature <= 0x1p64f)) return ENGRAM_EINVAL;
   if (a->d_grad != nullptr && !rows_ok(a->rows, a->vocab, a->grad_stride)) return ENGRAM_EINVAL;
   if (a->d_grad != nullptr && a->d_grad == a->d_logits && a->grad_stride != a->logits_stride)
     return ENGRAM_EINVAL;
@@ -56,7 +55,7 @@ extern "C" int engram_distill(const engram_distill_args *a) {
   if (a->d_loss == nullptr && a->d_lse == nullptr && a->d_lse_rest == nullptr &&
       a->d_grad == nullptr)
     return ENGRAM_EINVAL;
-  const size_t need = distill_workspace(a->rows, a->vocab);
+  const size_t need = distill_workspace(a->rows, a->vocab, a->logits_type);
   if (need > 0 && (a->d_workspace == nullptr || !aligned16(a->d_workspace) ||
                    a->workspace_bytes < need))
     return ENGRAM_EWORKSPACE;

@@ -38,17 +38,29 @@ struct ScanPart {
 };
 
 // ------------------------------------------------------------ distillation --
-// One bit a value marks the ids that a teacher's row names, in LDS: 32 KB.
+// Chunks of 8 values that a lane holds of a row, for values of `size` bytes (80
+// registers of the 128 that 1024 threads have each), and of a segment in the
+// backward pass.
+constexpr int distill_held(size_t size) { return size == 2 ? 20 : 10; }
+constexpr int distill_held_backward(size_t size) { return size == 2 ? 8 : 4; }
+// The threads of a block that holds a whole row; 0 where none does.
+inline int distill_threads(int64_t vocab, size_t size) {
+  for (int threads = 256; threads <= 1024; threads *= 2)
+    if (vocab >= 8 && vocab <= threads * 8 * distill_held(size)) return threads;
+  return 0;
+}
+// Other rows are cut: one bit a value marks the ids that a teacher's row names, in
+// LDS: 32 KB.
 constexpr int64_t kDistillMaxSeg = int64_t(1) << 18;
 constexpr int64_t kDistillBlocks = 1024;
 inline ScanShape distill_shape(int64_t rows, int64_t vocab) {
   return scan_shape(rows, vocab, kDistillBlocks, kDistillMaxSeg);
 }
 // The parts of every segment, then the two fp32 statistics of each row for the
-// gradient; nothing where a block takes a whole row.
-inline size_t distill_workspace(int64_t rows, int64_t vocab) {
+// gradient; nothing where a block holds a row.
+inline size_t distill_workspace(int64_t rows, int64_t vocab, int32_t type) {
+  if (rows == 0 || distill_threads(vocab, type == ENGRAM_BF16 ? 2 : 4) != 0) return 0;
   const ScanShape s = distill_shape(rows, vocab);
-  if (rows == 0 || s.segs == 1) return 0;
   return (size_t)rows * (size_t)s.segs * sizeof(ScanPart) + (size_t)rows * 8;
 }
 

@@ -64,7 +64,7 @@ extern "C" {
  *     not NULL), once a call.
  *   d_teacher [rows, top] of teacher_type; d_teacher_lse fp32 [rows] or NULL.
  *   rest 0 or 1; 1 needs d_teacher_lse.
- *   temperature > 0, finite.
+ *   temperature 2^-64 to 2^64.
  *   d_loss, d_lse, d_lse_rest (with rest only): fp32 [rows], written when not
  *     NULL.
  *   d_grad of logits_type, rows grad_stride values apart, written when not
@@ -96,7 +96,7 @@ typedef struct engram_distill_args {
 } engram_distill_args;
 
 /* Bytes of workspace of engram_distill; (size_t)-1 for sizes it refuses. */
-size_t engram_distill_workspace(int64_t rows, int64_t vocab);
+size_t engram_distill_workspace(int64_t rows, int64_t vocab, int32_t logits_type);
 int engram_distill(const engram_distill_args *args);
 int engram_distill_backward(const engram_distill_args *args);
 
