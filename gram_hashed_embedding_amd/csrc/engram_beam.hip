@@ -48,14 +48,14 @@ __device__ __forceinline__ float max16(float v) {
 template <class T>
 __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(const ScanArgs a) {
   __shared__ double part[kScanThreads / kWave];
+  __shared__ float most_of[kBeamMaxSeg / kBeamGroup];
   const int64_t row = blockIdx.x / a.segs, seg = blockIdx.x - row * a.segs;
   if (!beam_live(a.scores, a.finished, row)) return;
   const int64_t lo = seg * a.seg_len, hi = lo + a.seg_len < a.vocab ? lo + a.seg_len : a.vocab;
   const T *z = static_cast<const T *>(a.logits) + row * a.stride;
-  float *maxima = a.maxima + row * a.groups;
   constexpr int U = sizeof(T) == 2 ? 4 : 2;
   Running run;
-  each_chunks<T, U>(z, lo, hi, [&](int64_t at, float (&z)[U][8]) {
+  each_chunks<T, kScanThreads, U>(z, lo, hi, [&](int64_t at, float (&z)[U][8]) {
     float m = run.max;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -63,19 +63,24 @@ __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(const ScanArgs 
       m = max3(m, own, kNegInf);
       const float most = max16(own);
       const int64_t i = at + u * kScanTile + 8 * threadIdx.x;
-      if (threadIdx.x % 16 == 0 && i < hi) maxima[i / kBeamGroup] = most;
+      if (threadIdx.x % 16 == 0 && i < hi) most_of[(i - lo) / kBeamGroup] = most;
     }
     const float ref = run.raise(m, a.c);
 #pragma unroll
     for (int u = 0; u < U; ++u) run.add(z[u], ref, a.c);
   });
-  const RowSum s = block_join<kScanThreads>(run, a.c, part);
+  const RowSum s = block_join<kScanThreads>(run, a.c, part);  // (with a barrier)
+  float *maxima = a.maxima + row * a.groups + lo / kBeamGroup;
+  for (int i = threadIdx.x; i < (int)((hi - lo + kBeamGroup - 1) / kBeamGroup);
+       i += kScanThreads)
+    maxima[i] = most_of[i];
   if (threadIdx.x == 0) a.parts[row * a.segs + seg] = {s.sum, s.max, 0u};
 }
 
 // ----------------------------------------------------------------- choice --
 constexpr int kChooseThreads = 1024;
 constexpr int kChooseList = 2048;
+constexpr int kChooseGroups = 96;  // (at least ENGRAM_BEAM_MAX; kKeep values a thread)
 
 // A candidate: its value, and its place among all of them.
 struct Candidate {
@@ -90,81 +95,91 @@ constexpr double kNone = -__builtin_inf();
 struct ChooseLds {
   Candidate list[kChooseList];
   Candidate best[ENGRAM_BEAM_MAX];  // the answer, in order
-  double row_best[kChooseThreads / 16];
   Candidate wave_best[kChooseThreads / kWave];
-  double threshold;
-  int listed, taken;
+  uint32_t row_best[kChooseThreads / 16];
+  int listed;
 };
 
-// The first `count` of the candidates 0 .. n-1 (value_at(i), kNone where there is none, and
-// place_at(i)), in order, in l.best[0 .. l.taken).
+// Bits that order as the values do (rounded down to fp32), and a value that has at least
+// these bits.
+__device__ __forceinline__ uint32_t order_bits(double v) {
+  const uint32_t u = __float_as_uint(__double2float_rd(v));
+  return u ^ ((u >> 31) != 0 ? 0xffffffffu : 0x80000000u);
+}
+constexpr uint32_t kNoneBits = 0x007fffffu;  // of kNone
+__device__ __forceinline__ double value_of_bits(uint32_t k) {
+  if (k <= kNoneBits) return kNone;
+  return __uint_as_float(k ^ ((k >> 31) != 0 ? 0x80000000u : 0xffffffffu));
+}
+
+// Lists the candidates 0 .. n-1 of which the first `count` are some, in l.list in no order;
+// gives their number.  logit(i) loads what value(i, logit) is made of (kNone where there is
+// no candidate); place(i) is what equal values are ordered by; meanwhile() is done while
+// the first loads are on their way and ends in a barrier.
 //
 // A threshold first: of the largest values of 64 rows of 16 threads, the count-th
-// largest has at least `count` values at or above it.  What reaches it is listed and
-// ranked by counting.  More than the list holds (long runs of equal values) are taken
-// one at a time instead, each the first after the one before.  A thread keeps its
-// first kKeep values; their loads go out together.
+// largest has at least `count` values at or above it (its leading 20 bits are enough,
+// found bit by bit from ballots).  What reaches it is listed.  Where that is more than
+// the list holds (long runs of equal values), the first `count` are listed one at a
+// time instead, each the first after the one before.  A thread keeps its first kKeep
+// values; their loads go out together.
 constexpr int kKeep = 12;
-template <class VALUE, class PLACE>
-__device__ void choose(ChooseLds &l, int n, int count, VALUE value_at, PLACE place_at) {
+template <class LOGIT, class VALUE, class PLACE, class MEANWHILE>
+__device__ __forceinline__ int list_best(ChooseLds &l, int n, int count, LOGIT logit, VALUE value,
+                                         PLACE place, MEANWHILE meanwhile) {
   const int t = threadIdx.x;
+  float raw[kKeep];
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k) {
+    const int i = t + k * kChooseThreads;
+    if (k * kChooseThreads < n) raw[k] = logit(i < n ? i : n - 1);
+  }
+  if (t == 0) l.listed = 0;
+  meanwhile();
   double kept[kKeep], mine = kNone;
 #pragma unroll
   for (int k = 0; k < kKeep; ++k) {
     const int i = t + k * kChooseThreads;
-    kept[k] = i < n ? value_at(i) : kNone;
+    kept[k] = kNone;
+    if (k * kChooseThreads < n && i < n) kept[k] = value(i, raw[k]);
+    mine = fmax(mine, kept[k]);
   }
-#pragma unroll
-  for (int k = 0; k < kKeep; ++k) mine = fmax(mine, kept[k]);
   for (int i = t + kKeep * kChooseThreads; i < n; i += kChooseThreads)
-    mine = fmax(mine, value_at(i));
-  mine = lanes_reduce<16>(mine, [](double a, double b) { return fmax(a, b); });
-  if (t % 16 == 0) l.row_best[t / 16] = mine;
-  if (t == 0) l.listed = 0;
+    mine = fmax(mine, value(i, logit(i)));
+  const uint32_t row = lanes_max<16>(order_bits(mine));
+  if (t % 16 == 0) l.row_best[t / 16] = row;
   __syncthreads();
-  if (t < kWave) {
-    const double v = l.row_best[t];
-    int ahead = 0;
-#pragma unroll 8
-    for (int k = 0; k < kWave; ++k) {
-      const double o = l.row_best[k];
-      ahead += o > v || (o == v && k < t);
-    }
-    if (ahead == count - 1) l.threshold = v;
+  const uint32_t of_row = l.row_best[t % kWave];
+  uint32_t bits = 0;
+#pragma unroll
+  for (int b = 31; b >= 12; --b) {
+    const uint32_t test = bits | 1u << b;
+    if (__popcll(__ballot(of_row >= test)) >= count) bits = test;
   }
-  __syncthreads();
-  const double least = l.threshold;
+  const double least = value_of_bits(bits);
   const auto list = [&](int i, double v) {
     if (v > kNone && v >= least) {
       const int k = atomicAdd(&l.listed, 1);
-      if (k < kChooseList) l.list[k] = {v, place_at(i)};
+      if (k < kChooseList) l.list[k] = {v, place(i)};
     }
   };
+  if (mine > kNone && mine >= least) {
 #pragma unroll
-  for (int k = 0; k < kKeep; ++k) list(t + k * kChooseThreads, kept[k]);
-  for (int i = t + kKeep * kChooseThreads; i < n; i += kChooseThreads) list(i, value_at(i));
+    for (int k = 0; k < kKeep; ++k) list(t + k * kChooseThreads, kept[k]);
+    for (int i = t + kKeep * kChooseThreads; i < n; i += kChooseThreads)
+      list(i, value(i, logit(i)));
+  }
   __syncthreads();
   const int listed = l.listed;
-  if (listed <= kChooseList) {
-    for (int k = t; k < listed; k += kChooseThreads) {
-      const Candidate c = l.list[k];
-      int ahead = 0;
-#pragma unroll 4
-      for (int o = 0; o < listed; ++o) ahead += before(l.list[o], c);
-      if (ahead < count) l.best[ahead] = c;
-    }
-    if (t == 0) l.taken = listed < count ? listed : count;
-    __syncthreads();
-    return;
-  }
+  if (listed <= kChooseList) return listed;
   // (at least `count` candidates there)
   Candidate last = {__builtin_inf(), -1};
   for (int r = 0; r < count; ++r) {
     Candidate m = {kNone, INT64_MAX};
     for (int i = t; i < n; i += kChooseThreads) {
-      const double v = value_at(i);
+      const double v = value(i, logit(i));
       if (v > kNone && v <= last.value && v >= m.value) {
-        const Candidate c = {v, place_at(i)};
+        const Candidate c = {v, place(i)};
         if (before(last, c) && before(c, m)) m = c;
       }
     }
@@ -178,10 +193,23 @@ __device__ void choose(ChooseLds &l, int n, int count, VALUE value_at, PLACE pla
     last = l.wave_best[0];
     for (int w = 1; w < kChooseThreads / kWave; ++w)
       if (before(l.wave_best[w], last)) last = l.wave_best[w];
-    if (t == 0) l.best[r] = last;
+    if (t == 0) l.list[r] = last;
     __syncthreads();
   }
-  if (t == 0) l.taken = count;
+  return count;
+}
+
+// The first `count` of the listed candidates, in order, in l.best: each one's rank is the
+// number of those before it, counted by a wavefront.
+__device__ __forceinline__ void rank_listed(ChooseLds &l, int listed, int count) {
+  const int lane = threadIdx.x % kWave;
+  for (int k = threadIdx.x / kWave; k < listed; k += kChooseThreads / kWave) {
+    const Candidate c = l.list[k];
+    int ahead = 0;
+    for (int o = lane; o - lane < listed; o += kWave)
+      ahead += __popcll(__ballot(o < listed && before(l.list[o], c)));
+    if (lane == 0 && ahead < count) l.best[ahead] = c;
+  }
   __syncthreads();
 }
 
@@ -197,26 +225,11 @@ __global__ __launch_bounds__(kChooseThreads) void beam_choose_kernel(const Choos
   __shared__ ChooseLds l;
   __shared__ double lse[ENGRAM_BEAM_MAX];    // NaN: no candidate but a finished beam's
   __shared__ double score[ENGRAM_BEAM_MAX];
-  __shared__ int64_t group_at[ENGRAM_BEAM_MAX];  // of each chosen group: its first value
-  __shared__ int group_beam[ENGRAM_BEAM_MAX];
+  __shared__ int64_t group_at[kChooseGroups];  // of each chosen group: its first value
+  __shared__ int group_beam[kChooseGroups];
   const BeamCall &c = a.c;
   const int64_t b = blockIdx.x, first_row = b * c.beams;
   const int t = threadIdx.x, beams = (int)c.beams, count = (int)c.count;
-  // each beam's lse, a wavefront to a beam
-  for (int w = t / kWave; w < beams; w += kChooseThreads / kWave) {
-    const int64_t row = first_row + w;
-    double v = __builtin_nan("");
-    if (beam_live(c.scores, c.finished, row)) {
-      v = log_sum(wave_join(c.parts + row * a.segs, a.segs, a.log2e), 1.0);
-      if (!__builtin_isfinite(v)) v = __builtin_nan("");
-    }
-    if (t % kWave == 0) {
-      lse[w] = v;
-      score[w] = c.scores[row];
-    }
-  }
-  __syncthreads();
-  // the best groups; a finished beam's candidate is a group of its own (its first)
   const int groups = (int)a.groups;
   const auto value_of = [&](int w, float z) {
     const double v = score[w] + ((double)z - lse[w]);
@@ -231,37 +244,66 @@ __global__ __launch_bounds__(kChooseThreads) void beam_choose_kernel(const Choos
     const uint32_t w = __umulhi(i, a.per_group);
     return (int)(i - w * groups >= (uint32_t)groups ? w + 1 : w);
   };
-  choose(
+  // the best groups; a finished beam's candidate is a group of its own (its first)
+  int chosen = list_best(
       l, beams * groups, count,
-      [&](int i) {
+      // (of beams that were not scanned whatever the memory holds)
+      [&](int i) { return c.maxima[first_row * groups + i]; },
+      [&](int i, float z) {
         const int w = beam_of(i);
-        if (lse[w] == lse[w]) return value_of(w, c.maxima[first_row * groups + i]);
+        if (lse[w] == lse[w]) return value_of(w, z);
         return i == w * groups && finished(w) ? score[w] : kNone;
       },
-      [&](int i) { return (int64_t)i; });
-  const int chosen = l.taken;
+      [&](int i) { return (int64_t)i; },
+      [&] {
+        // each beam's lse, a wavefront to a beam
+        for (int w = t / kWave; w < beams; w += kChooseThreads / kWave) {
+          const int64_t row = first_row + w;
+          double v = __builtin_nan("");
+          if (beam_live(c.scores, c.finished, row)) {
+            v = log_sum(wave_join(c.parts + row * a.segs, a.segs, a.log2e), 1.0);
+            if (!__builtin_isfinite(v)) v = __builtin_nan("");
+          }
+          if (t % kWave == 0) {
+            lse[w] = v;
+            score[w] = c.scores[row];
+          }
+        }
+        __syncthreads();
+      });
+  // more than a few are cut to the first `count`
+  const bool ranked = chosen > kChooseGroups;
+  if (ranked) {
+    rank_listed(l, chosen, count);
+    chosen = chosen < count ? chosen : count;
+  }
   if (t < chosen) {
-    const int at = (int)l.best[t].at, w = beam_of(at);
+    const int at = (int)(ranked ? l.best[t].at : l.list[t].at), w = beam_of(at);
     group_beam[t] = w;
     group_at[t] = (int64_t)(at - w * groups) * kBeamGroup;
   }
   __syncthreads();
-  choose(
+  const int listed = list_best(
       l, chosen * (int)kBeamGroup, count,
       [&](int i) {
-        const int w = group_beam[i / kBeamGroup], k = i % kBeamGroup;
-        const int64_t v = group_at[i / kBeamGroup] + k;
-        if (lse[w] != lse[w]) return k == 0 ? score[w] : kNone;
-        if (v >= c.vocab) return kNone;
+        const int w = group_beam[i / kBeamGroup];
+        const int64_t v = group_at[i / kBeamGroup] + i % kBeamGroup;
         const T *z = static_cast<const T *>(c.logits) + (first_row + w) * c.stride;
-        return value_of(w, Chunk<T>::one(z[v]));
+        return v < c.vocab ? Chunk<T>::one(z[v]) : kNegInf;
+      },
+      [&](int i, float z) {
+        const int w = group_beam[i / kBeamGroup];
+        if (lse[w] == lse[w]) return value_of(w, z);
+        return i % kBeamGroup == 0 ? score[w] : kNone;
       },
       [&](int i) {
         const int w = group_beam[i / kBeamGroup];
         return w * c.vocab + (lse[w] != lse[w] ? c.eos : group_at[i / kBeamGroup] + i % kBeamGroup);
-      });
+      },
+      [] { __syncthreads(); });
+  rank_listed(l, listed, count);
   if (t < count) {
-    const bool there = t < l.taken;
+    const bool there = t < listed;
     const Candidate best = l.best[there ? t : 0];
     const int64_t w = there ? best.at / c.vocab : -1, v = there ? best.at - w * c.vocab : -1;
     const int64_t o = b * count + t;

@@ -432,7 +432,7 @@ __global__ __launch_bounds__(kScanThreads) void distill_scan_kernel(const Distil
   const T *z = static_cast<const T *>(a.logits) + row * a.stride;
   constexpr int U = sizeof(T) == 2 ? 4 : 2;
   Running run;
-  each_chunks<T, U>(z, lo, hi, [&](int64_t at, float (&v)[U][8]) {
+  each_chunks<T, kScanThreads, U>(z, lo, hi, [&](int64_t at, float (&v)[U][8]) {
     float m = run.max;
 #pragma unroll
     for (int u = 0; u < U; ++u) {

@@ -214,27 +214,38 @@ __device__ __forceinline__ double log_sum(const RowSum &v, double temperature) {
 }
 
 // -------------------------------------------------------- reading a segment --
-// A lane's chunks of the values [lo, hi) of a row (lo a multiple of kScanTile),
-// U at a time: use(chunks' first index / 8, z) is called by every lane of the
-// block, for chunks that lie before hi; values past hi are -inf.
-template <class T, int U, class USE>
+// The values [lo, hi) of a row by a block, U chunks a lane at a time: use(at, z) is
+// called by every lane with the chunks that start at at + 8 * (u * THREADS + lane);
+// values past hi are -inf.  The next chunks' loads are on their way meanwhile (the last
+// step's once more, so that no load hangs on a condition).
+template <class T, int THREADS, int U, class USE>
 __device__ __forceinline__ void each_chunks(const T *row, int64_t lo, int64_t hi, USE use) {
+  constexpr int kTile = 8 * THREADS, kStep = U * kTile;
   const int t = threadIdx.x;
+  const int64_t last = lo + (hi - lo) / kStep * kStep - kStep;  // the last whole step
   int64_t at = lo;
-  for (; at + U * kScanTile <= hi; at += U * kScanTile) {
+  if (at <= last) {
     Chunk<T> r[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) r[u].load(row + at + u * kScanTile + 8 * t);
-    float z[U][8];
+    for (int u = 0; u < U; ++u) r[u].load(row + at + u * kTile + 8 * t);
+    for (; at <= last; at += kStep) {
+      float z[U][8];
+      const int64_t next = at + kStep <= last ? at + kStep : last;
+      Chunk<T> n[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) r[u].values(z[u]);
-    use(at, z);
+      for (int u = 0; u < U; ++u) n[u].load(row + next + u * kTile + 8 * t);
+#pragma unroll
+      for (int u = 0; u < U; ++u) r[u].values(z[u]);
+      use(at, z);
+#pragma unroll
+      for (int u = 0; u < U; ++u) r[u] = n[u];
+    }
   }
   if (at < hi) {
     float z[U][8];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t i = at + u * kScanTile + 8 * t;
+      const int64_t i = at + u * kTile + 8 * t;
       if (i + 8 <= hi) {
         Chunk<T> r;
         r.load(row + i);

@@ -67,9 +67,10 @@ inline size_t distill_workspace(int64_t rows, int64_t vocab, int32_t type) {
 // --------------------------------------------------------------- selection --
 // The scan leaves the largest logit of every kBeamGroup values.
 constexpr int64_t kBeamGroup = 128;
-constexpr int64_t kBeamBlocks = 1024;
+constexpr int64_t kBeamBlocks = 2048;
+constexpr int64_t kBeamMaxSeg = int64_t(1) << 18;
 inline ScanShape beam_shape(int64_t rows, int64_t vocab) {
-  return scan_shape(rows, vocab, kBeamBlocks, kMaxVocab);
+  return scan_shape(rows, vocab, kBeamBlocks, kBeamMaxSeg);
 }
 struct BeamCall {
   const void *logits;
