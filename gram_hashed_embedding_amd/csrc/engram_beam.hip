@@ -24,7 +24,7 @@ namespace {
 struct ScanArgs {
   const void *logits;
   int64_t vocab, stride, segs, seg_len, groups;
-  float c;
+  Scale c;
   const float *scores;
   const uint8_t *finished;
   ScanPart *parts;
@@ -37,14 +37,6 @@ __device__ __forceinline__ bool beam_live(const float *scores, const uint8_t *fi
   return __builtin_isfinite(scores[row]) && (finished == nullptr || finished[row] == 0);
 }
 
-// The maximum over aligned groups of 16 lanes, by DPP.
-__device__ __forceinline__ float max16(float v) {
-  const auto op = [](uint32_t a, uint32_t b) {
-    return __float_as_uint(max3(__uint_as_float(a), __uint_as_float(b), kNegInf));
-  };
-  return __uint_as_float(lanes_reduce<16>(__float_as_uint(v), op));
-}
-
 template <class T>
 __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(const ScanArgs a) {
   __shared__ double part[kScanThreads / kWave];
@@ -53,15 +45,15 @@ __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(const ScanArgs 
   if (!beam_live(a.scores, a.finished, row)) return;
   const int64_t lo = seg * a.seg_len, hi = lo + a.seg_len < a.vocab ? lo + a.seg_len : a.vocab;
   const T *z = static_cast<const T *>(a.logits) + row * a.stride;
-  constexpr int U = sizeof(T) == 2 ? 4 : 2;
+  constexpr int U = sizeof(T) == 2 ? 2 : 1;
   Running run;
-  each_chunks<T, kScanThreads, U>(z, lo, hi, [&](int64_t at, float (&z)[U][8]) {
+  each_chunks<T, kScanThreads, U>(z, lo, hi, [] {}, [&](int64_t at, float (&z)[U][8]) {
     float m = run.max;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const float own = max8(kNegInf, z[u]);
       m = max3(m, own, kNegInf);
-      const float most = max16(own);
+      const float most = lanes_max_of<16>(own + 0.0f);
       const int64_t i = at + u * kScanTile + 8 * threadIdx.x;
       if (threadIdx.x % 16 == 0 && i < hi) most_of[(i - lo) / kBeamGroup] = most;
     }
@@ -217,7 +209,7 @@ struct ChooseArgs {
   BeamCall c;
   int64_t segs, groups;
   uint32_t per_group;  // 2^32 / groups, rounded down
-  float log2e;
+  Scale log2e;
 };
 
 template <class T>
@@ -402,7 +394,7 @@ int engram::launch_beam_select(const BeamCall &c, void *stream) {
   const ScanShape shape = beam_shape(rows, c.vocab);
   if (!grid_fits(rows * shape.segs, kScanThreads) || !grid_fits(c.batch, kChooseThreads))
     return ENGRAM_EINVAL;
-  const float log2e = 1.44269504088896340736f;
+  const Scale log2e = scale_of(1.0f);
   const int64_t groups = ceil_div(c.vocab, kBeamGroup);
   const ScanArgs s = {c.logits, c.vocab, c.stride, shape.segs, shape.seg_len, groups, log2e,
                       c.scores, c.finished, c.parts, c.maxima};

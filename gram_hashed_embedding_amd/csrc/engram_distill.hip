@@ -10,17 +10,19 @@
 // which the gradient of the unnamed ids is made of.  The gradient is written
 // for every id as if it were unnamed; the few named ones are written after it.
 //
-// A block holds its whole row in registers between the two passes, so a row is
-// read once (distill_hold_kernel); rows that no block can hold are read again
-// for the gradient.
+// For loss and gradient together a block holds its whole row in registers between
+// the two passes, so a row is read once (distill_hold_kernel); rows that no block
+// can hold, and a few long rows, which would leave CUs idle, are cut into segments
+// and read again for the gradient (distill_scan_kernel, distill_backward_kernel).
 #include "engram_vocab_dev.h"
 
 namespace engram {
 namespace {
 
 struct DistillArgs {
-  int64_t vocab, top, stride, grad_stride, segs, seg_len;
-  float temperature, c;  // c = log2(e) / temperature
+  int64_t rows, vocab, top, stride, grad_stride, segs, seg_len;
+  float temperature;
+  Scale c;  // log2(e) / temperature
   int teacher_type, rest;
   const void *logits;
   const int64_t *ids;
@@ -29,7 +31,7 @@ struct DistillArgs {
   float *loss, *lse, *lse_rest;
   void *grad;
   int64_t *err;
-  ScanPart *parts;
+  DistillPart *parts;
 };
 
 // What a block keeps of the teacher's row in LDS, `top` values each, and behind
@@ -51,12 +53,12 @@ struct RawEntries {
   static constexpr int kMost = ENGRAM_DISTILL_MAX_TOP / THREADS;
   int64_t id[kMost];
   float y[kMost], lse, weight;
-  __device__ __forceinline__ void load(const DistillArgs &a, int64_t row) {
+  __device__ __forceinline__ void load(const DistillArgs &a, int64_t row, int thread) {
     lse = a.teacher_lse != nullptr ? a.teacher_lse[row] : 0.0f;
     weight = a.grad_loss != nullptr ? a.grad_loss[row] : 0.0f;
 #pragma unroll
     for (int k = 0; k < kMost; ++k) {
-      const int64_t j = threadIdx.x + k * THREADS;
+      const int j = thread + k * THREADS;
       id[k] = -1;
       y[k] = kNegInf;
       if (j < a.top) {
@@ -80,18 +82,18 @@ struct Target {
 template <int THREADS>
 __device__ __forceinline__ Target read_target(const DistillArgs &a, int64_t row, const RawEntries<THREADS> &raw,
                               int64_t lo, int64_t hi, int words, Entries e, double *part,
-                              int64_t *err) {
+                              int64_t *err, const int thread = threadIdx.x) {
   constexpr int kMost = RawEntries<THREADS>::kMost;
   __shared__ int flags;  // 1: an entry is used, 2: an id may repeat
   const double T = a.temperature;
   const int top = (int)a.top;
-  if (threadIdx.x == 0) flags = words > 0 ? 0 : 2;
-  for (int i = threadIdx.x; i < words; i += THREADS) e.bits[i] = 0u;
+  if (thread == 0) flags = 0;
+  for (int i = thread; i < words; i += THREADS) e.bits[i] = 0u;
   double most = -__builtin_inf();
   int bad = 0, seen = 0;
 #pragma unroll
   for (int k = 0; k < kMost; ++k) {
-    const int j = threadIdx.x + k * THREADS;
+    const int j = thread + k * THREADS;
     if (j < top) {
       const int64_t id = raw.id[k];
       const bool ok = id >= 0 && id < a.vocab;
@@ -109,11 +111,11 @@ __device__ __forceinline__ Target read_target(const DistillArgs &a, int64_t row,
     ref = raw.lse;
     __syncthreads();
   } else {
-    ref = block_max<THREADS>(most, part);
+    ref = block_max<THREADS>(most, part, thread);
     if (ref == -__builtin_inf()) ref = 0.0;
   }
   double sum = 0.0;
-  for (int j = threadIdx.x; j < top; j += THREADS) {
+  for (int j = thread; j < top; j += THREADS) {
     const int32_t id = e.ids[j];
     const double p = id >= 0 ? exp64(e.p[j] - ref) : 0.0;
     e.p[j] = p;
@@ -124,25 +126,26 @@ __device__ __forceinline__ Target read_target(const DistillArgs &a, int64_t row,
     }
   }
   if (seen != 0) atomicOr(&flags, seen);
-  sum = block_sum<THREADS>(sum, part);
-  Target t = {sum, 0.0, (flags & 1) == 0};
+  sum = block_sum<THREADS>(sum, part, thread);
+  const uint32_t flag = uniform((uint32_t)flags);
+  Target t = {sum, 0.0, (flag & 1) == 0};
   if (a.teacher_lse == nullptr) {
     t.none |= sum == 0.0;
     if (sum != 0.0)
-      for (int j = threadIdx.x; j < top; j += THREADS) e.p[j] /= sum;
-    t.m = sum == 0.0 ? 0.0 : sum / sum;
+      for (int j = thread; j < top; j += THREADS) e.p[j] /= sum;
+    t.m = uniform(sum == 0.0 ? 0.0 : sum / sum);
   } else if (a.rest) {
     // (a smaller difference from 1 is what rounding teacher_lse to fp32 leaves)
     const double r = 1.0 - sum;
-    t.r = !t.none && r >= 0x1p-20 ? r : 0.0;
+    t.r = uniform(!t.none && r >= 0x1p-20 ? r : 0.0);
   }
-  if ((flags & 2) != 0) {
+  if (words == 0 || (flag & 2) != 0) {
     __syncthreads();
     double p[kMost];
     bool first[kMost];
 #pragma unroll
     for (int k = 0; k < kMost; ++k) {
-      const int j = threadIdx.x + k * THREADS;
+      const int j = thread + k * THREADS;
       const int32_t id = j < top ? e.ids[j] : -1;
       double total = 0.0;
       bool least = true;
@@ -158,7 +161,7 @@ __device__ __forceinline__ Target read_target(const DistillArgs &a, int64_t row,
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kMost; ++k) {
-      const int j = threadIdx.x + k * THREADS;
+      const int j = thread + k * THREADS;
       if (j < top) {
         e.p[j] = p[k];
         if (!first[k]) e.ids[j] = -1;
@@ -189,48 +192,50 @@ __device__ __forceinline__ Whole both(const RowSum &rest, const RowSum &named, d
                       : (double)rest.max - (double)named.max;
   const double w = rest.max == named.max ? 1.0 : exp64(d / T);  // (two empty sides are level)
   const double a = up ? rest.sum : rest.sum * w, b = up ? named.sum * w : named.sum;
-  const double sum = a + b;
-  return {{up ? rest.max : named.max, sum}, sum == 0.0 ? 0.0 : a / sum};
+  const double sum = uniform(a + b);
+  return {{uniform(up ? rest.max : named.max), sum}, uniform(sum == 0.0 ? 0.0 : a / sum)};
 }
 
 // The named logits' sum, in fp64, over the block; e.z is read by its own lanes.
 template <int THREADS>
-__device__ __forceinline__ RowSum sum_named(const DistillArgs &a, Entries e, double *part) {
+__device__ __forceinline__ RowSum sum_named(const DistillArgs &a, Entries e, double *part,
+                                            const int thread = threadIdx.x) {
   const int top = (int)a.top;
   float m = kNegInf;
-  for (int j = threadIdx.x; j < top; j += THREADS) m = max3(m, e.z[j], kNegInf);
-  m = block_max<THREADS>(m, reinterpret_cast<float *>(part));
+  for (int j = thread; j < top; j += THREADS) m = max3(m, e.z[j], kNegInf);
+  m = block_max<THREADS>(m, reinterpret_cast<float *>(part), thread);
   double sum = 0.0;
-  for (int j = threadIdx.x; j < top; j += THREADS)
+  for (int j = thread; j < top; j += THREADS)
     if (e.ids[j] >= 0) sum += exp64(((double)e.z[j] - (double)ref_of(m)) / a.temperature);
-  return {m, block_sum<THREADS>(sum, part)};
+  return {m, block_sum<THREADS>(sum, part, thread)};
 }
 
 // Loss and statistics of a row, written.
 template <int THREADS>
 __device__ __forceinline__ void write_row(const DistillArgs &a, int64_t row, const RowSum &rest,
-                          const RowSum &all, Entries e, const Target &t, double *part) {
+                          const RowSum &all, Entries e, const Target &t, double *part,
+                          const int thread = threadIdx.x) {
   const double T = a.temperature;
   const double none = -__builtin_inf();
   const int top = (int)a.top;
   double loss = 0.0, lse = 0.0;
-  if (threadIdx.x < (unsigned)top) {  // (the first lane is one of them)
+  if (thread < (unsigned)top) {  // (the first lane is one of them)
     lse = log_sum(all, T);
     if (a.loss != nullptr)
-      for (int j = threadIdx.x; j < top; j += THREADS) {
+      for (int j = thread; j < top; j += THREADS) {
         const double p = e.p[j];
         if (e.ids[j] >= 0 && p != 0.0)
           // (where no logit is finite every q is 0)
-          loss += p * (log(p) - (lse == none ? none : e.z[j] / T - lse));
+          loss += p * (log64(p) - (lse == none ? none : e.z[j] / T - lse));
       }
   }
-  if (a.loss != nullptr) loss = block_sum<THREADS>(loss, part);
-  if (threadIdx.x != 0) return;
+  if (a.loss != nullptr) loss = block_sum<THREADS>(loss, part, thread);
+  if (thread != 0) return;
   if (a.lse != nullptr) a.lse[row] = (float)lse;
   const double lse_rest = a.rest ? log_sum(rest, T) : 0.0;
   if (a.rest && a.lse_rest != nullptr) a.lse_rest[row] = (float)lse_rest;
   if (a.loss != nullptr) {
-    if (t.r != 0.0) loss += t.r * (log(t.r) - (lse_rest == none ? none : lse_rest - lse));
+    if (t.r != 0.0) loss += t.r * (log64(t.r) - (lse_rest == none ? none : lse_rest - lse));
     a.loss[row] = t.none ? 0.0f : (float)loss;
   }
 }
@@ -256,13 +261,6 @@ struct Held {
   // whether any lane has values in chunk k; whether all have eight (uniform)
   __device__ static __forceinline__ bool any(int n, int k) { return 8 * k * THREADS < n; }
   __device__ static __forceinline__ bool full(int n, int k) { return 8 * (k + 1) * THREADS <= n; }
-  // the lane, hidden from the compiler, which would keep the places of the loads in
-  // registers for the next use
-  __device__ static __forceinline__ int own_lane() {
-    int lane = threadIdx.x;
-    asm volatile("" : "+v"(lane));
-    return lane;
-  }
   // the address of a value: a uniform base and 32 bits of a lane's own
   __device__ static __forceinline__ const T *value(const T *row, uint32_t at) {
     return reinterpret_cast<const T *>(reinterpret_cast<const char *>(row) +
@@ -281,16 +279,19 @@ struct Held {
 #pragma unroll
     for (int k = 0; k < N; ++k) r[k].load(value(row, place(n, k, threadIdx.x)));
   }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int k = 0; k < N; ++k) r[k].clear();
+  }
 
   // The running sum of the unnamed values.
-  __device__ __forceinline__ void sum(int n, float c, const uint32_t *bits, Running &run) const {
+  __device__ __forceinline__ void sum(int n, Scale c, const uint32_t *bits, Running &run) const {
     const uint8_t *bytes = reinterpret_cast<const uint8_t *>(bits);
     constexpr int G = sizeof(T) == 2 ? 2 : 1;
-    static_assert(N % G == 0, "whole groups");
-    const int lane = own_lane();
+    const int lane = hidden_thread();
 #pragma unroll
     for (int g = 0; g < N; g += G) {
-      if (full(n, g + G - 1)) {
+      if (g + G <= N && full(n, g + G - 1)) {
         float z[G][8], m = run.max;
 #pragma unroll
         for (int u = 0; u < G; ++u) {
@@ -304,7 +305,7 @@ struct Held {
       } else {
 #pragma unroll
       for (int u = 0; u < G; ++u)
-        if (any(n, g + u)) {
+        if (g + u < N && any(n, g + u)) {
           float z[8];
           r[g + u].values(z);
           const int from = first(n, g + u, lane);
@@ -319,9 +320,13 @@ struct Held {
   }
 
   // factor * exp((z - ref) / T) in the place of every value.  (The values are unpacked
-  // and placed anew: kept from the sum they would take twice the registers.)
-  __device__ __forceinline__ void write(T *row, int n, float factor, float ref, float c) {
-    const int lane = own_lane();
+  // and placed anew: kept from the sum they would take twice the registers.)  With RELOAD
+  // a chunk that is done is loaded from the row `next`, or, without one, from one place.
+  template <bool RELOAD>
+  __device__ __forceinline__ void write(T *row, int n, float factor, float ref, Scale c,
+                                        const T *next, bool more) {
+    const int lane = hidden_thread();
+    const uint32_t all = more ? ~0u : 0u;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       if (any(n, k)) {
@@ -329,7 +334,10 @@ struct Held {
         float z[8];
         r[k].values(z);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = factor * exp2_fast((z[i] - ref) * c);
+        for (int i = 0; i < 8; ++i)
+          // (rounded to bf16 the second part of c is lost)
+          z[i] = factor * (sizeof(T) == 2 ? exp2_fast((z[i] - ref) * c.hi)
+                                          : exp_scaled(z[i] - ref, c));
         T *to = const_cast<T *>(value(row, place(n, k, lane)));
         const int from = full(n, k) ? 0 : first(n, k, lane);
         if (from == 0) {
@@ -340,6 +348,7 @@ struct Held {
             if (i >= from) store1(to + i, z[i]);
         }
       }
+      if (RELOAD) r[k].load(value(next, place(n, k, lane) & all));
     }
   }
 };
@@ -358,136 +367,256 @@ __device__ __forceinline__ void write_zeros(T *row, int64_t lo, int64_t hi, int 
 // The gradient of the named values in [lo, hi): q by q_of(z).
 template <class T, int THREADS, class Q>
 __device__ __forceinline__ void write_named(const DistillArgs &a, T *row, int64_t lo, int64_t hi,
-                                            double gt, Entries e, const Target &t, Q q_of) {
-  for (int j = threadIdx.x; j < (int)a.top; j += THREADS) {
+                                            double gt, Entries e, const Target &t, Q q_of,
+                                            const int thread = threadIdx.x) {
+  for (int j = thread; j < (int)a.top; j += THREADS) {
     const int32_t id = e.ids[j];
     if (id >= lo && id < hi)
       store1(row + id, (float)(gt * ((t.m + t.r) * q_of(e.z[j]) - e.p[j])));
   }
 }
 
+constexpr int64_t kComputeUnits = 256;
+constexpr int64_t kDistillWideRows = 512;
+
 extern __shared__ __align__(16) char lds[];
 
-// A block to a row that its registers hold: the loss and, with GRAD, the gradient.
-// The row's loads go out first and arrive behind the work on the teacher's entries.
-template <class T, int THREADS, bool GRAD>
+// Loss and gradient of rows that a block's registers hold.  As many blocks as stay on the
+// GPU together take the rows in turn: while a row's gradient is written chunk by chunk,
+// the next row's chunks are loaded into the registers that it leaves, so that loads,
+// stores and arithmetic go on side by side.  What a teacher's row gives is loaded before
+// the chunks (loads arrive in order) and worked on while they are on their way.
+template <class T, int THREADS>
 __global__ __launch_bounds__(THREADS, 4) void distill_hold_kernel(const DistillArgs a) {
-  constexpr int N = distill_held(sizeof(T));
+  constexpr int N = distill_held(sizeof(T), THREADS);
   __shared__ double part[THREADS / kWave];
-  const int64_t row = blockIdx.x;
-  const T *z = static_cast<const T *>(a.logits) + row * a.stride;
+  const int n = (int)a.vocab;
   const double T_ = a.temperature;
-  RawEntries<THREADS> raw;
-  raw.load(a, row);
-  Held<T, THREADS, N> held;
-  held.load(z, (int)a.vocab);
   Entries e(lds, a.top);
-  const Target t = read_target<THREADS>(a, row, raw, 0, a.vocab, (int)(a.vocab + 31) / 32, e,
-                                        part, a.err);
-  for (int j = threadIdx.x; j < (int)a.top; j += THREADS)
-    e.z[j] = e.ids[j] >= 0 ? Chunk<T>::one(z[e.ids[j]]) : kNegInf;
-  Running run;
-  held.sum((int)a.vocab, a.c, e.bits, run);
-  const RowSum rest = block_join<THREADS>(run, a.c, part);
-  const RowSum named = sum_named<THREADS>(a, e, part);
-  const Whole whole = both(rest, named, T_);
-  const RowSum &all = whole.all;
-  if (GRAD) {
+  int64_t row = blockIdx.x;
+  RawEntries<THREADS> raw;
+  raw.load(a, row, threadIdx.x);
+  Held<T, THREADS, N> held;
+  held.load(static_cast<const T *>(a.logits) + row * a.stride, n);
+  for (;;) {
+    const int thread = hidden_thread();
+    const float g = raw.weight;
+    const Target t = read_target<THREADS>(a, row, raw, 0, a.vocab, (n + 31) / 32, e, part, a.err,
+                                          thread);
+    Running run;
+    held.sum(hidden(n), a.c, e.bits, run);
+    const T *z = static_cast<const T *>(a.logits) + row * a.stride;
+    for (int j = thread; j < (int)a.top; j += THREADS)
+      e.z[j] = e.ids[j] >= 0 ? Chunk<T>::one(z[e.ids[j]]) : kNegInf;
+    const bool more = row + gridDim.x < a.rows;
+    const int64_t next = more ? row + gridDim.x : row;
+    raw.load(a, next, thread);
+    const RowSum rest = block_join<THREADS>(run, a.c, part, thread);
+    const RowSum named = sum_named<THREADS>(a, e, part, thread);
+    const Whole whole = both(rest, named, T_);
     // (every lane has read its named logits, before the barriers of the sums)
     T *grad = static_cast<T *>(a.grad) + row * a.grad_stride;
-    const float g = raw.weight;
-    if (g == 0.0f || t.none) {
-      write_zeros(grad, 0, a.vocab, THREADS);
-    } else {
-      const double gt = g / T_;
-      const float factor =
-          rest.sum == 0.0 ? 0.0f : (float)(gt * ((t.m + t.r) * whole.s - t.r) / rest.sum);
-      held.write(grad, (int)a.vocab, factor, ref_of(rest.max), a.c);
-      __syncthreads();
-      write_named<T, THREADS>(a, grad, 0, a.vocab, gt, e, t, [&](float x) {
-        return all.sum == 0.0
-                   ? 0.0
-                   : exp64(((double)x - (double)ref_of(all.max)) / T_) / all.sum;
-      });
-    }
+    const T *coming = static_cast<const T *>(a.logits) + next * a.stride;
+    // (a row that does not count: zeros, whatever it holds)
+    const bool counts = g != 0.0f && !t.none;
+    if (!counts) held.clear();
+    const double gt = uniform(g / T_);
+    const float factor =
+        uniform(!counts || rest.sum == 0.0
+                    ? 0.0f
+                    : (float)(gt * ((t.m + t.r) * whole.s - t.r) / rest.sum));
+    held.template write<true>(grad, hidden(n), factor, counts ? ref_of(rest.max) : 0.0f, a.c, coming,
+                              more);
+    __syncthreads();
+    if (counts)
+      write_named<T, THREADS>(
+          a, grad, 0, a.vocab, gt, e, t,
+          [&](float x) {
+            return whole.all.sum == 0.0
+                       ? 0.0
+                       : exp64(((double)x - (double)ref_of(whole.all.max)) / T_) / whole.all.sum;
+          },
+          thread);
+    write_row<THREADS>(a, row, rest, whole.all, e, t, part, thread);
+    if (!more) return;
+    row = next;
+    __syncthreads();  // (the entries are read until here)
   }
-  write_row<THREADS>(a, row, rest, all, e, t, part);
 }
 
-// A block to a segment of a row: the sum of its unnamed values.
+// The unnamed values of [lo, hi) of a row, summed while the teacher's entries are read and
+// their logits (of those that lie in it) loaded.
+template <class T, int THREADS>
+__device__ __forceinline__ RowSum scan_row(const DistillArgs &a, int64_t row, int64_t lo,
+                                           int64_t hi, Entries e, Target &t, double *part,
+                                           int64_t *err) {
+  constexpr int U = sizeof(T) == 2 ? 2 : 1;
+  const T *z = static_cast<const T *>(a.logits) + row * a.stride;
+  const uint8_t *bytes = reinterpret_cast<const uint8_t *>(e.bits);
+  RawEntries<THREADS> raw;
+  raw.load(a, row, threadIdx.x);
+  Running run;
+  each_chunks<T, THREADS, U>(
+      z, lo, hi,
+      [&] {
+        t = read_target<THREADS>(a, row, raw, lo, hi, (int)(hi - lo + 31) / 32, e, part, err);
+        for (int j = threadIdx.x; j < (int)a.top; j += THREADS) {
+          const int32_t id = e.ids[j];
+          e.z[j] = id >= lo && id < hi ? Chunk<T>::one(z[id]) : kNegInf;
+        }
+      },
+      [&](int64_t at, float (&v)[U][8]) {
+        float m = run.max;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int64_t i = at + (u * THREADS + (int)threadIdx.x) * 8;
+          leave_out(v[u], i < hi ? bytes[(i - lo) >> 3] : 0u);
+          m = max8(m, v[u]);
+        }
+        const float ref = run.raise(m, a.c);
+#pragma unroll
+        for (int u = 0; u < U; ++u) run.add(v[u], ref, a.c);
+      });
+  return block_join<THREADS>(run, a.c, part);
+}
+
+// A block to a row: its statistics and loss.
+template <class T, int THREADS>
+__global__ __launch_bounds__(THREADS, 8) void distill_row_kernel(const DistillArgs a) {
+  __shared__ double part[THREADS / kWave];
+  Entries e(lds, a.top);
+  Target t;
+  const int64_t row = blockIdx.x;
+  const RowSum rest = scan_row<T, THREADS>(a, row, 0, a.vocab, e, t, part, a.err);
+  const RowSum named = sum_named<THREADS>(a, e, part);
+  write_row<THREADS>(a, row, rest, both(rest, named, a.temperature).all, e, t, part);
+}
+
+// A block to a segment of a row: its part of the sums and of the loss.
 template <class T>
-__global__ __launch_bounds__(kScanThreads) void distill_scan_kernel(const DistillArgs a) {
+__global__ __launch_bounds__(kScanThreads, 8) void distill_scan_kernel(const DistillArgs a) {
   __shared__ double part[kScanThreads / kWave];
+  Entries e(lds, a.top);
+  Target t;
   const int64_t row = blockIdx.x / a.segs, seg = blockIdx.x - row * a.segs;
   const int64_t lo = seg * a.seg_len, hi = lo + a.seg_len < a.vocab ? lo + a.seg_len : a.vocab;
-  uint32_t *bits = reinterpret_cast<uint32_t *>(lds);
-  for (int i = threadIdx.x; i < (int)(a.seg_len / 32); i += kScanThreads) bits[i] = 0u;
-  __syncthreads();
-  for (int64_t j = threadIdx.x; j < a.top; j += kScanThreads) {
-    const int64_t id = a.ids[row * a.top + j];
-    if (id >= lo && id < hi) atomicOr(&bits[(id - lo) >> 5], 1u << ((id - lo) & 31));
+  const RowSum rest =
+      scan_row<T, kScanThreads>(a, row, lo, hi, e, t, part, seg == 0 ? a.err : nullptr);
+  const RowSum named = sum_named<kScanThreads>(a, e, part);
+  double loss = 0.0;  // but for the part of lse
+  for (int j = threadIdx.x; j < (int)a.top; j += kScanThreads) {
+    const int32_t id = e.ids[j];
+    const double p = e.p[j];
+    if (id >= lo && id < hi && p != 0.0) loss += p * (log64(p) - e.z[j] / a.temperature);
   }
-  __syncthreads();
-  const uint8_t *bytes = reinterpret_cast<const uint8_t *>(bits);
-  const T *z = static_cast<const T *>(a.logits) + row * a.stride;
-  constexpr int U = sizeof(T) == 2 ? 4 : 2;
-  Running run;
-  each_chunks<T, kScanThreads, U>(z, lo, hi, [&](int64_t at, float (&v)[U][8]) {
-    float m = run.max;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t i = at + u * kScanTile + 8 * threadIdx.x;
-      leave_out(v[u], i < hi ? bytes[(i - lo) >> 3] : 0u);
-      m = max8(m, v[u]);
-    }
-    const float ref = run.raise(m, a.c);
-#pragma unroll
-    for (int u = 0; u < U; ++u) run.add(v[u], ref, a.c);
-  });
-  const RowSum s = block_join<kScanThreads>(run, a.c, part);
-  if (threadIdx.x == 0) a.parts[row * a.segs + seg] = {s.sum, s.max, 0u};
+  loss = block_sum<kScanThreads>(loss, part);
+  if (threadIdx.x == 0)
+    a.parts[row * a.segs + seg] = {rest.sum, named.sum, loss, rest.max, named.max};
 }
 
-// A block to a row: the segments' sums joined, the row's statistics and loss.
-template <class T>
+// A row's parts, joined by every wavefront for itself.
+struct Joined {
+  RowSum rest, named;
+  double loss;
+};
+__device__ __forceinline__ Joined join_parts(const DistillArgs &a, int64_t row) {
+  const DistillPart *parts = a.parts + row * a.segs;
+  const int lane = threadIdx.x % kWave;
+  float mr = kNegInf, mn = kNegInf;
+  for (int64_t i = lane; i < a.segs; i += kWave) {
+    mr = max3(mr, parts[i].rest_max, kNegInf);
+    mn = max3(mn, parts[i].named_max, kNegInf);
+  }
+  mr = wave_max(mr);
+  mn = wave_max(mn);
+  double sr = 0.0, sn = 0.0, loss = 0.0;
+  for (int64_t i = lane; i < a.segs; i += kWave) {
+    const DistillPart p = parts[i];
+    sr += moved(p.rest_sum, p.rest_max, ref_of(mr), a.c);
+    // (fp64 terms: the step is too)
+    sn += p.named_max == kNegInf
+              ? p.named_sum
+              : p.named_sum * exp64(((double)p.named_max - (double)ref_of(mn)) / a.temperature);
+    loss += p.loss;
+  }
+  return {{mr, wave_sum(sr)}, {mn, wave_sum(sn)}, wave_sum(loss)};
+}
+
+// Loss and statistics of a row from its parts, written by one lane.
+__device__ __forceinline__ void write_joined(const DistillArgs &a, int64_t row, const Joined &v,
+                                             const Whole &whole, const Target &t) {
+  const double T_ = a.temperature, none = -__builtin_inf();
+  const double lse = log_sum(whole.all, T_), lse_rest = a.rest ? log_sum(v.rest, T_) : 0.0;
+  if (a.lse != nullptr) a.lse[row] = (float)lse;
+  if (a.rest && a.lse_rest != nullptr) a.lse_rest[row] = (float)lse_rest;
+  if (a.loss == nullptr) return;
+  // (where no logit is finite the parts hold the infinite loss of their targets)
+  double loss = lse == none || t.m == 0.0 ? v.loss : v.loss + t.m * lse;
+  if (t.r != 0.0) loss += t.r * (log64(t.r) - (lse_rest == none ? none : lse_rest - lse));
+  a.loss[row] = t.none ? 0.0f : (float)loss;
+}
+
+// A wavefront to a row: its parts joined.
 __global__ __launch_bounds__(kScanThreads) void distill_finish_kernel(const DistillArgs a) {
   __shared__ double part[kScanThreads / kWave];
   const int64_t row = blockIdx.x;
-  const T *z = static_cast<const T *>(a.logits) + row * a.stride;
   RawEntries<kScanThreads> raw;
-  raw.load(a, row);
+  raw.load(a, row, threadIdx.x);
   Entries e(lds, a.top);
-  const Target t = read_target<kScanThreads>(a, row, raw, 0, a.vocab, 0, e, part, a.err);
-  for (int j = threadIdx.x; j < (int)a.top; j += kScanThreads)
-    e.z[j] = e.ids[j] >= 0 ? Chunk<T>::one(z[e.ids[j]]) : kNegInf;
-  const RowSum rest = wave_join(a.parts + row * a.segs, a.segs, a.c);
-  const RowSum named = sum_named<kScanThreads>(a, e, part);
-  write_row<kScanThreads>(a, row, rest, both(rest, named, a.temperature).all, e, t,
-                          part);
+  const Target t = read_target<kScanThreads>(a, row, raw, 0, 0, 0, e, part, nullptr);
+  if (threadIdx.x >= kWave) return;
+  const Joined v = join_parts(a, row);
+  const Whole whole = both(v.rest, v.named, a.temperature);
+  if (threadIdx.x == 0) write_joined(a, row, v, whole, t);
 }
 
-// A block to a segment of a row: its gradient, from the statistics that were kept.
-// SHORT: a vocabulary of less than eight values.
-template <class T, bool SHORT>
-__global__ __launch_bounds__(kScanThreads) void distill_backward_kernel(const DistillArgs a) {
+// A block to a segment of a row: its gradient, from the statistics that were kept or, with
+// PARTS, from the parts that distill_scan_kernel left (the first segment's block then also
+// writes the row's loss and statistics).  SHORT: a vocabulary of less than eight values.
+template <class T, bool SHORT, bool PARTS>
+__global__ __launch_bounds__(kScanThreads) void distill_backward_kernel(const DistillArgs a,
+                                                                        const int64_t segs) {
   constexpr int N = distill_held_backward(sizeof(T));
   __shared__ double part[kScanThreads / kWave];
-  const int64_t row = blockIdx.x / a.segs, seg = blockIdx.x - row * a.segs;
+  const int64_t row = blockIdx.x / segs, seg = blockIdx.x - row * segs;
   // (whole chunks are shared out, so that every segment has eight values or more)
-  const int64_t chunks = a.vocab / 8, lo = chunks * seg / a.segs * 8;
-  const int64_t hi = seg + 1 == a.segs ? a.vocab : chunks * (seg + 1) / a.segs * 8;
+  const int64_t chunks = a.vocab / 8, lo = chunks * seg / segs * 8;
+  const int64_t hi = seg + 1 == segs ? a.vocab : chunks * (seg + 1) / segs * 8;
   const T *z = static_cast<const T *>(a.logits) + row * a.stride;
   T *grad = static_cast<T *>(a.grad) + row * a.grad_stride;
   const double T_ = a.temperature;
   RawEntries<kScanThreads> raw;
-  raw.load(a, row);
+  raw.load(a, row, threadIdx.x);
   Held<T, kScanThreads, N> held;
   if (!SHORT) held.load(z + lo, (int)(hi - lo));
   Entries e(lds, a.top);
   const Target t = read_target<kScanThreads>(a, row, raw, lo, hi, (int)(hi - lo + 31) / 32, e,
-                                             part, seg == 0 ? a.err : nullptr);
-  const float g = raw.weight;
-  if (g == 0.0f || t.none) {
+                                             part, !PARTS && seg == 0 ? a.err : nullptr);
+  // the unnamed: factor * exp((z - ref) / T); the named: q = exp(z / T - below) * scale
+  double below, scale = 1.0, f;
+  const double gt = raw.weight / T_;
+  float ref;
+  if (PARTS) {
+    const Joined v = join_parts(a, row);
+    const Whole whole = both(v.rest, v.named, T_);
+    if (seg == 0 && threadIdx.x == 0) write_joined(a, row, v, whole, t);
+    ref = ref_of(v.rest.max);
+    f = v.rest.sum == 0.0 ? 0.0 : gt * ((t.m + t.r) * whole.s - t.r) / v.rest.sum;
+    below = ref_of(whole.all.max) / T_;
+    scale = whole.all.sum == 0.0 ? 0.0 : 1.0 / whole.all.sum;
+  } else {
+    // base: the log of the unnamed values' own sum, or of the whole one without a class for
+    // the rest
+    const double lse = a.lse[row], base = a.rest ? a.lse_rest[row] : lse;
+    const bool empty = base == -__builtin_inf();
+    ref = empty || base != base ? 0.0f : (float)(base * T_);
+    f = gt * t.m;
+    if (a.rest) f = gt * ((t.m + t.r) * (empty ? 0.0 : exp64(base - lse)) - t.r);
+    f = empty ? 0.0 : f * exp64(ref / T_ - base);
+    below = lse == -__builtin_inf() ? 0.0 : lse;
+    scale = lse == -__builtin_inf() ? 0.0 : 1.0;
+  }
+  if (raw.weight == 0.0f || t.none) {
     write_zeros(grad, lo, hi, kScanThreads);
     return;
   }
@@ -496,29 +625,23 @@ __global__ __launch_bounds__(kScanThreads) void distill_backward_kernel(const Di
     const int32_t id = e.ids[j];
     e.z[j] = id >= lo && id < hi ? Chunk<T>::one(z[id]) : kNegInf;
   }
-  // the unnamed: factor * exp(z / T - base), base the log of their own sum (of the whole
-  // sum without a class for the rest)
-  const double lse = a.lse[row], base = a.rest ? a.lse_rest[row] : lse, gt = g / T_;
-  const bool empty = base == -__builtin_inf();
-  const float ref = empty || base != base ? 0.0f : (float)(base * T_);
-  double f = gt * t.m;
-  if (a.rest) f = gt * ((t.m + t.r) * (empty ? 0.0 : exp64(base - lse)) - t.r);
-  const float factor = empty ? 0.0f : (float)(f * exp64(ref / T_ - base));
+  const float factor = (float)f;
   float one = kNegInf;
   if (SHORT && threadIdx.x < a.vocab) one = Chunk<T>::one(z[threadIdx.x]);
   __syncthreads();
   if (!SHORT)
-    held.write(grad + lo, (int)(hi - lo), factor, ref, a.c);
+    held.template write<false>(grad + lo, (int)(hi - lo), factor, ref, a.c, nullptr, false);
   else if (threadIdx.x < a.vocab)
-    store1(grad + threadIdx.x, factor * exp2_fast((one - ref) * a.c));
+    store1(grad + threadIdx.x, factor * exp_scaled(one - ref, a.c));
   __syncthreads();
   write_named<T, kScanThreads>(a, grad, lo, hi, gt, e, t, [&](float x) {
-    return lse == -__builtin_inf() ? 0.0 : exp64(x / T_ - lse);
+    return scale == 0.0 ? 0.0 : exp64(x / T_ - below) * scale;
   });
 }
 
 DistillArgs device_args(const engram_distill_args &h, const ScanShape &shape) {
   DistillArgs a = {};
+  a.rows = h.rows;
   a.vocab = h.vocab;
   a.top = h.top;
   a.stride = h.logits_stride;
@@ -526,7 +649,7 @@ DistillArgs device_args(const engram_distill_args &h, const ScanShape &shape) {
   a.segs = shape.segs;
   a.seg_len = shape.seg_len;
   a.temperature = h.temperature;
-  a.c = (float)(1.4426950408889634 / (double)h.temperature);
+  a.c = scale_of(h.temperature);
   a.teacher_type = h.teacher_type;
   a.rest = h.rest;
   a.logits = h.d_logits;
@@ -547,28 +670,28 @@ size_t lds_bytes(int64_t top, int64_t values) {
 }
 
 template <class T, int THREADS>
-void enqueue_hold(const DistillArgs &a, int64_t rows, hipStream_t stream) {
-  const dim3 grid((unsigned)rows), block(THREADS);
-  const size_t bytes = lds_bytes(a.top, a.vocab);
-  if (a.grad != nullptr)
-    hipLaunchKernelGGL((distill_hold_kernel<T, THREADS, true>), grid, block, bytes, stream, a);
-  else
-    hipLaunchKernelGGL((distill_hold_kernel<T, THREADS, false>), grid, block, bytes, stream, a);
+void enqueue_hold(const DistillArgs &a, hipStream_t stream) {
+  // as many blocks as stay on the GPU together
+  const int64_t most = kComputeUnits * (1024 / THREADS);
+  hipLaunchKernelGGL((distill_hold_kernel<T, THREADS>),
+                     dim3((unsigned)(a.rows < most ? a.rows : most)), dim3(THREADS),
+                     lds_bytes(a.top, a.vocab), stream, a);
 }
 
-template <class T>
-int enqueue_backward(const engram_distill_args &h, DistillArgs a) {
+template <class T, bool PARTS>
+int enqueue_backward(const DistillArgs &a, hipStream_t stream) {
   const int64_t most = kScanThreads * distill_held_backward(sizeof(T));
   // (a segment of a row's chunks, and what is left of the last)
-  a.segs = h.vocab < 8 ? 1 : ceil_div(h.vocab / 8, most - 1);
-  if (!grid_fits(h.rows * a.segs, kScanThreads)) return ENGRAM_EINVAL;
-  const dim3 grid((unsigned)(h.rows * a.segs)), block(kScanThreads);
-  const size_t bytes = lds_bytes(h.top, most * 8);
-  const hipStream_t stream = as_stream(h.stream);
-  if (h.vocab < 8)
-    hipLaunchKernelGGL((distill_backward_kernel<T, true>), grid, block, bytes, stream, a);
+  const int64_t segs = a.vocab < 8 ? 1 : ceil_div(a.vocab / 8, most - 1);
+  if (!grid_fits(a.rows * segs, kScanThreads)) return ENGRAM_EINVAL;
+  const dim3 grid((unsigned)(a.rows * segs)), block(kScanThreads);
+  const size_t bytes = lds_bytes(a.top, most * 8);
+  if (a.vocab < 8)
+    hipLaunchKernelGGL((distill_backward_kernel<T, true, PARTS>), grid, block, bytes, stream, a,
+                       segs);
   else
-    hipLaunchKernelGGL((distill_backward_kernel<T, false>), grid, block, bytes, stream, a);
+    hipLaunchKernelGGL((distill_backward_kernel<T, false, PARTS>), grid, block, bytes, stream, a,
+                       segs);
   return launch_status();
 }
 
@@ -577,31 +700,32 @@ int enqueue(const engram_distill_args &h) {
   const ScanShape shape = distill_shape(h.rows, h.vocab);
   DistillArgs a = device_args(h, shape);
   const hipStream_t stream = as_stream(h.stream);
-  const int threads = distill_threads(h.vocab, sizeof(T));
+  const bool grad = h.d_grad != nullptr;
+  const int threads = grad ? distill_threads(h.rows, h.vocab, sizeof(T)) : 0;
   if (!grid_fits(h.rows, 1024) || !grid_fits(h.rows * shape.segs, kScanThreads))
     return ENGRAM_EINVAL;
-  if (threads != 0) {
-    if (threads == 256)
-      enqueue_hold<T, 256>(a, h.rows, stream);
-    else if (threads == 512)
-      enqueue_hold<T, 512>(a, h.rows, stream);
+  if (threads == 256) {
+    enqueue_hold<T, 256>(a, stream);
+  } else if (threads == 512) {
+    enqueue_hold<T, 512>(a, stream);
+  } else if (threads == 1024) {
+    enqueue_hold<T, 1024>(a, stream);
+  } else if (!grad && h.vocab <= kDistillMaxSeg) {
+    const dim3 rows((unsigned)h.rows);
+    const size_t bytes = lds_bytes(h.top, h.vocab);
+    if (h.rows <= kDistillWideRows)
+      hipLaunchKernelGGL((distill_row_kernel<T, 1024>), rows, dim3(1024), bytes, stream, a);
     else
-      enqueue_hold<T, 1024>(a, h.rows, stream);
-    return launch_status();
+      hipLaunchKernelGGL((distill_row_kernel<T, 256>), rows, dim3(256), bytes, stream, a);
+  } else {
+    a.parts = static_cast<DistillPart *>(h.d_workspace);
+    hipLaunchKernelGGL(distill_scan_kernel<T>, dim3((unsigned)(h.rows * shape.segs)),
+                       dim3(kScanThreads), lds_bytes(h.top, shape.seg_len), stream, a);
+    if (grad) return enqueue_backward<T, true>(a, stream);
+    hipLaunchKernelGGL(distill_finish_kernel, dim3((unsigned)h.rows), dim3(kScanThreads),
+                       lds_bytes(h.top, 0), stream, a);
   }
-  a.parts = static_cast<ScanPart *>(h.d_workspace);
-  float *kept = reinterpret_cast<float *>(a.parts + h.rows * shape.segs);
-  if (h.d_grad != nullptr) {
-    if (a.lse == nullptr) a.lse = kept;
-    if (a.lse_rest == nullptr) a.lse_rest = kept + h.rows;
-  }
-  hipLaunchKernelGGL(distill_scan_kernel<T>, dim3((unsigned)(h.rows * shape.segs)),
-                     dim3(kScanThreads), (size_t)shape.seg_len / 8, stream, a);
-  hipLaunchKernelGGL(distill_finish_kernel<T>, dim3((unsigned)h.rows), dim3(kScanThreads),
-                     lds_bytes(h.top, 0), stream, a);
-  if (h.d_grad == nullptr) return launch_status();
-  a.err = nullptr;  // counted already
-  return enqueue_backward<T>(h, a);
+  return launch_status();
 }
 
 }  // namespace
@@ -613,6 +737,7 @@ int engram::launch_distill(const engram_distill_args &h) {
 
 int engram::launch_distill_backward(const engram_distill_args &h) {
   const DistillArgs a = device_args(h, ScanShape{});
-  return h.logits_type == ENGRAM_BF16 ? enqueue_backward<uint16_t>(h, a)
-                                      : enqueue_backward<float>(h, a);
+  const hipStream_t stream = as_stream(h.stream);
+  return h.logits_type == ENGRAM_BF16 ? enqueue_backward<uint16_t, false>(a, stream)
+                                      : enqueue_backward<float, false>(a, stream);
 }

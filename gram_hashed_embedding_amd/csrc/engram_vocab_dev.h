@@ -10,6 +10,8 @@
 // logarithm is taken too.
 #pragma once
 
+#include <math.h>
+
 #include "engram_layer_dev.h"
 #include "engram_vocab_host.h"
 
@@ -19,7 +21,9 @@ constexpr float kNegInf = -__builtin_inff();
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// max(a, b, c) in one instruction (fmaxf quiets its operands first).
+// max(a, b, c) in one instruction (fmaxf quiets its operands first).  Its result goes to
+// ordinary instructions only: the compiler does not know it for a vector instruction, and
+// would leave no wait states before one that moves data across lanes.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
@@ -38,6 +42,7 @@ struct Chunk<uint16_t> {
   __device__ static __forceinline__ float one(uint16_t v) { return bf16_lo(v); }
   // hides where the bits came from, so that nothing made of them is kept
   __device__ __forceinline__ void renew() { asm volatile("" : "+v"(r)); }
+  __device__ __forceinline__ void clear() { r = u32x4{0u, 0u, 0u, 0u}; }
 };
 template <>
 struct Chunk<float> {
@@ -52,6 +57,7 @@ struct Chunk<float> {
   }
   __device__ static __forceinline__ float one(float v) { return v; }
   __device__ __forceinline__ void renew() { asm volatile("" : "+v"(a), "+v"(b)); }
+  __device__ __forceinline__ void clear() { a = b = f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
 };
 
 __device__ __forceinline__ float max8(float m, const float (&z)[8]) {
@@ -63,48 +69,84 @@ __device__ __forceinline__ float max8(float m, const float (&z)[8]) {
 // so that no difference of infinities arises.
 __device__ __forceinline__ float ref_of(float max) { return max == kNegInf ? 0.0f : max; }
 
+// log2(e) / temperature, in two parts: rounded to one, it would be off by up to 2^-25 of
+// it, which in the exponent of a term far below the maximum is more than fp32's rounding.
+// The second part is above 0, so that -inf times it is -inf as well.
+struct Scale {
+  float hi, lo;
+};
+inline Scale scale_of(float temperature) {
+  const double c = 1.4426950408889634 / (double)temperature;
+  float hi = (float)c;
+  while ((double)hi >= c) hi = nextafterf(hi, 0.0f);
+  return {hi, (float)(c - (double)hi)};
+}
+__device__ __forceinline__ float exp_scaled(float d, Scale c) {
+  return exp2_fast(__builtin_fmaf(d, c.lo, d * c.hi));
+}
+
 struct Running {
   float max = kNegInf, sum = 0.0f;
   // raises the maximum to at least m, and gives the point that exponents are taken from
-  __device__ __forceinline__ float raise(float m, float c) {
+  __device__ __forceinline__ float raise(float m, Scale c) {
     const float ref = ref_of(m);
-    sum *= exp2_fast((max - ref) * c);  // (2^-inf while there was none)
+    sum *= exp_scaled(max - ref, c);  // (2^-inf while there was none)
     max = m;
     return ref;
   }
-  __device__ __forceinline__ void add(const float (&z)[8], float ref, float c) {
+  __device__ __forceinline__ void add(const float (&z)[8], float ref, Scale c) {
     float e[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = exp2_fast((z[i] - ref) * c);
+    for (int i = 0; i < 8; ++i) e[i] = exp_scaled(z[i] - ref, c);
     sum += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
   }
 };
+
+// A constant made in scalar registers where it is used (as a literal the compiler keeps it
+// in vector registers throughout a loop around it).
+__device__ __forceinline__ double scalar(double v) {
+  asm volatile("" : "+s"(v));
+  return v;
+}
 
 // exp in fp64 by its series around 0 (|r| <= ln(2) / 2: the 11th power's term is
 // 2e-13), in few registers.
 __device__ __forceinline__ double exp64(double x) {
   x = x < -800.0 ? -800.0 : x;  // (0; a NaN stays one)
-  const double n = rint(x * 1.44269504088896340736);
-  const double r = fma(-n, 0.693147180559945309417, x);
-  double p = 1.0 / 3628800.0;
-  p = fma(p, r, 1.0 / 362880.0);
-  p = fma(p, r, 1.0 / 40320.0);
-  p = fma(p, r, 1.0 / 5040.0);
-  p = fma(p, r, 1.0 / 720.0);
-  p = fma(p, r, 1.0 / 120.0);
-  p = fma(p, r, 1.0 / 24.0);
-  p = fma(p, r, 1.0 / 6.0);
+  const double n = rint(x * scalar(1.44269504088896340736));
+  const double r = fma(-n, scalar(0.693147180559945309417), x);
+  double p = scalar(1.0 / 3628800.0);
+  p = fma(p, r, scalar(1.0 / 362880.0));
+  p = fma(p, r, scalar(1.0 / 40320.0));
+  p = fma(p, r, scalar(1.0 / 5040.0));
+  p = fma(p, r, scalar(1.0 / 720.0));
+  p = fma(p, r, scalar(1.0 / 120.0));
+  p = fma(p, r, scalar(1.0 / 24.0));
+  p = fma(p, r, scalar(1.0 / 6.0));
   p = fma(p, r, 0.5);
   p = fma(p, r, 1.0);
   p = fma(p, r, 1.0);
   return ldexp(p, (int)n);
 }
 
+// log in fp64: of x = 2^e m, m in [1/2, 1), from y = log(m) in fp32 (an error of about 1e-7)
+// and one step of Newton's method, log(m) = y + log(1 + d), d = m exp(-y) - 1, of which d^3 is
+// beyond fp64.
+__device__ __forceinline__ double log64(double x) {
+  if (!(x > 0.0) || __builtin_isinf(x))
+    return x == 0.0 ? -__builtin_inf() : x > 0.0 ? x : __builtin_nan("");
+  int e;
+  const double m = frexp(x, &e);
+  const double y = (double)(__builtin_amdgcn_logf((float)m) * 0.693147182464599609375f);
+  const double d = fma(m, exp64(-y), -1.0);
+  return fma((double)e, scalar(0.693147180559945309417), y + (d - 0.5 * d * d));
+}
+
 // ----------------------------------------------- reductions over wavefronts --
 template <int LANES>
 __device__ __forceinline__ float lanes_max_of(float v) {
   return __uint_as_float(lanes_reduce<LANES>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
-    return __float_as_uint(max3(__uint_as_float(a), __uint_as_float(b), kNegInf));
+    return __float_as_uint(__builtin_fmaxf(__uint_as_float(a), __uint_as_float(b)));
   }));
 }
 __device__ __forceinline__ float wave_max(float v) { return lanes_max_of<kWave>(v); }
@@ -149,38 +191,66 @@ __device__ __forceinline__ double wave_max(double v) {
   return lanes_reduce<kWave>(v, [](double a, double b) { return fmax(a, b); });
 }
 
+// The thread's number, hidden from the compiler: what is made of it inside a loop is made
+// there, not kept in registers from before it.
+__device__ __forceinline__ int hidden_thread() {
+  int t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
+
+// The same for a number that every lane has alike.
+__device__ __forceinline__ int hidden(int n) {
+  asm volatile("" : "+s"(n));
+  return n;
+}
+
+// A value that every lane has alike, in scalar registers.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+}
+__device__ __forceinline__ float uniform(float v) {
+  return __uint_as_float(uniform(__float_as_uint(v)));
+}
+__device__ __forceinline__ double uniform(double v) {
+  return double_of(uniform(low_of(v)), uniform(high_of(v)));
+}
+
 // Over a block, in the same order for every row; `part` holds a slot a wavefront, which
 // each wavefront's lanes read one to a lane.
 template <int THREADS, class V>
-__device__ __forceinline__ V wave_of(const V *part) {
-  return part[threadIdx.x % (THREADS / kWave)];
+__device__ __forceinline__ V wave_of(const V *part, int t) {
+  return part[t % (THREADS / kWave)];
 }
 template <int THREADS>
-__device__ __forceinline__ double block_sum(double v, double *part) {
+__device__ __forceinline__ double block_sum(double v, double *part,
+                                            int t = threadIdx.x) {
   v = wave_sum(v);
-  if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = v;
+  if (t % kWave == 0) part[t / kWave] = v;
   __syncthreads();
-  v = wave_of<THREADS>(part);
+  v = wave_of<THREADS>(part, t);
   __syncthreads();
-  return lanes_reduce<THREADS / kWave>(v, [](double a, double b) { return a + b; });
+  return uniform(lanes_reduce<THREADS / kWave>(v, [](double a, double b) { return a + b; }));
 }
 template <int THREADS>
-__device__ __forceinline__ double block_max(double v, double *part) {
+__device__ __forceinline__ double block_max(double v, double *part,
+                                            int t = threadIdx.x) {
   v = wave_max(v);
-  if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = v;
+  if (t % kWave == 0) part[t / kWave] = v;
   __syncthreads();
-  v = wave_of<THREADS>(part);
+  v = wave_of<THREADS>(part, t);
   __syncthreads();
-  return lanes_reduce<THREADS / kWave>(v, [](double a, double b) { return fmax(a, b); });
+  return uniform(lanes_reduce<THREADS / kWave>(v, [](double a, double b) { return fmax(a, b); }));
 }
 template <int THREADS>
-__device__ __forceinline__ float block_max(float v, float *part) {
+__device__ __forceinline__ float block_max(float v, float *part,
+                                            int t = threadIdx.x) {
   v = wave_max(v);
-  if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = v;
+  if (t % kWave == 0) part[t / kWave] = v;
   __syncthreads();
-  v = wave_of<THREADS>(part);
+  v = wave_of<THREADS>(part, t);
   __syncthreads();
-  return lanes_max_of<THREADS / kWave>(v);
+  return uniform(lanes_max_of<THREADS / kWave>(v));
 }
 
 // A sum of exponentials with its maximum: of exp((z - max) / temperature).
@@ -189,17 +259,18 @@ struct RowSum {
   double sum;
 };
 // s, taken from max, as taken from ref.
-__device__ __forceinline__ double moved(double s, float max, float ref, float c) {
-  return max == kNegInf ? s : s * (double)exp2_fast((max - ref) * c);
+__device__ __forceinline__ double moved(double s, float max, float ref, Scale c) {
+  return max == kNegInf ? s : s * (double)exp_scaled(max - ref, c);
 }
 // The lanes' running sums over a block.
 template <int THREADS>
-__device__ __forceinline__ RowSum block_join(const Running &run, float c, double *part) {
-  const float m = block_max<THREADS>(run.max, reinterpret_cast<float *>(part));
-  return {m, block_sum<THREADS>(moved(run.sum, run.max, ref_of(m), c), part)};
+__device__ __forceinline__ RowSum block_join(const Running &run, Scale c, double *part,
+                                             int t = threadIdx.x) {
+  const float m = block_max<THREADS>(run.max, reinterpret_cast<float *>(part), t);
+  return {m, block_sum<THREADS>(moved(run.sum, run.max, ref_of(m), c), part, t)};
 }
 // The sums of a row's segments, joined by a wavefront.
-__device__ __forceinline__ RowSum wave_join(const ScanPart *parts, int64_t n, float c) {
+__device__ __forceinline__ RowSum wave_join(const ScanPart *parts, int64_t n, Scale c) {
   float m = kNegInf;
   for (int64_t i = threadIdx.x % kWave; i < n; i += kWave) m = max3(m, parts[i].max, kNegInf);
   m = wave_max(m);
@@ -210,16 +281,17 @@ __device__ __forceinline__ RowSum wave_join(const ScanPart *parts, int64_t n, fl
 }
 // log of the sum of exp(z / temperature): -inf for none.
 __device__ __forceinline__ double log_sum(const RowSum &v, double temperature) {
-  return ref_of(v.max) / temperature + log(v.sum);
+  return ref_of(v.max) / temperature + log64(v.sum);
 }
 
 // -------------------------------------------------------- reading a segment --
 // The values [lo, hi) of a row by a block, U chunks a lane at a time: use(at, z) is
 // called by every lane with the chunks that start at at + 8 * (u * THREADS + lane);
-// values past hi are -inf.  The next chunks' loads are on their way meanwhile (the last
-// step's once more, so that no load hangs on a condition).
-template <class T, int THREADS, int U, class USE>
-__device__ __forceinline__ void each_chunks(const T *row, int64_t lo, int64_t hi, USE use) {
+// values past hi are -inf.  The next chunks' loads are on their way meanwhile; first() is
+// called once, behind the first ones.
+template <class T, int THREADS, int U, class FIRST, class USE>
+__device__ __forceinline__ void each_chunks(const T *row, int64_t lo, int64_t hi, FIRST first,
+                                            USE use) {
   constexpr int kTile = 8 * THREADS, kStep = U * kTile;
   const int t = threadIdx.x;
   const int64_t last = lo + (hi - lo) / kStep * kStep - kStep;  // the last whole step
@@ -228,18 +300,25 @@ __device__ __forceinline__ void each_chunks(const T *row, int64_t lo, int64_t hi
     Chunk<T> r[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) r[u].load(row + at + u * kTile + 8 * t);
-    for (; at <= last; at += kStep) {
+    first();
+    for (; at < last; at += kStep) {
       float z[U][8];
-      const int64_t next = at + kStep <= last ? at + kStep : last;
       Chunk<T> n[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) n[u].load(row + next + u * kTile + 8 * t);
+      for (int u = 0; u < U; ++u) n[u].load(row + at + kStep + u * kTile + 8 * t);
 #pragma unroll
       for (int u = 0; u < U; ++u) r[u].values(z[u]);
       use(at, z);
 #pragma unroll
       for (int u = 0; u < U; ++u) r[u] = n[u];
     }
+    float z[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) r[u].values(z[u]);
+    use(at, z);
+    at += kStep;
+  } else {
+    first();
   }
   if (at < hi) {
     float z[U][8];

@@ -38,36 +38,46 @@ struct ScanPart {
 };
 
 // ------------------------------------------------------------ distillation --
-// Chunks of 8 values that a lane holds of a row, for values of `size` bytes (80
-// registers of the 128 that 1024 threads have each), and of a segment in the
-// backward pass.
-constexpr int distill_held(size_t size) { return size == 2 ? 20 : 10; }
-constexpr int distill_held_backward(size_t size) { return size == 2 ? 8 : 4; }
-// The threads of a block that holds a whole row; 0 where none does.
-inline int distill_threads(int64_t vocab, size_t size) {
-  for (int threads = 256; threads <= 1024; threads *= 2)
-    if (vocab >= 8 && vocab <= threads * 8 * distill_held(size)) return threads;
-  return 0;
+// Chunks of 8 values that a lane holds of a row, for values of `size` bytes (of the 128
+// registers that a lane has in blocks of 1024, or four blocks of 256, on a CU), and of a
+// segment in the backward pass.
+constexpr int distill_held(size_t size, int threads) {
+  return (threads >= 512 ? 20 : 16) * 2 / (int)size;
 }
-// Other rows are cut: one bit a value marks the ids that a teacher's row names, in
-// LDS: 32 KB.
+constexpr int distill_held_backward(size_t size) { return size == 2 ? 8 : 4; }
+// Rows are cut where a gradient is asked for and there are few of them, and where a row's
+// bits (one a value: whether a teacher's row names it) would take more than 32 KB of LDS.
 constexpr int64_t kDistillMaxSeg = int64_t(1) << 18;
 constexpr int64_t kDistillBlocks = 1024;
+constexpr int64_t kDistillFewRows = 128, kDistillFewVocab = 65536;
 inline ScanShape distill_shape(int64_t rows, int64_t vocab) {
   return scan_shape(rows, vocab, kDistillBlocks, kDistillMaxSeg);
 }
-// The parts of every segment, then the two fp32 statistics of each row for the
-// gradient; nothing where a block holds a row.
-inline size_t distill_workspace(int64_t rows, int64_t vocab, int32_t type) {
-  if (rows == 0 || distill_threads(vocab, type == ENGRAM_BF16 ? 2 : 4) != 0) return 0;
-  const ScanShape s = distill_shape(rows, vocab);
-  return (size_t)rows * (size_t)s.segs * sizeof(ScanPart) + (size_t)rows * 8;
+// The threads of a block that holds a whole row for its gradient; 0 where none does.
+inline int distill_threads(int64_t rows, int64_t vocab, size_t size) {
+  if (vocab < 8 || (rows <= kDistillFewRows && vocab >= kDistillFewVocab)) return 0;
+  for (int threads = 256; threads <= 1024; threads *= 2)
+    if (vocab <= threads * 8 * distill_held(size, threads)) return threads;
+  return 0;
+}
+// What a segment of a row leaves: its sums (of the values that the teacher does not name,
+// and of those it does) beside their maxima, and its part of the loss.
+struct DistillPart {
+  double rest_sum, named_sum, loss;
+  float rest_max, named_max;
+};
+// The parts of every segment; nothing where a block takes a row.
+inline size_t distill_workspace(int64_t rows, int64_t vocab, int32_t type, bool grad) {
+  const bool cut = grad ? distill_threads(rows, vocab, type == ENGRAM_BF16 ? 2 : 4) == 0
+                        : vocab > kDistillMaxSeg;
+  if (rows == 0 || !cut) return 0;
+  return (size_t)rows * (size_t)distill_shape(rows, vocab).segs * sizeof(DistillPart);
 }
 
 // --------------------------------------------------------------- selection --
 // The scan leaves the largest logit of every kBeamGroup values.
 constexpr int64_t kBeamGroup = 128;
-constexpr int64_t kBeamBlocks = 2048;
+constexpr int64_t kBeamBlocks = 1024;
 constexpr int64_t kBeamMaxSeg = int64_t(1) << 18;
 inline ScanShape beam_shape(int64_t rows, int64_t vocab) {
   return scan_shape(rows, vocab, kBeamBlocks, kBeamMaxSeg);

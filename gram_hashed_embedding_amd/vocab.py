@@ -148,7 +148,7 @@ def engram_distill(logits, ids, teacher, *, teacher_lse=None, rest=False, temper
             lse_rest = torch.empty(lead, dtype=torch.float32, device=device)
         rest_p = _per_row(lse_rest, lead, rows, "lse_rest", index)
     err_p = _optional(err_count, torch.int64, 1, "err_count", index)
-    ws_p, size = 0, _lib.engram_distill_workspace(rows, vocab, kind)
+    ws_p, size = 0, _lib.engram_distill_workspace(rows, vocab, kind, int(bool(grad_p)))
     if size:
         workspace = _bytes(workspace, size, device, index, "engram_distill_workspace")
         ws_p, size = workspace.data_ptr(), workspace.numel()
@@ -185,8 +185,8 @@ def engram_distill_backward(grad_loss, logits, ids, teacher, lse, *, teacher_lse
     return grad
 
 
-def engram_distill_workspace(rows, vocab, dtype=torch.bfloat16) -> int:
-    need = _lib.engram_distill_workspace(rows, vocab, _TYPES[dtype])
+def engram_distill_workspace(rows, vocab, dtype=torch.bfloat16, grad=False) -> int:
+    need = _lib.engram_distill_workspace(rows, vocab, _TYPES[dtype], int(bool(grad)))
     if need == _BAD_SIZE:
         raise EngramError(abi.ENGRAM_EINVAL, "engram_distill_workspace")
     return need
