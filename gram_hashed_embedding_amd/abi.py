@@ -1,5 +1,6 @@
 """ctypes declarations of the libengram.so C ABI (include/engram.h, and
-include/engram_layer.h in declare_layer), without torch: the binding (engram.py) applies them to the built library, and the
+include/engram_layer.h in declare_layer, include/engram_vocab.h in declare_vocab), without
+torch: the binding (engram.py) applies them to the built library, and the
 host-side checks of the same entry points, built for the CPU under
 sanitizers, are driven through them by the tests.
 """
@@ -32,6 +33,10 @@ BF16 = 0                          # ENGRAM_BF16
 F32 = 1                           # ENGRAM_F32
 ACT_BLOCK = 128                   # ENGRAM_ACT_BLOCK
 NORM_MAX_GROUP = 16384            # ENGRAM_NORM_MAX_GROUP
+
+DISTILL_MAX_TOP = 1024            # ENGRAM_DISTILL_MAX_TOP
+BEAM_MAX = 64                     # ENGRAM_BEAM_MAX
+FORK_MAX_POOLS = 8                # ENGRAM_FORK_MAX_POOLS
 
 _i64p = ctypes.POINTER(ctypes.c_int64)
 _vp = ctypes.c_void_p
@@ -171,11 +176,6 @@ def declare_layer(lib):
     return lib
 
 
-DISTILL_MAX_TOP = 1024            # ENGRAM_DISTILL_MAX_TOP
-BEAM_MAX = 64                     # ENGRAM_BEAM_MAX
-FORK_MAX_POOLS = 8                # ENGRAM_FORK_MAX_POOLS
-
-
 class EngramDistillArgs(ctypes.Structure):
     """struct engram_distill_args of include/engram_vocab.h, field for field."""
     _fields_ = [
@@ -202,8 +202,7 @@ def declare_vocab(lib):
         ("engram_beam_select", ctypes.c_int,
          [_vp, i32, i64, _vp, _vp, i64, i64, i64, i64, i64, _vp, _vp, _vp, _vp, _vp, size, _vp]),
         ("engram_beam_fork", ctypes.c_int,
-         [_vp, _vp, i64, i64, ctypes.POINTER(_vp), _i64p, i32, i64, _vp, _vp, _vp, i64, _vp, i64,
-          _vp, _vp]),
+         [_vp, _vp, i64, i64, _vp, _vp, i32, i64, _vp, _vp, _vp, i64, _vp, i64, _vp, _vp]),
     ]:
         f = getattr(lib, name)
         f.restype, f.argtypes = result, args

@@ -12,6 +12,7 @@ in the header.
 from __future__ import annotations
 
 import ctypes
+import math
 import struct
 from typing import NamedTuple, Optional
 
@@ -48,11 +49,33 @@ def _logits(t, what):
     kind = _TYPES.get(t.dtype)
     if kind is None:
         raise TypeError(f"{what} must be bfloat16 or float32, is {t.dtype}")
-    vocab = t.shape[-1] if t.dim() else 0
+    shape = t.shape
+    vocab = shape[-1] if shape else 0
     if vocab < 1:
         raise ValueError(f"{what} must be [..., vocab]")
     stride = vocab if t.is_contiguous() else _row_stride(t, what)
     return index, t.numel() // vocab, vocab, stride, kind
+
+
+# New tensors are made from a given one where that has the shape already: the call that takes a
+# shape, a type and a device takes twice as long, and a small call's time is its host time.
+def _new_rows(like, lead, logits):
+    """fp32 [lead], as `like` where that is so already."""
+    if like is not None and like.shape == lead:
+        return torch.empty_like(like)
+    return logits.new_empty(lead, dtype=torch.float32)
+
+
+def _workspace(workspace, need, like, index, what):
+    """The address and size of a workspace of at least `need` bytes; the tensor too, which has to
+    live until the call was made."""
+    if need == _BAD_SIZE:
+        raise EngramError(abi.ENGRAM_EINVAL, what)
+    if workspace is None:
+        workspace = like.new_empty((need + 15) // 4, dtype=torch.float32)
+        return workspace, workspace.data_ptr(), need
+    workspace = _bytes(workspace, need, like.device, index, what)
+    return workspace, workspace.data_ptr(), workspace.numel()
 
 
 # -------------------------------------------------------------- distillation --
@@ -123,14 +146,14 @@ def engram_distill(logits, ids, teacher, *, teacher_lse=None, rest=False, temper
     class more.  With grad_loss (fp32 [...], the loss' gradients; 0 where a row does not count)
     the gradient is written too, into grad, which may be logits."""
     index, rows, vocab, stride, kind = _logits(logits, "logits")
-    lead, device = logits.shape[:-1], logits.device
+    lead = logits.shape[:-1]
     top, teacher_kind, ids_p, teacher_p, tlse_p = _entries(logits, ids, teacher, teacher_lse,
                                                            rows, index)
     if rest and teacher_lse is None:
         raise ValueError("rest needs teacher_lse")
     if lse_rest is not None and not rest:
         raise ValueError("lse_rest needs rest")
-    weight_p = grad_p = grad_stride = rest_p = 0
+    weight_p = grad_p = grad_stride = rest_p = ws_p = 0
     if grad_loss is not None:
         weight_p = _per_row(grad_loss, lead, rows, "grad_loss", index)
         grad, grad_stride = _grad_of(logits, grad, index)
@@ -138,20 +161,24 @@ def engram_distill(logits, ids, teacher, *, teacher_lse=None, rest=False, temper
     elif grad is not None:
         raise ValueError("grad needs grad_loss")
     if loss is None:
-        loss = torch.empty(lead, dtype=torch.float32, device=device)
+        loss = _new_rows(grad_loss if grad_loss is not None else teacher_lse, lead, logits)
+        loss_p = loss.data_ptr()
+    else:
+        loss_p = _per_row(loss, lead, rows, "loss", index)
     if lse is None:
-        lse = torch.empty(lead, dtype=torch.float32, device=device)
-    loss_p = _per_row(loss, lead, rows, "loss", index)
-    lse_p = _per_row(lse, lead, rows, "lse", index)
+        lse = _new_rows(loss, lead, logits)
+        lse_p = lse.data_ptr()
+    else:
+        lse_p = _per_row(lse, lead, rows, "lse", index)
     if rest:
         if lse_rest is None:
-            lse_rest = torch.empty(lead, dtype=torch.float32, device=device)
+            lse_rest = _new_rows(loss, lead, logits)
         rest_p = _per_row(lse_rest, lead, rows, "lse_rest", index)
-    err_p = _optional(err_count, torch.int64, 1, "err_count", index)
-    ws_p, size = 0, _lib.engram_distill_workspace(rows, vocab, kind, int(bool(grad_p)))
+    err_p = 0 if err_count is None else _tensor(err_count, torch.int64, 1, "err_count", index)
+    size = _lib.engram_distill_workspace(rows, vocab, kind, 1 if grad_p else 0)
     if size:
-        workspace = _bytes(workspace, size, device, index, "engram_distill_workspace")
-        ws_p, size = workspace.data_ptr(), workspace.numel()
+        workspace, ws_p, size = _workspace(workspace, size, logits, index,
+                                           "engram_distill_workspace")
     _run(index, "engram_distill", _DISTILL.pack(
         rows, vocab, top, stride, grad_stride, temperature, kind, teacher_kind, int(bool(rest)),
         logits.data_ptr(), ids_p, teacher_p, tlse_p, weight_p, loss_p, lse_p, rest_p, grad_p,
@@ -212,37 +239,55 @@ def engram_beam_select(logits, scores, count=None, *, finished=None, eos=-1, out
     index, rows, vocab, stride, kind = _logits(logits, "logits")
     if not isinstance(scores, torch.Tensor) or scores.dim() != 2:
         raise ValueError("scores must be [batch, beams]")
-    batch, beams = scores.shape
+    batch, beams = lead = scores.shape
     if rows != batch * beams or logits.dim() not in (2, 3) or \
-            (logits.dim() == 3 and logits.shape[:2] != scores.shape):
+            (logits.dim() == 3 and logits.shape[:2] != lead):
         raise ValueError("logits must be [batch * beams, vocab] or [batch, beams, vocab]")
     count = beams if count is None else int(count)
     if not 1 <= count <= BEAM_MAX or not 1 <= beams <= BEAM_MAX:
         raise ValueError(f"beams and count must be 1 to {BEAM_MAX}")
     scores_p = _tensor(scores, torch.float32, rows, "scores", index)
-    finished_p = _optional(finished, torch.bool, rows, "finished", index)
-    if finished is not None and finished.shape != scores.shape:
-        _check_rows(finished, scores.shape, (), "finished")
-    device = logits.device
-
-    def output(t, dtype, what):
-        if t is None:
-            t = torch.empty((batch, count), dtype=dtype, device=device)
-        p = _tensor(t, dtype, batch * count, what, index)
-        if t.shape != (batch, count):
-            _check_rows(t, (batch, count), (), what)
-        return t, p
-
-    out_scores, os_p = output(out_scores, torch.float32, "out_scores")
-    parents, op_p = output(parents, torch.int64, "parents")
-    tokens, ot_p = output(tokens, torch.int64, "tokens")
-    out_finished, of_p = output(out_finished, torch.bool, "out_finished")
+    finished_p = 0
+    if finished is not None:
+        finished_p = _tensor(finished, torch.bool, rows, "finished", index)
+        if finished.shape != lead:
+            _check_rows(finished, lead, (), "finished")
+    shape = (batch, count)
+    if out_scores is None:
+        out_scores = torch.empty_like(scores) if count == beams else scores.new_empty(shape)
+        os_p = out_scores.data_ptr()
+    else:
+        os_p = _chosen(out_scores, torch.float32, shape, "out_scores", index)
+    if parents is None:
+        parents = torch.empty_like(out_scores, dtype=torch.int64)
+        op_p = parents.data_ptr()
+    else:
+        op_p = _chosen(parents, torch.int64, shape, "parents", index)
+    if tokens is None:
+        tokens = torch.empty_like(out_scores, dtype=torch.int64)
+        ot_p = tokens.data_ptr()
+    else:
+        ot_p = _chosen(tokens, torch.int64, shape, "tokens", index)
+    if out_finished is None:
+        out_finished = torch.empty_like(out_scores, dtype=torch.bool)
+        of_p = out_finished.data_ptr()
+    else:
+        of_p = _chosen(out_finished, torch.bool, shape, "out_finished", index)
     need = _lib.engram_beam_select_workspace(batch, beams, vocab)
-    workspace = _bytes(workspace, need, device, index, "engram_beam_select_workspace")
+    workspace, ws_p, size = _workspace(workspace, need, scores, index,
+                                       "engram_beam_select_workspace")
     _run(index, "engram_beam_select", logits.data_ptr(), kind, stride, scores_p, finished_p,
-         int(eos), batch, beams, vocab, count, os_p, op_p, ot_p, of_p, workspace.data_ptr(),
-         workspace.numel(), _stream_of(index))
+         int(eos), batch, beams, vocab, count, os_p, op_p, ot_p, of_p, ws_p, size,
+         _stream_of(index))
     return Beams(out_scores, parents, tokens, out_finished)
+
+
+def _chosen(t, dtype, shape, what, index):
+    """The address of an output [batch, count]."""
+    p = _tensor(t, dtype, shape[0] * shape[1], what, index)
+    if t.shape != shape:
+        _check_rows(t, shape, (), what)
+    return p
 
 
 def engram_beam_select_workspace(batch, beams, vocab) -> int:
@@ -250,6 +295,9 @@ def engram_beam_select_workspace(batch, beams, vocab) -> int:
     if need == _BAD_SIZE:
         raise EngramError(abi.ENGRAM_EINVAL, "engram_beam_select_workspace")
     return need
+
+
+_LISTS = [struct.Struct(f"={n}Q") for n in range(FORK_MAX_POOLS + 1)]  # 64-bit numbers
 
 
 class Fork(NamedTuple):
@@ -267,7 +315,7 @@ def engram_beam_fork(parents, pools=(), *, slots=None, tokens=None, history=None
     slots int64 [batch, beams] of the old beams (None: 0, 1, ...).  With tokens int64 [batch,
     beams] and history int64 [batch, beams, n] also each new beam's history: the last new_len
     (default n) of its parent's and its token."""
-    device, index = _device_of(parents, "parents")
+    _, index = _device_of(parents, "parents")
     if parents.dim() != 2:
         raise ValueError("parents must be [batch, beams]")
     batch, beams = parents.shape
@@ -279,22 +327,27 @@ def engram_beam_fork(parents, pools=(), *, slots=None, tokens=None, history=None
     pools = (pools,) if isinstance(pools, torch.Tensor) else tuple(pools)
     if len(pools) > FORK_MAX_POOLS:
         raise ValueError(f"at most {FORK_MAX_POOLS} pools")
-    count, addresses, sizes = 0, (ctypes.c_void_p * len(pools))(), \
-        (ctypes.c_int64 * len(pools))()
+    count, addresses, sizes = 0, [], []
     for i, pool in enumerate(pools):
         if not isinstance(pool, torch.Tensor) or pool.dim() < 1:
             raise TypeError("a pool must be a device (cuda) tensor [slot_count, ...]")
-        addresses[i] = _tensor(pool, pool.dtype, pool.numel(), "a pool", index)
-        if i and pool.shape[0] != count:
+        numel = pool.numel()
+        addresses.append(_tensor(pool, pool.dtype, numel, "a pool", index))
+        slots_here = pool.shape[0]
+        if i and slots_here != count:
             raise ValueError("pools must have the same number of slots")
-        count = pool.shape[0]
-        values = 1
-        for axis in pool.shape[1:]:
-            values *= axis
-        sizes[i] = values * pool.element_size()
+        count = slots_here
+        if slots_here:
+            sizes.append(numel // slots_here * pool.element_size())
+        else:
+            sizes.append(math.prod(pool.shape[1:]) * pool.element_size())
     if new_slots is None:
-        new_slots = torch.empty((batch, beams), dtype=torch.int64, device=device)
-    new_p = _tensor(new_slots, torch.int64, n, "new_slots", index)
+        new_slots = torch.empty_like(parents)
+        new_p = new_slots.data_ptr()
+    else:
+        new_p = _tensor(new_slots, torch.int64, n, "new_slots", index)
+        if new_slots.shape != parents.shape:
+            _check_rows(new_slots, parents.shape, (), "new_slots")
     tokens_p = history_p = out_p = have = 0
     if history is not None:
         if tokens is None:
@@ -310,12 +363,18 @@ def engram_beam_fork(parents, pools=(), *, slots=None, tokens=None, history=None
             _check_rows(tokens, parents.shape, (), "tokens")
         history_p = _tensor(history, torch.int64, n * have, "history", index)
         if new_history is None:
-            new_history = torch.empty((batch, beams, new_len), dtype=torch.int64, device=device)
-        out_p = _tensor(new_history, torch.int64, n * new_len, "new_history", index)
+            new_history = (torch.empty_like(history) if new_len == have
+                           else history.new_empty((batch, beams, new_len)))
+            out_p = new_history.data_ptr()
+        else:
+            out_p = _tensor(new_history, torch.int64, n * new_len, "new_history", index)
+            if new_history.shape != (batch, beams, new_len):
+                _check_rows(new_history, (batch, beams, new_len), (new_len,), "new_history")
     elif new_history is not None or new_len is not None:
         raise ValueError("new_history and new_len need history")
     err_p = _optional(err_count, torch.int64, 1, "err_count", index)
-    _run(index, "engram_beam_fork", parents_p, slots_p, batch, beams, addresses, sizes,
-         len(pools), count, new_p, tokens_p if history is not None else None, history_p, have,
+    lists = _LISTS[len(pools)]
+    _run(index, "engram_beam_fork", parents_p, slots_p, batch, beams, lists.pack(*addresses),
+         lists.pack(*sizes), len(pools), count, new_p, tokens_p if history is not None else None, history_p, have,
          out_p, new_len or 0, err_p, _stream_of(index))
     return Fork(new_slots, new_history)
