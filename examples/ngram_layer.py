@@ -1,6 +1,6 @@
 """The front of a model around the hashed n-gram lookup, trained and then served
 token by token, every step in the library's kernels (torch: the gate's small
-product, the weights' SGD, the loss).
+product, the vocabulary's, the weights' SGD, the loss of the first run).
 
     r    = sqrt(C) * E[tokens]                      engram_embed (a float stream)
     e    = table[hash(tokens)]                      engram_lookup
@@ -11,6 +11,11 @@ product, the weights' SGD, the loss).
 
 The backward reads the checkpoints, not x and y; it ends in both tables: the
 embedding's gradient by sorted tokens and the hashed rows' fused SignSGD step.
+
+    logits = next E^T, the embedding's rows again
+    loss and its gradient from a teacher's top logits     engram_distill
+    a beam search: the best continuations, then the       engram_beam_select
+    beams' rings and histories in their order             engram_beam_fork
 
     python examples/ngram_layer.py [--steps 20]
 """
@@ -25,6 +30,7 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 from gram_hashed_embedding_amd import engram as E  # noqa: E402
 from gram_hashed_embedding_amd import layer as L  # noqa: E402
+from gram_hashed_embedding_amd import vocab as V  # noqa: E402
 from gram_hashed_embedding_amd import workloads  # noqa: E402
 
 KERNEL = 4
@@ -104,15 +110,35 @@ class NgramLayer:
             self.master[name] -= lr * g
         self.cast()
 
+    # ---------------------------------------------------------- vocabulary --
+    def logits(self, hidden):
+        return hidden @ self.w["embed"].t()
+
+    def distill(self, tokens, ids, teacher, lr, table_lr, **kw):
+        """One step towards a teacher's top logits (ids, teacher [batch, seq, top]; further
+        arguments as engram_distill's): the mean loss."""
+        hidden, kept = self.forward(tokens)
+        weight = torch.full(tokens.shape, 1.0 / tokens.numel(), device=tokens.device)
+        logits = self.logits(hidden)
+        d = V.engram_distill(logits, ids, teacher, grad_loss=weight, grad=logits, **kw)
+        flat = d.grad.view(-1, d.grad.shape[-1])
+        # the product's two gradients: the layer's, and the rows' as the vocabulary's side
+        d_hidden = (flat @ self.w["embed"]).view_as(hidden)
+        d_rows = (flat.t().contiguous() @ hidden.view(-1, self.channels)).float()
+        self.backward(d_hidden, kept, lr, table_lr)
+        self.master["embed"] -= lr * d_rows
+        self.cast()
+        return d.loss.mean()
+
     # ------------------------------------------------------------- serving --
     def ring(self, sequences, device="cuda"):
         """An empty ring of the convolution's latest inputs for each sequence."""
         rows = (KERNEL - 1) * self.dilation
         return torch.empty((sequences, rows, self.channels), dtype=torch.bfloat16, device=device)
 
-    def step(self, history, position, ring):
+    def step(self, history, position, ring, slots=None):
         """next for one token a sequence: history int64 [batch, up to n] ends in it, position
-        int64 [batch] counts it from its sequence's start."""
+        int64 [batch] counts it from its sequence's start; slots: each sequence's ring."""
         batch, have = history.shape
         r = L.engram_embed(history[:, -1].contiguous(), self.w["embed"], self.scale,
                            out_dtype=torch.float32)
@@ -120,8 +146,34 @@ class NgramLayer:
         n = L.engram_residual_norm(e.view(batch, self.channels), w_next=self.w["w_in"],
                                    groups=self.heads)
         y = L.engram_ple_conv_step(n.next, ring, self.w["conv"], self.dilation, position,
-                                   bias=self.w["bias"])
+                                   slots=slots, bias=self.w["bias"])
         return self.combine(r, y)[1].next
+
+    def search(self, first, beams, steps, eos=-1):
+        """A beam search of `steps` tokens after each sequence's `first` (int64 [batch]): (tokens
+        [batch, beams, 1 + steps], scores [batch, beams], finished), the best first.  A beam
+        that nothing is left for has score -inf."""
+        batch, n = first.shape[0], self.wl.ngram_size
+        device = first.device
+        chosen = first[:, None, None].expand(batch, beams, 1).contiguous()
+        # the first step has one beam; the others' scores keep them out of the choice
+        scores = torch.full((batch, beams), -math.inf, device=device)
+        scores[:, 0] = 0.0
+        finished = torch.zeros((batch, beams), dtype=torch.bool, device=device)
+        ring, slots = self.ring(batch * beams, device), None
+        for t in range(steps):
+            have = min(n, t + 1)
+            # (a beam without tokens of its own, -1, steps on from token 0 and is not chosen)
+            recent = chosen[:, :, t + 1 - have:].clamp(min=0).view(batch * beams, have)
+            position = torch.full((batch * beams,), t, dtype=torch.int64, device=device)
+            hidden = self.step(recent.contiguous(), position, ring,
+                               None if slots is None else slots.view(-1))
+            b = V.engram_beam_select(self.logits(hidden), scores, finished=finished if eos >= 0
+                                     else None, eos=eos)
+            f = V.engram_beam_fork(b.parents, ring, slots=slots, tokens=b.tokens, history=chosen,
+                                   new_len=t + 2)
+            scores, finished, slots, chosen = b.scores, b.finished, f.slots, f.history
+        return chosen, scores, finished
 
 
 def main(argv=None):
@@ -151,6 +203,18 @@ def main(argv=None):
         one = net.step(history, position, ring)
         worst = max(worst, float((one.float() - whole[:, t].float()).abs().max()))
     print(f"{wl.seq} tokens one at a time: largest difference from the whole sequence {worst}")
+
+    # a teacher of the same shape, of which the best 16 logits at every position are known
+    teacher = NgramLayer(wl, vocab=1000, seed=1)
+    told = teacher.logits(teacher.forward(tokens)[0]).float()
+    top = torch.topk(told, 16, dim=-1)
+    for step in range(min(args.steps, 5)):
+        loss = net.distill(tokens, top.indices.contiguous(), top.values.contiguous(), args.lr,
+                           args.table_lr, teacher_lse=torch.logsumexp(told, -1), rest=True)
+        print(f"distillation step {step}: loss {float(loss):.4f}", flush=True)
+    found, scores, _ = net.search(tokens[:, 0].contiguous(), beams=4, steps=6)
+    for row, score in zip(found[0].tolist(), scores[0].tolist()):
+        print(f"beam {row}: {score:.3f}")
     return losses, worst
 
 

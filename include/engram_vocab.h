@@ -72,7 +72,10 @@ extern "C" {
  *   The workspace (engram_distill_workspace bytes, 16-byte aligned) is needed
  *   where that is not 0.
  * engram_distill_backward -- the gradient alone, from the d_lse (and, with
- *   rest, d_lse_rest) that engram_distill wrote; no workspace; d_loss is NULL.
+ *   rest, d_lse_rest) that engram_distill wrote: q = exp(z / temperature - lse),
+ *   q / s = exp(z / temperature - lse_rest).  (Where every logit of a sum is a
+ *   mask's lowest value, its fp32 logarithm does not hold that of their number,
+ *   and each such exponential is 1.)  No workspace; d_loss is NULL.
  * Errors: EINVAL, EWORKSPACE.  rows == 0 enqueues nothing.
  */
 typedef struct engram_distill_args {
