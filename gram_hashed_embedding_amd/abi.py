@@ -181,8 +181,8 @@ class EngramDistillArgs(ctypes.Structure):
     _fields_ = [
         ("rows", ctypes.c_int64), ("vocab", ctypes.c_int64), ("top", ctypes.c_int64),
         ("logits_stride", ctypes.c_int64), ("grad_stride", ctypes.c_int64),
-        ("temperature", ctypes.c_float), ("logits_type", ctypes.c_int32),
-        ("teacher_type", ctypes.c_int32), ("rest", ctypes.c_int32),
+        ("temperature", ctypes.c_double), ("logits_type", ctypes.c_int32),
+        ("teacher_type", ctypes.c_int32), ("rest", ctypes.c_int32), ("reserved", ctypes.c_int32),
         ("d_logits", _vp), ("d_ids", _vp), ("d_teacher", _vp), ("d_teacher_lse", _vp),
         ("d_grad_loss", _vp), ("d_loss", _vp), ("d_lse", _vp), ("d_lse_rest", _vp),
         ("d_grad", _vp), ("d_err_count", _vp), ("d_workspace", _vp),

@@ -394,7 +394,7 @@ int engram::launch_beam_select(const BeamCall &c, void *stream) {
   const ScanShape shape = beam_shape(rows, c.vocab);
   if (!grid_fits(rows * shape.segs, kScanThreads) || !grid_fits(c.batch, kChooseThreads))
     return ENGRAM_EINVAL;
-  const Scale log2e = scale_of(1.0f);
+  const Scale log2e = scale_of(1.0);
   const int64_t groups = ceil_div(c.vocab, kBeamGroup);
   const ScanArgs s = {c.logits, c.vocab, c.stride, shape.segs, shape.seg_len, groups, log2e,
                       c.scores, c.finished, c.parts, c.maxima};

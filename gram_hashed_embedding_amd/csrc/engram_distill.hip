@@ -21,7 +21,7 @@ namespace {
 
 struct DistillArgs {
   int64_t rows, vocab, top, stride, grad_stride, segs, seg_len;
-  float temperature;
+  double temperature;
   Scale c;  // log2(e) / temperature
   int teacher_type, rest;
   const void *logits;
@@ -41,9 +41,12 @@ struct Entries {
   int32_t *ids;   // -1: unused, or an earlier entry has the id
   float *z;       // the student's logit
   uint32_t *bits;
-  __device__ Entries(char *lds, int64_t top)
+  __device__ Entries(char *lds, int64_t top) : Entries(lds, lds, top) {}
+  // (the bits behind another row's entries)
+  __device__ Entries(char *lds, char *before, int64_t top)
       : p(reinterpret_cast<double *>(lds)), ids(reinterpret_cast<int32_t *>(p + top)),
-        z(reinterpret_cast<float *>(ids + top)), bits(reinterpret_cast<uint32_t *>(z + top)) {}
+        z(reinterpret_cast<float *>(ids + top)),
+        bits(reinterpret_cast<uint32_t *>(before + top * 16)) {}
 };
 constexpr size_t kEntryBytes = 16;
 
@@ -382,65 +385,233 @@ constexpr int64_t kDistillWideRows = 512;
 extern __shared__ __align__(16) char lds[];
 
 // Loss and gradient of rows that a block's registers hold.  As many blocks as stay on the
-// GPU together take the rows in turn: while a row's gradient is written chunk by chunk,
-// the next row's chunks are loaded into the registers that it leaves, so that loads,
-// stores and arithmetic go on side by side.  What a teacher's row gives is loaded before
-// the chunks (loads arrive in order) and worked on while they are on their way.
+// GPU together take the rows in turn.  All wavefronts but one hold the row: they sum it
+// (while its last chunks arrive), write its gradient chunk by chunk, and load the next
+// row's chunks into the registers that this leaves, so that loads, stores and arithmetic
+// go on side by side.  The last wavefront does what is not the vocabulary's: it reads the
+// next row's target while a gradient is written, and writes the named values and the loss
+// of the row before while one is summed.  Two barriers a row.
+//
+// One row of the CU's registers at a time, its 2 x 304 KB (151,936 bf16 values) against the
+// arithmetic of two exponentials a value: without the wavefront of its own, each row's
+// target, sums' joins and loss were waited for in turn (4096 rows: 610 us).
+struct RowInfo {
+  double m, r, named_sum;
+  float named_max, weight;
+  int none;
+};
+
+// Every lane's stores to LDS before, for the other lanes of its wavefront after.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// A wavefront's read_target() and sum_named() for a whole row.
+template <class T>
+__device__ __forceinline__ void prepare_row(const DistillArgs &a, int64_t row, Entries e,
+                                            RowInfo *info, int lane) {
+  const double T_ = a.temperature;
+  const int top = (int)a.top;
+  const int words = (int)((a.vocab + 31) / 32);
+  double most = -__builtin_inf();
+  int bad = 0;
+  bool used = false;
+  for (int j = lane; j < top; j += kWave) {
+    const int64_t id = a.ids[row * a.top + j];
+    const float y = a.teacher_type == ENGRAM_BF16
+                        ? bf16_lo(static_cast<const uint16_t *>(a.teacher)[row * a.top + j])
+                        : static_cast<const float *>(a.teacher)[row * a.top + j];
+    const bool ok = id >= 0 && id < a.vocab;
+    bad += !ok && id != -1;
+    used |= ok;
+    const double v = ok ? y / T_ : -__builtin_inf();
+    e.ids[j] = ok ? (int32_t)id : -1;
+    e.p[j] = v;
+    most = fmax(most, v);
+  }
+  for (int i = lane; i < words; i += kWave) e.bits[i] = 0u;
+  count_errors(bad, a.err);
+  wave_sync();
+  double ref;
+  if (a.teacher_lse != nullptr) {
+    ref = a.teacher_lse[row];
+  } else {
+    ref = uniform(wave_max(most));
+    if (ref == -__builtin_inf()) ref = 0.0;
+  }
+  const T *z = static_cast<const T *>(a.logits) + row * a.stride;
+  double sum = 0.0;
+  float max = kNegInf;
+  bool again = false;
+  for (int j = lane; j < top; j += kWave) {
+    const int32_t id = e.ids[j];
+    const float x = id >= 0 ? Chunk<T>::one(z[id]) : kNegInf;
+    const double p = id >= 0 ? exp64(e.p[j] - ref) : 0.0;
+    if (id >= 0) {
+      const uint32_t bit = 1u << (id & 31);
+      again |= (atomicOr(&e.bits[id >> 5], bit) & bit) != 0;
+    }
+    e.p[j] = p;
+    e.z[j] = x;
+    sum += p;
+    max = __builtin_fmaxf(max, x);
+  }
+  sum = uniform(wave_sum(sum));
+  double m = sum, r = 0.0;
+  bool none = __ballot(used) == 0;
+  if (a.teacher_lse == nullptr) {
+    none |= sum == 0.0;
+    if (sum != 0.0)
+      for (int j = lane; j < top; j += kWave) e.p[j] /= sum;
+    m = sum == 0.0 ? 0.0 : sum / sum;
+  } else if (a.rest) {
+    r = 1.0 - sum;
+    r = !none && r >= 0x1p-20 ? r : 0.0;
+  }
+  wave_sync();
+  if (__ballot(again) != 0) {
+    // (64 entries at a time: those before them are done, and the first of an id keeps it)
+    for (int c = 0; c < top; c += kWave) {
+      const int j = c + lane;
+      const int32_t id = j < top ? e.ids[j] : -1;
+      double total = 0.0;
+      bool first = true;
+      if (id >= 0)
+        for (int i = 0; i < top; ++i)
+          if (e.ids[i] == id) {
+            total += e.p[i];
+            first &= i >= j;
+          }
+      wave_sync();
+      if (id >= 0) {
+        if (first)
+          e.p[j] = total;
+        else
+          e.ids[j] = -1;
+      }
+      wave_sync();
+    }
+  }
+  max = uniform(wave_max(max));
+  double named = 0.0;
+  for (int j = lane; j < top; j += kWave)
+    if (e.ids[j] >= 0) named += exp64(((double)e.z[j] - (double)ref_of(max)) / T_);
+  named = wave_sum(named);
+  if (lane == 0)
+    *info = {m, r, named, max, a.grad_loss[row], none};
+}
+
+// A wavefront's write_named() and write_row().
+template <class T>
+__device__ __forceinline__ void finish_row(const DistillArgs &a, int64_t row, Entries e,
+                                           const RowInfo &info, const RowSum &rest,
+                                           const RowSum &all, int lane) {
+  const double T_ = a.temperature, none = -__builtin_inf();
+  const int top = (int)a.top;
+  const double lse = log_sum(all, T_);
+  T *grad = static_cast<T *>(a.grad) + row * a.grad_stride;
+  const bool counts = info.weight != 0.0f && info.none == 0;
+  const double gt = info.weight / T_;
+  double loss = 0.0;
+  for (int j = lane; j < top; j += kWave) {
+    const int32_t id = e.ids[j];
+    if (id < 0) continue;
+    const double p = e.p[j], z = e.z[j];
+    if (p != 0.0)  // (where no logit is finite every q is 0)
+      loss += p * (log64(p) - (lse == none ? none : z / T_ - lse));
+    if (counts) {
+      const double q =
+          all.sum == 0.0 ? 0.0 : exp64((z - (double)ref_of(all.max)) / T_) / all.sum;
+      store1(grad + id, (float)(gt * ((info.m + info.r) * q - p)));
+    }
+  }
+  loss = wave_sum(loss);
+  if (lane != 0) return;
+  const double lse_rest = a.rest ? log_sum(rest, T_) : 0.0;
+  if (a.lse != nullptr) a.lse[row] = (float)lse;
+  if (a.rest && a.lse_rest != nullptr) a.lse_rest[row] = (float)lse_rest;
+  if (a.loss != nullptr) {
+    if (info.r != 0.0)
+      loss += info.r * (log64(info.r) - (lse_rest == none ? none : lse_rest - lse));
+    a.loss[row] = info.none != 0 ? 0.0f : (float)loss;
+  }
+}
+
 template <class T, int THREADS>
 __global__ __launch_bounds__(THREADS, 4) void distill_hold_kernel(const DistillArgs a) {
-  constexpr int N = distill_held(sizeof(T), THREADS);
-  __shared__ double part[THREADS / kWave];
+  constexpr int kLast = THREADS / kWave - 1;
+  constexpr int N = distill_held(sizeof(T));
+  __shared__ RowInfo infos[2];
+  __shared__ double wave_sums[THREADS / kWave];
+  __shared__ float wave_maxima[THREADS / kWave];
   const int n = (int)a.vocab;
   const double T_ = a.temperature;
-  Entries e(lds, a.top);
-  int64_t row = blockIdx.x;
-  RawEntries<THREADS> raw;
-  raw.load(a, row, threadIdx.x);
-  Held<T, THREADS, N> held;
-  held.load(static_cast<const T *>(a.logits) + row * a.stride, n);
-  for (;;) {
-    const int thread = hidden_thread();
-    const float g = raw.weight;
-    const Target t = read_target<THREADS>(a, row, raw, 0, a.vocab, (n + 31) / 32, e, part, a.err,
-                                          thread);
-    Running run;
-    held.sum(hidden(n), a.c, e.bits, run);
-    const T *z = static_cast<const T *>(a.logits) + row * a.stride;
-    for (int j = thread; j < (int)a.top; j += THREADS)
-      e.z[j] = e.ids[j] >= 0 ? Chunk<T>::one(z[e.ids[j]]) : kNegInf;
+  // two rows' entries, and the bits of one behind them
+  char *other = lds + a.top * kEntryBytes;
+  const bool holds = uniform(threadIdx.x / kWave) != kLast;
+  Held<T, THREADS - kWave, N> held;
+  int64_t row = blockIdx.x, before = -1;
+  if (holds)
+    held.load(static_cast<const T *>(a.logits) + row * a.stride, n);
+  else
+    prepare_row<T>(a, row, Entries(lds, other, a.top), &infos[0], threadIdx.x % kWave);
+  if (threadIdx.x % kWave == 0 && !holds) {
+    wave_sums[kLast] = 0.0;
+    wave_maxima[kLast] = kNegInf;
+  }
+  __syncthreads();
+  RowSum rest = {kNegInf, 0.0}, all = rest;
+  for (int odd = 0;; odd ^= 1) {
+    const int thread = hidden_thread(), lane = thread % kWave;
+    const Entries e(odd ? other : lds, other, a.top), was(odd ? lds : other, other, a.top);
+    if (holds) {
+      Running run;
+      held.sum(hidden(n), a.c, e.bits, run);
+      const float m = wave_max(run.max);
+      const double s = wave_sum(moved(run.sum, run.max, ref_of(m), a.c));
+      if (lane == 0) {
+        wave_maxima[thread / kWave] = m;
+        wave_sums[thread / kWave] = s;
+      }
+    } else if (before >= 0) {
+      finish_row<T>(a, before, was, infos[odd ^ 1], rest, all, lane);
+    }
+    __syncthreads();
+    const RowInfo &info = infos[odd];
+    {
+      constexpr int kWaves = THREADS / kWave;
+      const float m1 = wave_maxima[lane % kWaves];
+      const float m = uniform(lanes_max_of<kWaves>(m1));
+      const double s = moved(wave_sums[lane % kWaves], m1, ref_of(m), a.c);
+      rest = {m, uniform(lanes_reduce<kWaves>(s, [](double x, double y) { return x + y; }))};
+    }
+    const Whole whole = both(rest, RowSum{info.named_max, info.named_sum}, T_);
+    all = whole.all;
     const bool more = row + gridDim.x < a.rows;
     const int64_t next = more ? row + gridDim.x : row;
-    raw.load(a, next, thread);
-    const RowSum rest = block_join<THREADS>(run, a.c, part, thread);
-    const RowSum named = sum_named<THREADS>(a, e, part, thread);
-    const Whole whole = both(rest, named, T_);
-    // (every lane has read its named logits, before the barriers of the sums)
-    T *grad = static_cast<T *>(a.grad) + row * a.grad_stride;
-    const T *coming = static_cast<const T *>(a.logits) + next * a.stride;
-    // (a row that does not count: zeros, whatever it holds)
-    const bool counts = g != 0.0f && !t.none;
-    if (!counts) held.clear();
-    const double gt = uniform(g / T_);
-    const float factor =
-        uniform(!counts || rest.sum == 0.0
-                    ? 0.0f
-                    : (float)(gt * ((t.m + t.r) * whole.s - t.r) / rest.sum));
-    held.template write<true>(grad, hidden(n), factor, counts ? ref_of(rest.max) : 0.0f, a.c, coming,
-                              more);
+    if (holds) {
+      // (a row that does not count: zeros, whatever it holds)
+      const bool counts = info.weight != 0.0f && info.none == 0;
+      if (!counts) held.clear();
+      const float factor =
+          uniform(!counts || rest.sum == 0.0
+                      ? 0.0f
+                      : (float)(info.weight / T_ * ((info.m + info.r) * whole.s - info.r) /
+                                rest.sum));
+      held.template write<true>(static_cast<T *>(a.grad) + row * a.grad_stride, hidden(n),
+                                factor, counts ? ref_of(rest.max) : 0.0f, a.c,
+                                static_cast<const T *>(a.logits) + next * a.stride, more);
+    } else if (more) {
+      prepare_row<T>(a, next, was, &infos[odd ^ 1], lane);
+    }
     __syncthreads();
-    if (counts)
-      write_named<T, THREADS>(
-          a, grad, 0, a.vocab, gt, e, t,
-          [&](float x) {
-            return whole.all.sum == 0.0
-                       ? 0.0
-                       : exp64(((double)x - (double)ref_of(whole.all.max)) / T_) / whole.all.sum;
-          },
-          thread);
-    write_row<THREADS>(a, row, rest, whole.all, e, t, part, thread);
-    if (!more) return;
+    before = row;
     row = next;
-    __syncthreads();  // (the entries are read until here)
+    if (!more) {
+      if (!holds) finish_row<T>(a, before, e, info, rest, all, lane);
+      return;
+    }
   }
 }
 
@@ -675,7 +846,7 @@ void enqueue_hold(const DistillArgs &a, hipStream_t stream) {
   const int64_t most = kComputeUnits * (1024 / THREADS);
   hipLaunchKernelGGL((distill_hold_kernel<T, THREADS>),
                      dim3((unsigned)(a.rows < most ? a.rows : most)), dim3(THREADS),
-                     lds_bytes(a.top, a.vocab), stream, a);
+                     lds_bytes(2 * a.top, a.vocab), stream, a);
 }
 
 template <class T, bool PARTS>

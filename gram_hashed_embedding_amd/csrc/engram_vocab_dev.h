@@ -75,8 +75,8 @@ __device__ __forceinline__ float ref_of(float max) { return max == kNegInf ? 0.0
 struct Scale {
   float hi, lo;
 };
-inline Scale scale_of(float temperature) {
-  const double c = 1.4426950408889634 / (double)temperature;
+inline Scale scale_of(double temperature) {
+  const double c = 1.4426950408889634 / temperature;
   float hi = (float)c;
   while ((double)hi >= c) hi = nextafterf(hi, 0.0f);
   return {hi, (float)(c - (double)hi)};

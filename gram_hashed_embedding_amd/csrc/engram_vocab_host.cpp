@@ -35,7 +35,8 @@ int check_distill(const engram_distill_args *a) {
   if (!mul_fits(a->rows, a->top * 8, INT64_MAX / 16)) return ENGRAM_EINVAL;
   if (!type_ok(a->logits_type) || !type_ok(a->teacher_type)) return ENGRAM_EINVAL;
   if (a->rest != 0 && a->rest != 1) return ENGRAM_EINVAL;
-  if (!(a->temperature >= 0x1p-64f && a->temperature <= 0x1p64f)) return ENGRAM_EINVAL;
+  if (!(a->temperature >= 0x1p-64 && a->temperature <= 0x1p64)) return ENGRAM_EINVAL;
+  if (a->reserved != 0) return ENGRAM_EINVAL;
   if (a->d_grad != nullptr && !rows_ok(a->rows, a->vocab, a->grad_stride)) return ENGRAM_EINVAL;
   if (a->d_grad != nullptr && a->d_grad == a->d_logits && a->grad_stride != a->logits_stride)
     return ENGRAM_EINVAL;

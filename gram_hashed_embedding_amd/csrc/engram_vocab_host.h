@@ -41,9 +41,7 @@ struct ScanPart {
 // Chunks of 8 values that a lane holds of a row, for values of `size` bytes (of the 128
 // registers that a lane has in blocks of 1024, or four blocks of 256, on a CU), and of a
 // segment in the backward pass.
-constexpr int distill_held(size_t size, int threads) {
-  return (threads >= 512 ? 20 : 16) * 2 / (int)size;
-}
+constexpr int distill_held(size_t size) { return size == 2 ? 20 : 10; }
 constexpr int distill_held_backward(size_t size) { return size == 2 ? 8 : 4; }
 // Rows are cut where a gradient is asked for and there are few of them, and where a row's
 // bits (one a value: whether a teacher's row names it) would take more than 32 KB of LDS.
@@ -57,7 +55,7 @@ inline ScanShape distill_shape(int64_t rows, int64_t vocab) {
 inline int distill_threads(int64_t rows, int64_t vocab, size_t size) {
   if (vocab < 8 || (rows <= kDistillFewRows && vocab >= kDistillFewVocab)) return 0;
   for (int threads = 256; threads <= 1024; threads *= 2)
-    if (vocab <= threads * 8 * distill_held(size, threads)) return threads;
+    if (vocab <= (threads - 64) * 8 * distill_held(size)) return threads;  // (one wavefront less)
   return 0;
 }
 // What a segment of a row leaves: its sums (of the values that the teacher does not name,

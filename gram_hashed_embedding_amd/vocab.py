@@ -88,7 +88,7 @@ class Distill(NamedTuple):
 
 
 # struct engram_distill_args, packed in one go
-_DISTILL = struct.Struct("=5qf3i" + 13 * "Q")
+_DISTILL = struct.Struct("=5qd4i" + 13 * "Q")
 assert _DISTILL.size == ctypes.sizeof(abi.EngramDistillArgs)
 
 
@@ -180,7 +180,7 @@ def engram_distill(logits, ids, teacher, *, teacher_lse=None, rest=False, temper
         workspace, ws_p, size = _workspace(workspace, size, logits, index,
                                            "engram_distill_workspace")
     _run(index, "engram_distill", _DISTILL.pack(
-        rows, vocab, top, stride, grad_stride, temperature, kind, teacher_kind, int(bool(rest)),
+        rows, vocab, top, stride, grad_stride, temperature, kind, teacher_kind, int(bool(rest)), 0,
         logits.data_ptr(), ids_p, teacher_p, tlse_p, weight_p, loss_p, lse_p, rest_p, grad_p,
         err_p, ws_p, size, _stream_of(index)))
     return Distill(loss, lse, lse_rest, grad)
@@ -207,7 +207,7 @@ def engram_distill_backward(grad_loss, logits, ids, teacher, lse, *, teacher_lse
     err_p = _optional(err_count, torch.int64, 1, "err_count", index)
     _run(index, "engram_distill_backward", _DISTILL.pack(
         rows, vocab, top, stride, grad_stride, temperature, kind, teacher_kind,
-        int(lse_rest is not None), logits.data_ptr(), ids_p, teacher_p, tlse_p, weight_p, 0,
+        int(lse_rest is not None), 0, logits.data_ptr(), ids_p, teacher_p, tlse_p, weight_p, 0,
         lse_p, rest_p, grad.data_ptr(), err_p, 0, 0, _stream_of(index)))
     return grad
 

@@ -81,8 +81,9 @@ extern "C" {
 typedef struct engram_distill_args {
   int64_t rows, vocab, top;
   int64_t logits_stride, grad_stride;
-  float temperature;
+  double temperature;
   int32_t logits_type, teacher_type, rest;
+  int32_t reserved; /* 0 */
   const void *d_logits;
   const int64_t *d_ids;
   const void *d_teacher;

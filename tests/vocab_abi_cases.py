@@ -27,7 +27,7 @@ SHARED = [
     dict(rows=-1), dict(vocab=0), dict(vocab=(1 << 30) + 1, logits_stride=1 << 31), dict(top=0),
     dict(top=abi.DISTILL_MAX_TOP + 1), dict(logits_stride=49), dict(grad_stride=49),
     dict(rows=1 << 58), dict(logits_type=2), dict(logits_type=-1), dict(teacher_type=2),
-    dict(rest=2), dict(rest=-1), dict(temperature=0.0), dict(temperature=-1.0),
+    dict(rest=2), dict(rest=-1), dict(reserved=1), dict(temperature=0.0), dict(temperature=-1.0),
     dict(temperature=float("nan")), dict(temperature=float("inf")), dict(temperature=2.0 ** -65),
     dict(temperature=2.0 ** 65), dict(d_logits=None), dict(d_ids=None), dict(d_teacher=None),
     dict(d_teacher_lse=None), dict(rest=0), dict(d_grad_loss=None),

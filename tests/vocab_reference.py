@@ -57,7 +57,6 @@ def distill(logits, ids, teacher, teacher_lse=None, rest=False, temperature=1.0,
     out = {k: torch.zeros(rows, dtype=f, device=dev)
            for k in ("loss", "lse", "lse_rest", "scale")}
     out["grad"], out["slack"] = (torch.zeros((rows, vocab), dtype=f, device=dev) for _ in range(2))
-    temperature = float(torch.tensor(temperature, dtype=torch.float32))
     for t in range(rows):
         z = logits[t].double() / temperature
         P, named, m, r, none = target(ids[t], teacher[t], vocab, temperature,
