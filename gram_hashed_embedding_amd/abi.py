@@ -195,7 +195,7 @@ def declare_vocab(lib):
     i64, i32, size = ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
     distill = _vp  # an EngramDistillArgs by reference, or its bytes
     for name, result, args in [
-        ("engram_distill_workspace", size, [i64, i64, i32, i32]),
+        ("engram_distill_workspace", size, [i64, i64, i32]),
         ("engram_distill", ctypes.c_int, [distill]),
         ("engram_distill_backward", ctypes.c_int, [distill]),
         ("engram_beam_select_workspace", size, [i64, i64, i64]),

@@ -39,7 +39,7 @@ __device__ __forceinline__ bool beam_live(const float *scores, const uint8_t *fi
 
 template <class T>
 __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(const ScanArgs a) {
-  __shared__ double part[kScanThreads / kWave];
+  __shared__ JoinLds<kScanThreads / kWave> join;
   __shared__ float most_of[kBeamMaxSeg / kBeamGroup];
   const int64_t row = blockIdx.x / a.segs, seg = blockIdx.x - row * a.segs;
   if (!beam_live(a.scores, a.finished, row)) return;
@@ -47,7 +47,7 @@ __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(const ScanArgs 
   const T *z = static_cast<const T *>(a.logits) + row * a.stride;
   constexpr int U = sizeof(T) == 2 ? 2 : 1;
   Running run;
-  each_chunks<T, kScanThreads, U>(z, lo, hi, [] {}, [&](int64_t at, float (&z)[U][8]) {
+  each_chunks<T, kScanThreads, U, true>(z, lo, hi, [] {}, [&](int64_t at, float (&z)[U][8]) {
     float m = run.max;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -61,7 +61,7 @@ __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(const ScanArgs 
 #pragma unroll
     for (int u = 0; u < U; ++u) run.add(z[u], ref, a.c);
   });
-  const RowSum s = block_join<kScanThreads>(run, a.c, part);  // (with a barrier)
+  const RowSum s = block_join(run, a.c, join);  // (with a barrier)
   float *maxima = a.maxima + row * a.groups + lo / kBeamGroup;
   for (int i = threadIdx.x; i < (int)((hi - lo + kBeamGroup - 1) / kBeamGroup);
        i += kScanThreads)

@@ -30,34 +30,51 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// Eight values from any address of their type: the loads are 16 bytes wide
-// (global memory takes them at any alignment).
+// Eight values at any address of their type: the loads and stores are 16 bytes wide
+// (global memory takes them at any alignment).  ONCE: not read again, or not soon, so that
+// the caches keep what is.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 template <class T>
 struct Chunk;
 template <>
 struct Chunk<uint16_t> {
   u32x4 r;
-  __device__ __forceinline__ void load(const uint16_t *p) { __builtin_memcpy(&r, p, 16); }
+  template <bool ONCE = false>
+  __device__ __forceinline__ void load(const uint16_t *p) {
+    const u32x4_any *q = reinterpret_cast<const u32x4_any *>(p);
+    r = ONCE ? __builtin_nontemporal_load(q) : *q;
+  }
   __device__ __forceinline__ void values(float (&z)[8]) const { unpack_bf16x8(r, z); }
   __device__ static __forceinline__ float one(uint16_t v) { return bf16_lo(v); }
-  // hides where the bits came from, so that nothing made of them is kept
-  __device__ __forceinline__ void renew() { asm volatile("" : "+v"(r)); }
-  __device__ __forceinline__ void clear() { r = u32x4{0u, 0u, 0u, 0u}; }
+  __device__ static __forceinline__ void store_one(uint16_t *p, float v) {
+    *p = (uint16_t)pack_bf16(v, 0.0f);
+  }
+  __device__ static __forceinline__ void store_once(uint16_t *p, const float (&v)[8]) {
+    const u32x4 w = pack_bf16x8(v);
+    __builtin_nontemporal_store(w, reinterpret_cast<u32x4_any *>(p));
+  }
 };
 template <>
 struct Chunk<float> {
   f32x4 a, b;
+  template <bool ONCE = false>
   __device__ __forceinline__ void load(const float *p) {
-    __builtin_memcpy(&a, p, 16);
-    __builtin_memcpy(&b, p + 4, 16);
+    const f32x4_any *q = reinterpret_cast<const f32x4_any *>(p);
+    a = ONCE ? __builtin_nontemporal_load(q) : *q;
+    b = ONCE ? __builtin_nontemporal_load(q + 1) : q[1];
   }
   __device__ __forceinline__ void values(float (&z)[8]) const {
     z[0] = a.x; z[1] = a.y; z[2] = a.z; z[3] = a.w;
     z[4] = b.x; z[5] = b.y; z[6] = b.z; z[7] = b.w;
   }
   __device__ static __forceinline__ float one(float v) { return v; }
-  __device__ __forceinline__ void renew() { asm volatile("" : "+v"(a), "+v"(b)); }
-  __device__ __forceinline__ void clear() { a = b = f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
+  __device__ static __forceinline__ void store_one(float *p, float v) { *p = v; }
+  __device__ static __forceinline__ void store_once(float *p, const float (&v)[8]) {
+    f32x4_any *q = reinterpret_cast<f32x4_any *>(p);
+    __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, q);
+    __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, q + 1);
+  }
 };
 
 __device__ __forceinline__ float max8(float m, const float (&z)[8]) {
@@ -102,27 +119,20 @@ struct Running {
   }
 };
 
-// A constant made in scalar registers where it is used (as a literal the compiler keeps it
-// in vector registers throughout a loop around it).
-__device__ __forceinline__ double scalar(double v) {
-  asm volatile("" : "+s"(v));
-  return v;
-}
-
 // exp in fp64 by its series around 0 (|r| <= ln(2) / 2: the 11th power's term is
 // 2e-13), in few registers.
 __device__ __forceinline__ double exp64(double x) {
   x = x < -800.0 ? -800.0 : x;  // (0; a NaN stays one)
-  const double n = rint(x * scalar(1.44269504088896340736));
-  const double r = fma(-n, scalar(0.693147180559945309417), x);
-  double p = scalar(1.0 / 3628800.0);
-  p = fma(p, r, scalar(1.0 / 362880.0));
-  p = fma(p, r, scalar(1.0 / 40320.0));
-  p = fma(p, r, scalar(1.0 / 5040.0));
-  p = fma(p, r, scalar(1.0 / 720.0));
-  p = fma(p, r, scalar(1.0 / 120.0));
-  p = fma(p, r, scalar(1.0 / 24.0));
-  p = fma(p, r, scalar(1.0 / 6.0));
+  const double n = rint(x * 1.44269504088896340736);
+  const double r = fma(-n, 0.693147180559945309417, x);
+  double p = 1.0 / 3628800.0;
+  p = fma(p, r, 1.0 / 362880.0);
+  p = fma(p, r, 1.0 / 40320.0);
+  p = fma(p, r, 1.0 / 5040.0);
+  p = fma(p, r, 1.0 / 720.0);
+  p = fma(p, r, 1.0 / 120.0);
+  p = fma(p, r, 1.0 / 24.0);
+  p = fma(p, r, 1.0 / 6.0);
   p = fma(p, r, 0.5);
   p = fma(p, r, 1.0);
   p = fma(p, r, 1.0);
@@ -139,7 +149,7 @@ __device__ __forceinline__ double log64(double x) {
   const double m = frexp(x, &e);
   const double y = (double)(__builtin_amdgcn_logf((float)m) * 0.693147182464599609375f);
   const double d = fma(m, exp64(-y), -1.0);
-  return fma((double)e, scalar(0.693147180559945309417), y + (d - 0.5 * d * d));
+  return fma((double)e, 0.693147180559945309417, y + (d - 0.5 * d * d));
 }
 
 // ----------------------------------------------- reductions over wavefronts --
@@ -191,20 +201,6 @@ __device__ __forceinline__ double wave_max(double v) {
   return lanes_reduce<kWave>(v, [](double a, double b) { return fmax(a, b); });
 }
 
-// The thread's number, hidden from the compiler: what is made of it inside a loop is made
-// there, not kept in registers from before it.
-__device__ __forceinline__ int hidden_thread() {
-  int t = threadIdx.x;
-  asm volatile("" : "+v"(t));
-  return t;
-}
-
-// The same for a number that every lane has alike.
-__device__ __forceinline__ int hidden(int n) {
-  asm volatile("" : "+s"(n));
-  return n;
-}
-
 // A value that every lane has alike, in scalar registers.
 __device__ __forceinline__ uint32_t uniform(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
@@ -216,41 +212,10 @@ __device__ __forceinline__ double uniform(double v) {
   return double_of(uniform(low_of(v)), uniform(high_of(v)));
 }
 
-// Over a block, in the same order for every row; `part` holds a slot a wavefront, which
-// each wavefront's lanes read one to a lane.
-template <int THREADS, class V>
-__device__ __forceinline__ V wave_of(const V *part, int t) {
-  return part[t % (THREADS / kWave)];
-}
-template <int THREADS>
-__device__ __forceinline__ double block_sum(double v, double *part,
-                                            int t = threadIdx.x) {
-  v = wave_sum(v);
-  if (t % kWave == 0) part[t / kWave] = v;
-  __syncthreads();
-  v = wave_of<THREADS>(part, t);
-  __syncthreads();
-  return uniform(lanes_reduce<THREADS / kWave>(v, [](double a, double b) { return a + b; }));
-}
-template <int THREADS>
-__device__ __forceinline__ double block_max(double v, double *part,
-                                            int t = threadIdx.x) {
-  v = wave_max(v);
-  if (t % kWave == 0) part[t / kWave] = v;
-  __syncthreads();
-  v = wave_of<THREADS>(part, t);
-  __syncthreads();
-  return uniform(lanes_reduce<THREADS / kWave>(v, [](double a, double b) { return fmax(a, b); }));
-}
-template <int THREADS>
-__device__ __forceinline__ float block_max(float v, float *part,
-                                            int t = threadIdx.x) {
-  v = wave_max(v);
-  if (t % kWave == 0) part[t / kWave] = v;
-  __syncthreads();
-  v = wave_of<THREADS>(part, t);
-  __syncthreads();
-  return uniform(lanes_max_of<THREADS / kWave>(v));
+// Every lane's stores to LDS before, for the other lanes of its wavefront after.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
 // A sum of exponentials with its maximum: of exp((z - max) / temperature).
@@ -262,12 +227,27 @@ struct RowSum {
 __device__ __forceinline__ double moved(double s, float max, float ref, Scale c) {
   return max == kNegInf ? s : s * (double)exp_scaled(max - ref, c);
 }
-// The lanes' running sums over a block.
-template <int THREADS>
-__device__ __forceinline__ RowSum block_join(const Running &run, Scale c, double *part,
-                                             int t = threadIdx.x) {
-  const float m = block_max<THREADS>(run.max, reinterpret_cast<float *>(part), t);
-  return {m, block_sum<THREADS>(moved(run.sum, run.max, ref_of(m), c), part, t)};
+// The lanes' running sums over a block of WAVES wavefronts, in the same order for every
+// row: one barrier, after which every wavefront joins the others' for itself.
+template <int WAVES>
+struct JoinLds {
+  float max[WAVES];
+  double sum[WAVES];
+};
+template <int WAVES>
+__device__ __forceinline__ RowSum block_join(const Running &run, Scale c, JoinLds<WAVES> &l) {
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const float own = wave_max(run.max);
+  const double part = wave_sum(moved(run.sum, run.max, ref_of(own), c));
+  if (lane == 0) {
+    l.max[wave] = own;
+    l.sum[wave] = part;
+  }
+  __syncthreads();
+  const float other = l.max[lane % WAVES];
+  const float m = uniform(lanes_max_of<WAVES>(other));
+  const double s = moved(l.sum[lane % WAVES], other, ref_of(m), c);
+  return {m, uniform(lanes_reduce<WAVES>(s, [](double a, double b) { return a + b; }))};
 }
 // The sums of a row's segments, joined by a wavefront.
 __device__ __forceinline__ RowSum wave_join(const ScanPart *parts, int64_t n, Scale c) {
@@ -289,7 +269,7 @@ __device__ __forceinline__ double log_sum(const RowSum &v, double temperature) {
 // called by every lane with the chunks that start at at + 8 * (u * THREADS + lane);
 // values past hi are -inf.  The next chunks' loads are on their way meanwhile; first() is
 // called once, behind the first ones.
-template <class T, int THREADS, int U, class FIRST, class USE>
+template <class T, int THREADS, int U, bool ONCE, class FIRST, class USE>
 __device__ __forceinline__ void each_chunks(const T *row, int64_t lo, int64_t hi, FIRST first,
                                             USE use) {
   constexpr int kTile = 8 * THREADS, kStep = U * kTile;
@@ -299,13 +279,13 @@ __device__ __forceinline__ void each_chunks(const T *row, int64_t lo, int64_t hi
   if (at <= last) {
     Chunk<T> r[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) r[u].load(row + at + u * kTile + 8 * t);
+    for (int u = 0; u < U; ++u) r[u].template load<ONCE>(row + at + u * kTile + 8 * t);
     first();
     for (; at < last; at += kStep) {
       float z[U][8];
       Chunk<T> n[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) n[u].load(row + at + kStep + u * kTile + 8 * t);
+      for (int u = 0; u < U; ++u) n[u].template load<ONCE>(row + at + kStep + u * kTile + 8 * t);
 #pragma unroll
       for (int u = 0; u < U; ++u) r[u].values(z[u]);
       use(at, z);
@@ -327,7 +307,7 @@ __device__ __forceinline__ void each_chunks(const T *row, int64_t lo, int64_t hi
       const int64_t i = at + u * kTile + 8 * t;
       if (i + 8 <= hi) {
         Chunk<T> r;
-        r.load(row + i);
+        r.template load<ONCE>(row + i);
         r.values(z[u]);
       } else {
 #pragma unroll

@@ -19,11 +19,9 @@ bool rows_ok(int64_t rows, int64_t vocab, int64_t stride) {
 }  // namespace
 
 // ------------------------------------------------------------ distillation --
-extern "C" size_t engram_distill_workspace(int64_t rows, int64_t vocab,
-                                          int32_t logits_type, int32_t grad) {
-  if (!rows_ok(rows, vocab, vocab) || !type_ok(logits_type) || grad < 0 || grad > 1)
-    return (size_t)-1;
-  return distill_workspace(rows, vocab, logits_type, grad != 0);
+extern "C" size_t engram_distill_workspace(int64_t rows, int64_t vocab, int32_t grad) {
+  if (!rows_ok(rows, vocab, vocab) || grad < 0 || grad > 1) return (size_t)-1;
+  return distill_workspace(rows, vocab, grad != 0);
 }
 
 namespace {
@@ -57,7 +55,7 @@ extern "C" int engram_distill(const engram_distill_args *a) {
   if (a->d_loss == nullptr && a->d_lse == nullptr && a->d_lse_rest == nullptr &&
       a->d_grad == nullptr)
     return ENGRAM_EINVAL;
-  const size_t need = distill_workspace(a->rows, a->vocab, a->logits_type, a->d_grad != nullptr);
+  const size_t need = distill_workspace(a->rows, a->vocab, a->d_grad != nullptr);
   if (need > 0 && (a->d_workspace == nullptr || !aligned16(a->d_workspace) ||
                    a->workspace_bytes < need))
     return ENGRAM_EWORKSPACE;

@@ -38,37 +38,30 @@ struct ScanPart {
 };
 
 // ------------------------------------------------------------ distillation --
-// Chunks of 8 values that a lane holds of a row, for values of `size` bytes (of the 128
-// registers that a lane has in blocks of 1024, or four blocks of 256, on a CU), and of a
-// segment in the backward pass.
-constexpr int distill_held(size_t size) { return size == 2 ? 20 : 10; }
+// Chunks of 8 values that a lane of the backward pass holds.
 constexpr int distill_held_backward(size_t size) { return size == 2 ? 8 : 4; }
-// Rows are cut where a gradient is asked for and there are few of them, and where a row's
-// bits (one a value: whether a teacher's row names it) would take more than 32 KB of LDS.
+// A block takes a whole row, but for a few long rows with a gradient, which would leave CUs
+// idle, and where a row's bits (one a value: whether a teacher's row names it) would take
+// more than 32 KB of LDS: those are cut.
 constexpr int64_t kDistillMaxSeg = int64_t(1) << 18;
 constexpr int64_t kDistillBlocks = 1024;
 constexpr int64_t kDistillFewRows = 128, kDistillFewVocab = 65536;
 inline ScanShape distill_shape(int64_t rows, int64_t vocab) {
   return scan_shape(rows, vocab, kDistillBlocks, kDistillMaxSeg);
 }
-// The threads of a block that holds a whole row for its gradient; 0 where none does.
-inline int distill_threads(int64_t rows, int64_t vocab, size_t size) {
-  if (vocab < 8 || (rows <= kDistillFewRows && vocab >= kDistillFewVocab)) return 0;
-  for (int threads = 256; threads <= 1024; threads *= 2)
-    if (vocab <= (threads - 64) * 8 * distill_held(size)) return threads;  // (one wavefront less)
-  return 0;
+inline bool distill_cut(int64_t rows, int64_t vocab, bool grad) {
+  return vocab > kDistillMaxSeg || (grad && rows <= kDistillFewRows && vocab >= kDistillFewVocab);
 }
 // What a segment of a row leaves: its sums (of the values that the teacher does not name,
-// and of those it does) beside their maxima, and its part of the loss.
+// and of those it does) beside their maxima, its part of the loss, and the probability
+// that this part is over.
 struct DistillPart {
-  double rest_sum, named_sum, loss;
+  double rest_sum, named_sum, loss, mass;
   float rest_max, named_max;
 };
 // The parts of every segment; nothing where a block takes a row.
-inline size_t distill_workspace(int64_t rows, int64_t vocab, int32_t type, bool grad) {
-  const bool cut = grad ? distill_threads(rows, vocab, type == ENGRAM_BF16 ? 2 : 4) == 0
-                        : vocab > kDistillMaxSeg;
-  if (rows == 0 || !cut) return 0;
+inline size_t distill_workspace(int64_t rows, int64_t vocab, bool grad) {
+  if (rows == 0 || !distill_cut(rows, vocab, grad)) return 0;
   return (size_t)rows * (size_t)distill_shape(rows, vocab).segs * sizeof(DistillPart);
 }
 

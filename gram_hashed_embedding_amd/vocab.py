@@ -175,7 +175,7 @@ def engram_distill(logits, ids, teacher, *, teacher_lse=None, rest=False, temper
             lse_rest = _new_rows(loss, lead, logits)
         rest_p = _per_row(lse_rest, lead, rows, "lse_rest", index)
     err_p = 0 if err_count is None else _tensor(err_count, torch.int64, 1, "err_count", index)
-    size = _lib.engram_distill_workspace(rows, vocab, kind, 1 if grad_p else 0)
+    size = _lib.engram_distill_workspace(rows, vocab, 1 if grad_p else 0)
     if size:
         workspace, ws_p, size = _workspace(workspace, size, logits, index,
                                            "engram_distill_workspace")
@@ -212,8 +212,8 @@ def engram_distill_backward(grad_loss, logits, ids, teacher, lse, *, teacher_lse
     return grad
 
 
-def engram_distill_workspace(rows, vocab, dtype=torch.bfloat16, grad=False) -> int:
-    need = _lib.engram_distill_workspace(rows, vocab, _TYPES[dtype], int(bool(grad)))
+def engram_distill_workspace(rows, vocab, grad=False) -> int:
+    need = _lib.engram_distill_workspace(rows, vocab, int(bool(grad)))
     if need == _BAD_SIZE:
         raise EngramError(abi.ENGRAM_EINVAL, "engram_distill_workspace")
     return need

@@ -101,8 +101,7 @@ typedef struct engram_distill_args {
 
 /* Bytes of workspace of engram_distill, grad 1 with d_grad and 0 without; (size_t)-1 for
  * sizes it refuses. */
-size_t engram_distill_workspace(int64_t rows, int64_t vocab, int32_t logits_type,
-                                int32_t grad);
+size_t engram_distill_workspace(int64_t rows, int64_t vocab, int32_t grad);
 int engram_distill(const engram_distill_args *args);
 int engram_distill_backward(const engram_distill_args *args);
 

@@ -119,7 +119,7 @@ def test_two_streams_at_once():
 def test_captured_and_replayed(vocab):
     """Two graphs that share a workspace, replayed in turn with new inputs, eager calls and
     synchronizations between."""
-    need = max(V.engram_distill_workspace(12, vocab, BF, grad=True),
+    need = max(V.engram_distill_workspace(12, vocab, grad=True),
                V.engram_beam_select_workspace(3, 4, vocab), 16)
     ws = torch.empty(need, dtype=torch.uint8, device="cuda")
     sets = [make(5, vocab), make(6, vocab)]

@@ -66,7 +66,7 @@ for rows in (1, 3, 127, 129, 5000):
               1 << 30):
         for grad in (0, 1):
             for kind in (abi.BF16, abi.F32):
-                need = lib.engram_distill_workspace(rows, n, kind, grad)
+                need = lib.engram_distill_workspace(rows, n, grad)
                 more = dict(d_grad=V.B, d_grad_loss=V.A) if grad else \
                     dict(d_grad=None, d_grad_loss=None)
                 assert V.distill(lib.engram_distill, rows=rows, vocab=n, logits_stride=n,

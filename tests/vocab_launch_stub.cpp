@@ -17,7 +17,7 @@ void require(bool ok) {
 int launch_distill(const engram_distill_args &a) {
   require(a.rows > 0 && a.vocab > 0 && a.d_logits && a.d_ids && a.d_teacher);
   require((a.d_grad != nullptr) == (a.d_grad_loss != nullptr));
-  const size_t need = distill_workspace(a.rows, a.vocab, a.logits_type, a.d_grad != nullptr);
+  const size_t need = distill_workspace(a.rows, a.vocab, a.d_grad != nullptr);
   require(need == 0 || (a.d_workspace && a.workspace_bytes >= need));
   const ScanShape s = distill_shape(a.rows, a.vocab);
   require(s.segs * s.seg_len >= a.vocab && (s.segs - 1) * s.seg_len < a.vocab);
