@@ -54,10 +54,14 @@ extern "C" {
  * hold.  A logit of -inf has q = 0 (a row of them: lse -inf, q 0); a target
  * with q = 0 gives a loss of +inf and a finite gradient.  NaN and +inf logits
  * make their own row's loss NaN, and its gradient where it is not 0.
- * Sums over the vocabulary: fp32 terms, summed in fp32 by each lane (at most
- * a few hundred terms) and in fp64 across lanes, in a fixed order; the
- * teacher's part in fp64.  The gradient is rounded once to the logits' type.
- *   rows, vocab (1 to 2^30), top (1 to ENGRAM_DISTILL_MAX_TOP).
+ * Sums over the vocabulary: fp32 terms, summed in fp32 by each lane (128
+ * chunks of 8 at most) and in fp64 across lanes, in a fixed order: two calls
+ * give the same bits.  The named logits' part, the teacher's and the logarithms
+ * are fp64; a term of less than 2^-126 of the largest is lost.  The gradient is
+ * rounded once to the logits' type.
+ *   rows (up to 4,194,303, and rows * ceil(vocab / 16384) for a gradient up to
+ *     16,777,215, / 8192 for fp32: a launch's threads), vocab (1 to 2^30), top
+ *     (1 to ENGRAM_DISTILL_MAX_TOP).
  *   d_logits of logits_type, rows logits_stride values apart.
  *   d_ids int64 [rows, top]: -1 marks an unused entry; other ids outside
  *     [0, vocab) are treated the same and add one each to *d_err_count (when
