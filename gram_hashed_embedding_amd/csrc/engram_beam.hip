@@ -5,11 +5,12 @@
 //
 // Selection.  One pass over the logits (beam_scan_kernel) leaves each segment's
 // sum of exponentials and the largest logit of every kBeamGroup adjacent
-// values.  The `count` best candidates lie in the `count` best groups (by their
-// largest value, equal ones by place: the candidate before which `count` others
-// come cannot be one of the first `count`), so beam_choose_kernel, a block to a
-// sequence, finds those among 1/128 of the values, reads them again and takes
-// the best of `count` times 128 candidates.  Both choices are exact in fp64.
+// values, counted from the first whole cache line; those before it are a row's
+// group 0, which may be empty.  The `count` best candidates lie in the `count`
+// best groups (by their largest value, equal ones by place: the candidate before
+// which `count` others come cannot be one of the first `count`), so
+// beam_choose_kernel, a block to a sequence, finds those among 1/128 of the
+// values, reads them again and takes the best of `count` times 128 candidates.  Both choices are exact in fp64.
 //
 // Reordering.  A new beam that is the first child of its parent keeps the
 // parent's slot; only the others' states are copied, into slots of beams that
@@ -37,16 +38,32 @@ __device__ __forceinline__ bool beam_live(const float *scores, const uint8_t *fi
   return __builtin_isfinite(scores[row]) && (finished == nullptr || finished[row] == 0);
 }
 
+// A block to a segment of a beam's logits.  Memory bounds it: 512 beams of 151,936 bf16 values
+// are read in 28 us (5.5 TB/s); 4 chunks a lane and step instead of 2 are no faster.  The
+// groups' maxima wait in LDS and are written 4 bytes a lane next to each other at the end,
+// not by every 16th lane in between.  Groups begin at whole cache lines: 4096 beams of 50,257
+// bf16 values take 97 us for a selection, 108 if they begin with the row.  One beam or a few: 4 to 6 us, a block's own latency.
 template <class T>
 __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(const ScanArgs a) {
   __shared__ JoinLds<kScanThreads / kWave> join;
-  __shared__ float most_of[kBeamMaxSeg / kBeamGroup];
+  __shared__ float most_of[kBeamMaxSeg / kBeamGroup];  // but of group 0
   const int64_t row = blockIdx.x / a.segs, seg = blockIdx.x - row * a.segs;
   if (!beam_live(a.scores, a.finished, row)) return;
-  const int64_t lo = seg * a.seg_len, hi = lo + a.seg_len < a.vocab ? lo + a.seg_len : a.vocab;
   const T *z = static_cast<const T *>(a.logits) + row * a.stride;
+  const int lead = lead_of(z, a.vocab);
+  int64_t lo = lead + seg * a.seg_len, hi = lo + a.seg_len;
+  lo = lo < a.vocab ? lo : a.vocab;
+  hi = hi < a.vocab ? hi : a.vocab;
+  float *maxima = a.maxima + row * a.groups;
   constexpr int U = sizeof(T) == 2 ? 2 : 1;
   Running run;
+  if (seg == 0 && threadIdx.x < kWave) {
+    const float one = (int)threadIdx.x < lead ? Chunk<T>::one(z[threadIdx.x]) : kNegInf;
+    const float ref = run.raise(one, a.c);
+    run.sum = exp_scaled(one - ref, a.c);
+    const float most = wave_max(one);
+    if (threadIdx.x == 0) maxima[0] = most;
+  }
   each_chunks<T, kScanThreads, U, true>(z, lo, hi, [] {}, [&](int64_t at, float (&z)[U][8]) {
     float m = run.max;
 #pragma unroll
@@ -62,10 +79,11 @@ __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(const ScanArgs 
     for (int u = 0; u < U; ++u) run.add(z[u], ref, a.c);
   });
   const RowSum s = block_join(run, a.c, join);  // (with a barrier)
-  float *maxima = a.maxima + row * a.groups + lo / kBeamGroup;
-  for (int i = threadIdx.x; i < (int)((hi - lo + kBeamGroup - 1) / kBeamGroup);
-       i += kScanThreads)
-    maxima[i] = most_of[i];
+  // (the last group may lie behind the row)
+  const int64_t first = 1 + seg * (a.seg_len / kBeamGroup), behind = a.groups - first;
+  const int n = (int)(behind < a.seg_len / kBeamGroup ? behind : a.seg_len / kBeamGroup);
+  for (int i = threadIdx.x; i < n; i += kScanThreads)
+    maxima[first + i] = i * kBeamGroup < hi - lo ? most_of[i] : kNegInf;
   if (threadIdx.x == 0) a.parts[row * a.segs + seg] = {s.sum, s.max, 0u};
 }
 
@@ -212,12 +230,19 @@ struct ChooseArgs {
   Scale log2e;
 };
 
+// A block to a sequence.  Its bytes are few (8 beams of 151,936 values: 38 KB of maxima and 24
+// KB of groups read again): it is a chain of loads, barriers and ballots, 9.4 us for one beam
+// and 13.8 for 64 sequences of 8, so it runs once whatever the batch.  What shortened it: the
+// loads of a pass all sent before the first is used and behind the beams' sums, no division
+// of 64 bits, and the first choice's groups left unordered (21 to 23 us -> 14).  Of 512
+// threads, tried before that, a whole selection took 56 us where it took 50 of 1024.
 template <class T>
 __global__ __launch_bounds__(kChooseThreads) void beam_choose_kernel(const ChooseArgs a) {
   __shared__ ChooseLds l;
   __shared__ double lse[ENGRAM_BEAM_MAX];    // NaN: no candidate but a finished beam's
   __shared__ double score[ENGRAM_BEAM_MAX];
   __shared__ int64_t group_at[kChooseGroups];  // of each chosen group: its first value
+  __shared__ int64_t group_end[kChooseGroups];  // what it ends before
   __shared__ int group_beam[kChooseGroups];
   const BeamCall &c = a.c;
   const int64_t b = blockIdx.x, first_row = b * c.beams;
@@ -271,8 +296,12 @@ __global__ __launch_bounds__(kChooseThreads) void beam_choose_kernel(const Choos
   }
   if (t < chosen) {
     const int at = (int)(ranked ? l.best[t].at : l.list[t].at), w = beam_of(at);
+    const int g = at - w * groups;
+    const T *z = static_cast<const T *>(c.logits) + (first_row + w) * c.stride;
+    const int lead = lead_of(z, c.vocab);
     group_beam[t] = w;
-    group_at[t] = (int64_t)(at - w * groups) * kBeamGroup;
+    group_at[t] = g == 0 ? 0 : lead + (g - 1) * kBeamGroup;
+    group_end[t] = g == 0 ? lead : c.vocab;
   }
   __syncthreads();
   const int listed = list_best(
@@ -281,7 +310,7 @@ __global__ __launch_bounds__(kChooseThreads) void beam_choose_kernel(const Choos
         const int w = group_beam[i / kBeamGroup];
         const int64_t v = group_at[i / kBeamGroup] + i % kBeamGroup;
         const T *z = static_cast<const T *>(c.logits) + (first_row + w) * c.stride;
-        return v < c.vocab ? Chunk<T>::one(z[v]) : kNegInf;
+        return v < group_end[i / kBeamGroup] ? Chunk<T>::one(z[v]) : kNegInf;
       },
       [&](int i, float z) {
         const int w = group_beam[i / kBeamGroup];
@@ -313,7 +342,10 @@ constexpr int kForkSteps = 4;
 constexpr int64_t kForkChunk = (int64_t)kForkThreads * kForkSteps * 16;  // bytes a block copies
 
 // Blocks: `chunks` of every new beam (the pools' slots one after another); the first
-// of them also writes the beam's slot and history.
+// of them also writes the beam's slot and history.  A block copies 16 KB, 4 loads of 16
+// bytes in flight a lane.  64 x 8 beams with slots of 192 KB, of which about a third are
+// copied: 14.6 us, 4.8 TB/s (70 MB in all, too few for more); a few beams 4.2 us, a launch's
+// latency.
 __global__ __launch_bounds__(kForkThreads) void beam_fork_kernel(const ForkCall c,
                                                                  const int64_t chunks) {
   const int64_t entry = blockIdx.x / chunks;
@@ -395,12 +427,11 @@ int engram::launch_beam_select(const BeamCall &c, void *stream) {
   if (!grid_fits(rows * shape.segs, kScanThreads) || !grid_fits(c.batch, kChooseThreads))
     return ENGRAM_EINVAL;
   const Scale log2e = scale_of(1.0);
-  const int64_t groups = ceil_div(c.vocab, kBeamGroup);
+  const int64_t groups = beam_groups(c.vocab);
   const ScanArgs s = {c.logits, c.vocab, c.stride, shape.segs, shape.seg_len, groups, log2e,
                       c.scores, c.finished, c.parts, c.maxima};
   const ChooseArgs a = {c, shape.segs, groups,
-                        groups > 1 ? (uint32_t)((uint64_t(1) << 32) / groups) : 0xffffffffu,
-                        log2e};
+                        (uint32_t)((uint64_t(1) << 32) / groups), log2e};
   const dim3 grid((unsigned)(rows * shape.segs)), block(kScanThreads);
   const dim3 sequences((unsigned)c.batch), wide(kChooseThreads);
   if (c.type == ENGRAM_BF16) {

@@ -17,6 +17,11 @@
 // For loss and gradient together a block reads its row twice, the second time
 // from the Infinity Cache: the rows in flight are kept within its 256 MB, and
 // the gradient is stored past it (distill_row_kernel).
+//
+// What bounds it is memory: a value costs 2 or 4 bytes and a subtraction, a
+// product, a v_exp_f32 and an addition, so the floor is each logit read once and
+// each gradient written once.  At each kernel below stands what it reaches of
+// the 6.6 TB/s that a large streaming copy does here.
 #include "engram_vocab_dev.h"
 
 namespace engram {
@@ -49,6 +54,8 @@ struct Entries {
         z(reinterpret_cast<float *>(ids + top)), bits(reinterpret_cast<uint32_t *>(z + top)) {}
 };
 constexpr size_t kEntryBytes = 16;
+constexpr int kLead = kWave;  // bits before the first chunk's
+static_assert(kLead * 2 >= kLine, "a wavefront reads a lead");
 
 // What the teacher's row gives beside them.
 struct RowInfo {
@@ -59,11 +66,13 @@ struct RowInfo {
 };
 
 // Reads the teacher's row, by one wavefront: e and *info, for the values [lo, hi) of the
-// vocabulary.  Entries of one id become one, the first, with their sum in their order.
-// WHOLE: the statistics' sum over the named logits too.
+// vocabulary, of which first_bit (kLead before lo at most) has the first bit.  Entries of one id
+// become one, the first, with their sum in their order.  WHOLE: the statistics' sum over the
+// named logits too.
 template <class T, bool WHOLE>
 __device__ __forceinline__ void read_target(const DistillArgs &a, int64_t row, int64_t lo,
-                                            int64_t hi, Entries e, RowInfo *info, int64_t *err) {
+                                            int64_t hi, int64_t first_bit, Entries e,
+                                            RowInfo *info, int64_t *err) {
   const double T_ = a.temperature;
   const int top = (int)a.top, lane = threadIdx.x;
   double most = -__builtin_inf();
@@ -83,7 +92,7 @@ __device__ __forceinline__ void read_target(const DistillArgs &a, int64_t row, i
     most = fmax(most, v);
   }
   count_errors(bad, err);
-  for (int i = lane; i < (int)((hi - lo + 31) / 32); i += kWave) e.bits[i] = 0u;
+  for (int i = lane; i < (int)((hi - first_bit + 31) / 32); i += kWave) e.bits[i] = 0u;
   wave_sync();
   double ref;
   if (a.teacher_lse != nullptr) {
@@ -102,8 +111,8 @@ __device__ __forceinline__ void read_target(const DistillArgs &a, int64_t row, i
     const float x = here ? Chunk<T>::one(z[id]) : kNegInf;
     const double p = id >= 0 ? exp64(e.p[j] - ref) : 0.0;
     if (here) {
-      const uint32_t bit = 1u << ((id - lo) & 31);
-      again |= (atomicOr(&e.bits[(id - lo) >> 5], bit) & bit) != 0;
+      const uint32_t at = (uint32_t)(id - first_bit), bit = 1u << (at & 31);
+      again |= (atomicOr(&e.bits[at >> 5], bit) & bit) != 0;
     }
     e.p[j] = p;
     e.z[j] = x;
@@ -168,7 +177,9 @@ __device__ __forceinline__ void leave_out(float (&z)[8], uint32_t named) {
 }
 
 // The unnamed values of [lo, hi) of a row, summed by a block; the first wavefront reads the
-// teacher's row while the first values are on their way.
+// teacher's row while the first values are on their way.  (Were the named ids not left out
+// here but subtracted afterwards, losses would be off by 1e-6 to 3e-6: the sum's rounding
+// against what is left of it.  Left out they are within 5e-8.)
 template <class T, int THREADS>
 __device__ __forceinline__ RowSum scan_row(const DistillArgs &a, int64_t row, int64_t lo,
                                            int64_t hi, Entries e, RowInfo *info,
@@ -176,11 +187,21 @@ __device__ __forceinline__ RowSum scan_row(const DistillArgs &a, int64_t row, in
   constexpr int U = sizeof(T) == 2 ? 2 : 1;
   const T *z = static_cast<const T *>(a.logits) + row * a.stride;
   const uint8_t *bytes = reinterpret_cast<const uint8_t *>(e.bits);
+  const int lead = lead_of(z + lo, hi - lo), lane = threadIdx.x;
+  const int64_t body = lo + lead;
+  float one = lane < lead ? Chunk<T>::one(z[lo + lane]) : kNegInf;
   Running run;
   each_chunks<T, THREADS, U, false>(
-      z, lo, hi,
+      z, body, hi,
       [&] {
-        if (threadIdx.x < kWave) read_target<T, true>(a, row, lo, hi, e, info, err);
+        if (lane < kWave) {
+          read_target<T, true>(a, row, lo, hi, body - kLead, e, info, err);
+          const int bit = kLead - lead + lane;
+          if (lane < lead && (e.bits[bit >> 5] >> (bit & 31) & 1u) == 0u) {
+            const float ref = run.raise(one, a.c);
+            run.sum += exp_scaled(one - ref, a.c);
+          }
+        }
         __syncthreads();
       },
       [&](int64_t at, float (&v)[U][8]) {
@@ -188,7 +209,7 @@ __device__ __forceinline__ RowSum scan_row(const DistillArgs &a, int64_t row, in
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int64_t i = at + (u * THREADS + (int)threadIdx.x) * 8;
-          leave_out(v[u], i < hi ? bytes[(i - lo) >> 3] : 0u);
+          leave_out(v[u], i < hi ? bytes[kLead / 8 + ((i - body) >> 3)] : 0u);
           m = max8(m, v[u]);
         }
         const float ref = run.raise(m, a.c);
@@ -229,12 +250,14 @@ __device__ __forceinline__ Gradient gradient_of(const RowInfo &info, const RowSu
 }
 
 template <class T>
+__device__ __forceinline__ float gradient_value(float z, const Gradient &g, Scale c) {
+  // (rounded to bf16 the second part of c is lost)
+  return g.factor * (sizeof(T) == 2 ? exp2_fast((z - g.ref) * c.hi) : exp_scaled(z - g.ref, c));
+}
+template <class T>
 __device__ __forceinline__ void gradient_values(float (&z)[8], const Gradient &g, Scale c) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    // (rounded to bf16 the second part of c is lost)
-    z[i] = g.factor * (sizeof(T) == 2 ? exp2_fast((z[i] - g.ref) * c.hi)
-                                      : exp_scaled(z[i] - g.ref, c));
+  for (int i = 0; i < 8; ++i) z[i] = gradient_value<T>(z[i], g, c);
 }
 
 template <class T>
@@ -303,6 +326,21 @@ extern __shared__ __align__(16) char lds[];
 
 // A block to a row: its loss and statistics and, with GRAD, its gradient, for which the row
 // is read again.  8 wavefronts a SIMD in blocks of each size.
+//
+// Without GRAD it is one pass: 4096 x 151,936 bf16 245 us (5.1 TB/s), 4096 x 50,257 83 us
+// (5.0), 1031 x 50,257 27 us (3.9: four blocks a CU and no second round of them, so that the
+// teacher's row before it and the joins behind it are not hidden).  With GRAD 4096 x 151,936
+// bf16 takes 527 us, 4.7 TB/s of the floor's bytes, its blocks reading and writing in turn.
+// Tried instead for these 2.5 GB: the row held in registers from one pass to the other, so
+// that nothing is read twice, 566 us (304 KB leave a CU one block, whose joins then stall
+// it), the same with persistent blocks 610; all rows scanned, then written, 128 to 1024 rows
+// at a time 721 to 1114; ordinary stores 618 against 534 in turn (the gradient pushes rows
+// out of the Infinity Cache); the second pass backwards, or 1 or 4 chunks a lane and step,
+// no change.
+//
+// Chunks start at whole cache lines of the logits, which the gradient usually shares: with
+// the row's first value at the first chunk 4096 x 50,257 bf16 took 226 us with its gradient
+// and 92 without (now 194 and 83), 50,256 192 and 82 (184, 82).
 template <class T, int THREADS, bool GRAD>
 __global__ __launch_bounds__(THREADS, 8) void distill_row_kernel(const DistillArgs a) {
   __shared__ JoinLds<THREADS / kWave> join;
@@ -318,8 +356,15 @@ __global__ __launch_bounds__(THREADS, 8) void distill_row_kernel(const DistillAr
       write_zeros(grad, 0, a.vocab, THREADS);
     } else {
       constexpr int U = sizeof(T) == 2 ? 2 : 1;
+      const T *z = static_cast<const T *>(a.logits) + row * a.stride;
+      const int lead = lead_of(z, a.vocab), thread = threadIdx.x;
       each_chunks<T, THREADS, U, true>(
-          static_cast<const T *>(a.logits) + row * a.stride, 0, a.vocab, [] {},
+          z, lead, a.vocab,
+          [&] {
+            if (thread >= lead) return;
+            const float one = gradient_value<T>(Chunk<T>::one(z[thread]), g, a.c);
+            Chunk<T>::store_one(grad + thread, one);
+          },
           [&](int64_t at, float (&v)[U][8]) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -346,7 +391,9 @@ __global__ __launch_bounds__(THREADS, 8) void distill_row_kernel(const DistillAr
   if (threadIdx.x == 0) write_row(a, row, rest, whole.all, loss, info);
 }
 
-// A block to a segment of a row: its part of the sums and of the loss.
+// A block to a segment of a row: its part of the sums and of the loss.  64 x 151,936 bf16,
+// 16 blocks to a row: 11.4 us, of which the bytes are 3; the rest is the launch and the
+// latency of one block's chain (ids, their logits, their sum, the joins).
 template <class T>
 __global__ __launch_bounds__(kScanThreads, 8) void distill_scan_kernel(const DistillArgs a) {
   __shared__ JoinLds<kScanThreads / kWave> join;
@@ -394,12 +441,13 @@ __device__ __forceinline__ Joined join_parts(const DistillArgs &a, int64_t row) 
   return {{mr, wave_sum(sr)}, {mn, wave_sum(sn)}, wave_sum(loss)};
 }
 
-// A wavefront to a row: its parts joined.
+// A wavefront to a row: its parts joined.  Few bytes: it is the latency of a launch and of
+// the teacher's row, read again.
 template <class T>
 __global__ __launch_bounds__(kWave) void distill_finish_kernel(const DistillArgs a) {
   __shared__ RowInfo info;
   const int64_t row = blockIdx.x;
-  read_target<T, false>(a, row, 0, 0, Entries(lds, a.top), &info, nullptr);
+  read_target<T, false>(a, row, 0, 0, 0, Entries(lds, a.top), &info, nullptr);
   const Joined v = join_parts(a, row);
   const Whole whole = both(v.rest, v.named, a.temperature);
   if (threadIdx.x == 0) write_row(a, row, v.rest, whole.all, v.loss, info);
@@ -409,30 +457,41 @@ __global__ __launch_bounds__(kWave) void distill_finish_kernel(const DistillArgs
 // PARTS, from the parts that distill_scan_kernel left (the first segment's block then also
 // writes the row's loss and statistics).  The segment's values are in registers while the
 // teacher's row is read.
+//
+// 2049 x 32,000 fp32: 104 us (5.0 TB/s of reads and writes; loads that stay in the caches
+// 124 against 110 timed alike), 16,384 x 32,000 bf16 366 (5.7), 4096 x 151,936 bf16 470
+// (5.3), 4096 x 50,257 bf16 149 (5.5; 179 without the alignment to cache lines).  With
+// PARTS, 64 x 151,936 bf16: 11.8 us, latency as in the scan.
 template <class T, bool PARTS>
 __global__ __launch_bounds__(kScanThreads) void distill_backward_kernel(const DistillArgs a,
                                                                         const int64_t segs) {
   constexpr int N = distill_held_backward(sizeof(T));
   __shared__ RowInfo info;
   const int64_t row = blockIdx.x / segs, seg = blockIdx.x - row * segs;
-  // (whole chunks are shared out; the last segment has what is left of one too)
-  const int64_t chunks = a.vocab / 8, lo = chunks * seg / segs * 8;
-  const int64_t hi = seg + 1 == segs ? a.vocab : chunks * (seg + 1) / segs * 8;
-  const T *z = static_cast<const T *>(a.logits) + row * a.stride + lo;
+  constexpr int64_t kLineValues = kLine / sizeof(T);
+  const T *z = static_cast<const T *>(a.logits) + row * a.stride;
   T *grad = static_cast<T *>(a.grad) + row * a.grad_stride;
+  // whole cache lines are shared out; the first segment has the values before them too, the
+  // last those behind: one to each lane of a wavefront
+  const int lead = lead_of(z, a.vocab);
+  const int64_t lines = (a.vocab - lead) / kLineValues;
+  const int64_t body = lead + lines * seg / segs * kLineValues;
+  const int64_t end = lead + lines * (seg + 1) / segs * kLineValues;
+  const int64_t lo = seg == 0 ? 0 : body, hi = seg + 1 == segs ? a.vocab : end;
   const double T_ = a.temperature;
-  const int n = (int)(hi - lo), thread = threadIdx.x;
+  const int n = (int)(end - body), thread = threadIdx.x;
   Chunk<T> r[N];
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     const int i = 8 * (k * kScanThreads + thread);
-    if (i + 8 <= n) r[k].template load<true>(z + i);
+    if (i < n) r[k].template load<true>(z + body + i);
   }
-  const int left = n / 8 * 8 + thread;  // of the values behind the last whole chunk
-  const float one = left < n ? Chunk<T>::one(z[left]) : kNegInf;
+  const int64_t side = thread < kWave ? lo + thread : end + thread - kWave;
+  const bool has_side = thread < kWave ? side < body : thread < 2 * kWave && side < hi;
+  const float one = has_side ? Chunk<T>::one(z[side]) : kNegInf;
   Entries e(lds, a.top);
   if (thread < kWave)
-    read_target<T, false>(a, row, lo, hi, e, &info, !PARTS && seg == 0 ? a.err : nullptr);
+    read_target<T, false>(a, row, lo, hi, lo, e, &info, !PARTS && seg == 0 ? a.err : nullptr);
   __syncthreads();
   Gradient g;
   double below, scale;
@@ -465,18 +524,14 @@ __global__ __launch_bounds__(kScanThreads) void distill_backward_kernel(const Di
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     const int i = 8 * (k * kScanThreads + thread);
-    if (i + 8 <= n) {
+    if (i < n) {
       float v[8];
       r[k].values(v);
       gradient_values<T>(v, g, a.c);
-      Chunk<T>::store_once(grad + lo + i, v);
+      Chunk<T>::store_once(grad + body + i, v);
     }
   }
-  if (left < n) {
-    float v[8] = {one, one, one, one, one, one, one, one};
-    gradient_values<T>(v, g, a.c);
-    Chunk<T>::store_one(grad + lo + left, v[0]);
-  }
+  if (has_side) Chunk<T>::store_one(grad + side, gradient_value<T>(one, g, a.c));
   __syncthreads();
   if (thread < kWave) write_named<T>(a, grad, lo, hi, e, info, below, scale);
 }
@@ -508,7 +563,7 @@ DistillArgs device_args(const engram_distill_args &h, const ScanShape &shape) {
 }
 
 size_t lds_bytes(int64_t top, int64_t values) {
-  return (size_t)top * kEntryBytes + (size_t)ceil_div(values, 32) * 4;
+  return (size_t)top * kEntryBytes + (size_t)ceil_div(values + kLead, 32) * 4;
 }
 
 template <class T, int THREADS>
@@ -523,18 +578,26 @@ void enqueue_rows(const DistillArgs &a, hipStream_t stream) {
 
 template <class T, bool PARTS>
 int enqueue_backward(const DistillArgs &a, hipStream_t stream) {
-  const int64_t most = kScanThreads * distill_held_backward(sizeof(T));  // chunks
-  const int64_t segs = a.vocab < 8 ? 1 : ceil_div(a.vocab / 8, most);
+  const int64_t most = 8 * kScanThreads * distill_held_backward(sizeof(T));  // values
+  const int64_t segs = ceil_div(a.vocab, most);
   if (!grid_fits(a.rows * segs, kScanThreads)) return ENGRAM_EINVAL;
   hipLaunchKernelGGL((distill_backward_kernel<T, PARTS>), dim3((unsigned)(a.rows * segs)),
-                     dim3(kScanThreads), lds_bytes(a.top, most * 8 + 8), stream, a, segs);
+                     dim3(kScanThreads), lds_bytes(a.top, most + 2 * kLead), stream, a, segs);
   return launch_status();
 }
 
 // Bytes of a row up to which a CU's eight blocks of 256 threads, or four of 512, keep the
-// rows in flight (2048 or 1024 of them) within the Infinity Cache.
-constexpr int64_t kDistillRow256 = 100000, kDistillRow512 = 200000;
-constexpr int64_t kDistillWideRows = 512;
+// rows in flight (2048 or 1024 of them) within 112 MB, about half the Infinity Cache, so that
+// the second read finds them there; narrower blocks are quicker at their joins and more of
+// them overlap.  4096 rows with their gradient, us by 256 / 512 / 1024 threads: bf16 16,000
+// values 68 / 84 / 112, 24,000 96 / 101 / 136, 32,000 126 / 120 / 144, 40,000 158 / 145 / 160,
+// 60,000 253 / 230 / 218, 98,000 421 / 382 / 364, 151,936 646 / 548 / 538; fp32 16,000 141 /
+// 128 / 127, 32,000 276 / 262 / 230.
+constexpr int64_t kDistillRow256 = 55000, kDistillRow512 = 110000;
+// Rows up to which each has a CU of its own and its passes gain by every thread: 256 x 32,000
+// bf16 17.4 us by 1024 threads and 19.6 by 256 (without a gradient 13.3 and 14.2), but 512 x
+// 8000 17.7 and 15.5, 768 x 32,000 35.5 and 27.5, 1031 x 50,257 77.7 and 69.6 (40.4, 34.2).
+constexpr int64_t kDistillWideRows = 256;
 
 template <class T>
 int enqueue(const engram_distill_args &h) {

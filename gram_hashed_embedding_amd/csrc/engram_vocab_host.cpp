@@ -85,7 +85,7 @@ extern "C" size_t engram_beam_select_workspace(int64_t batch, int64_t beams, int
   if (!beams_ok(batch, beams) || !rows_ok(batch * beams, vocab, vocab)) return (size_t)-1;
   const int64_t rows = batch * beams;
   if (rows == 0) return 0;
-  return beam_parts_bytes(rows, vocab) + (size_t)rows * (size_t)ceil_div(vocab, kBeamGroup) * 4;
+  return beam_parts_bytes(rows, vocab) + (size_t)rows * (size_t)beam_groups(vocab) * 4;
 }
 
 extern "C" int engram_beam_select(const void *d_logits, int32_t type, int64_t logits_stride,

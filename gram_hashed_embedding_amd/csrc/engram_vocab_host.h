@@ -9,7 +9,7 @@
 namespace engram {
 
 // A row of logits is read in chunks of 8 values, a lane to a chunk, by blocks
-// of kScanThreads lanes; a block's step takes kScanSteps chunks a lane.
+// of kScanThreads lanes.
 constexpr int kScanThreads = 256;
 constexpr int64_t kScanTile = 8 * kScanThreads;  // values
 constexpr int64_t kMaxVocab = int64_t(1) << 30;
@@ -38,11 +38,15 @@ struct ScanPart {
 };
 
 // ------------------------------------------------------------ distillation --
-// Chunks of 8 values that a lane of the backward pass holds.
+// Chunks of 8 values that a lane of the backward pass holds, 32 registers of them: 2049 x
+// 32,000 in fp32 takes 105.4 us, with half as many 106.4 (the teacher's row is read by twice
+// the blocks), with twice as many 109.2 (fewer wavefronts fit a CU).
 constexpr int distill_held_backward(size_t size) { return size == 2 ? 8 : 4; }
 // A block takes a whole row, but for a few long rows with a gradient, which would leave CUs
 // idle, and where a row's bits (one a value: whether a teacher's row names it) would take
-// more than 32 KB of LDS: those are cut.
+// more than 32 KB of LDS: those are cut.  Loss and gradient of rows of 151,936 bf16 values,
+// cut / not: 16 rows 21.5 / 32.0 us, 64 rows 25.6 / 32.1, 128 rows 34.7 / 34.4.  The loss
+// alone gains nothing: its one pass is short beside what a second launch costs.
 constexpr int64_t kDistillMaxSeg = int64_t(1) << 18;
 constexpr int64_t kDistillBlocks = 1024;
 constexpr int64_t kDistillFewRows = 128, kDistillFewVocab = 65536;
@@ -66,13 +70,18 @@ inline size_t distill_workspace(int64_t rows, int64_t vocab, bool grad) {
 }
 
 // --------------------------------------------------------------- selection --
-// The scan leaves the largest logit of every kBeamGroup values.
+// The scan leaves the largest logit of every kBeamGroup values (16 lanes' chunks): the
+// choice reads 1/64 of a bf16 row's bytes for them, and at most 96 groups of it again.  A
+// selection among 512 rows of 151,936 bf16 values takes 44.2 us with 1024 blocks (two to a
+// row), 46.7 with 2048 and 47.3 with 4096: a block's join is paid more often.
 constexpr int64_t kBeamGroup = 128;
 constexpr int64_t kBeamBlocks = 1024;
 constexpr int64_t kBeamMaxSeg = int64_t(1) << 18;
 inline ScanShape beam_shape(int64_t rows, int64_t vocab) {
   return scan_shape(rows, vocab, kBeamBlocks, kBeamMaxSeg);
 }
+// (one more: the values before the first whole cache line)
+inline int64_t beam_groups(int64_t vocab) { return 1 + ceil_div(vocab, kBeamGroup); }
 struct BeamCall {
   const void *logits;
   int32_t type;

@@ -55,9 +55,10 @@ extern "C" {
  * with q = 0 gives a loss of +inf and a finite gradient.  NaN and +inf logits
  * make their own row's loss NaN, and its gradient where it is not 0.
  * Sums over the vocabulary: fp32 terms, summed in fp32 by each lane (128
- * chunks of 8 at most) and in fp64 across lanes, in a fixed order: two calls
- * give the same bits.  The named logits' part, the teacher's and the logarithms
- * are fp64; a term of less than 2^-126 of the largest is lost.  The gradient is
+ * chunks of 8 and a value at most) and in fp64 across lanes, in an order that
+ * the sizes and the alignment of a row's address fix: a repeated call gives the
+ * same bits.  The named logits' part, the teacher's and the logarithms are
+ * fp64; a term of less than 2^-126 of the largest is lost.  The gradient is
  * rounded once to the logits' type.
  *   rows (up to 4,194,303, and rows * ceil(vocab / 16384) for a gradient up to
  *     16,777,215, / 8192 for fp32: a launch's threads), vocab (1 to 2^30), top

@@ -10,9 +10,9 @@ LEAST_REST = 2.0 ** -20
 # What a sum of fp32 exponentials may be off by, relative to itself: v_exp_f32's 1 ulp (2^-23);
 # the roundings of a term's exponent x (a subtraction, a product, an fma: 3 * 2^-24 * x * ln 2),
 # whose mean over the terms is at most the distribution's entropy, 18 bits for 2^18 values; the
-# additions of one lane, one a chunk of at most 2^18 values / 256 lanes / 8 = 128, and 3 within
-# a chunk, 2^-24 each.
-SUM = (2 + 3 * 18 * math.log(2) + 131) * 2.0 ** -24
+# additions of one lane, one a chunk of at most 2^18 values / 256 lanes / 8 = 128, one for a value
+# before the first whole cache line, and 3 within a chunk, 2^-24 each.
+SUM = (2 + 3 * 18 * math.log(2) + 132) * 2.0 ** -24
 # A gradient's share q: that, a term's own roundings (x up to 200 among those that are not lost:
 # 2^-23 + 200 * 3 * 2^-24 * ln 2), and twice the fp32 rounding of an lse up to 64 (2^-19 each).
 SHARE = SUM + 2.0 ** -23 + 600 * math.log(2) * 2.0 ** -24 + 2.0 ** -18
