@@ -178,6 +178,27 @@ def test_rows_apart_and_outputs():
     assert empty.scores.shape == (0, 5)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("vocab", [1, 3, 63, 64, 65, 127, 128, 129, 130, 191, 192, 193, 2300])
+def test_every_place_in_a_cache_line(vocab, dtype):
+    """Logits from every value of a cache line on, the best first, last, and level at both."""
+    z, s = logits(2, 3, vocab, dtype, seed=vocab)
+    z[0, 0, 0], z[0, 1, vocab - 1] = 9.0, 9.5
+    z[1, 0, 0] = z[1, 0, vocab - 1] = z[1, 0, vocab // 2] = 9.0
+    finished = torch.zeros((2, 3), dtype=torch.bool, device="cuda")
+    finished[1, 2] = True
+    line = 128 // dtype.itemsize
+    for first in range(line):
+        wide = torch.full((first + 6 * (vocab + 1) + line,), math.inf, dtype=dtype, device="cuda")
+        part = wide.as_strided((6, vocab), (vocab + 1, 1), first)
+        part.copy_(z.view(6, vocab))
+        workspace = torch.full((V.engram_beam_select_workspace(2, 3, vocab),), 127,
+                               dtype=torch.uint8, device="cuda")
+        check(z, s, 5, finished, vocab - 1,
+              got=V.engram_beam_select(part, s, 5, finished=finished, eos=vocab - 1,
+                                       workspace=workspace))
+
+
 def test_rows_past_32_bits():
     stride = 1 << 27
     z, s = logits(5, 4, 700, seed=14)
@@ -210,7 +231,8 @@ def test_select_refusals():
     with pytest.raises(ValueError):
         V.engram_beam_select(z, s, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
-        V.engram_beam_select(torch.zeros((65, 9), device="cuda"), torch.zeros((1, 65), device="cuda"))
+        V.engram_beam_select(torch.zeros((65, 9), device="cuda"),
+                             torch.zeros((1, 65), device="cuda"))
 
 
 # ------------------------------------------------------------- reordering --
@@ -272,7 +294,8 @@ def test_slots_that_are_none():
     assert torch.equal(pool, before) and int(err) == 3
 
 
-@pytest.mark.parametrize("have, new_len", [(1, 1), (4, 4), (4, 5), (4, 2), (4, 1), (0, 1), (700, 701)])
+@pytest.mark.parametrize("have, new_len", [(1, 1), (4, 4), (4, 5), (4, 2), (4, 1), (0, 1),
+                                           (700, 701)])
 def test_histories(have, new_len):
     parents, slots = fork_case(6, 5, 30, seed=have)
     history = torch.randint(0, 1 << 40, (6, 5, have), device="cuda")

@@ -1,7 +1,7 @@
 """Distillation from a teacher's top logits against the definition in 64 bits: every kernel
-(rows held in registers by blocks of each size, streamed, cut into segments; gradients from the
-statistics), types, odd sizes and strides, rows that a mask leaves nothing of, what does not
-count, and refusals.  The tolerances are derived in vocab_reference."""
+(a block of each size to a row, rows cut into segments, gradients from the statistics), types, odd
+sizes, strides and addresses, rows that a mask leaves nothing of, what does not count, and
+refusals.  The tolerances are derived in vocab_reference."""
 import math
 
 import pytest
@@ -75,8 +75,7 @@ def test_vocabularies(vocab, dtype, target):
     check_all(p, weight)
 
 
-# blocks of 256, 512 and 1024 threads that hold a row (16, 20 and 20 chunks of 8 bf16 values a
-# lane, half as many floats), and rows past the largest
+# a few rows, around whole steps of a block and the lengths from which rows are cut
 @pytest.mark.parametrize("rows, vocab, dtype", [
     (3, 32768, BF), (3, 32769, BF), (131, 65537, BF), (3, 81921, BF), (130, 81920, BF),
     (130, 81921, BF), (129, 163840, BF), (129, 163841, BF), (3, 16385, F32), (3, 40961, F32),
@@ -88,9 +87,50 @@ def test_long_rows(rows, vocab, dtype):
 
 @pytest.mark.parametrize("rows, vocab", [(1, 5000), (513, 3001), (1100, 2500), (2100, 700)])
 def test_many_rows(rows, vocab):
-    """More rows than blocks stay on the GPU: a block takes several in turn."""
+    """More rows than blocks stay on the GPU."""
     p, weight = problem(rows, vocab, 7, BF, seed=rows)
     check_all(p, weight)
+
+
+# rows up to 256 by blocks of 1024 threads; with a gradient more of up to 55,000 bytes by 256,
+# up to 110,000 by 512, longer ones by 1024; up to 128 rows of 65,536 values or more cut, and
+# all past 2^18
+@pytest.mark.parametrize("rows, vocab, dtype", [
+    (256, 2049, BF), (257, 2049, BF), (257, 27500, BF), (257, 27501, BF), (257, 55000, BF),
+    (257, 55001, BF), (257, 13750, F32), (257, 13751, F32), (257, 27500, F32), (257, 27501, F32),
+    (128, 65535, BF), (128, 65536, BF), (129, 65536, BF), (128, 65537, F32), (129, 65537, F32),
+    (129, 262144, BF), (129, 262145, BF), (1, 262144, F32)])
+def test_rows_that_a_rule_divides(rows, vocab, dtype):
+    p, weight = problem(rows, vocab, 5, dtype, seed=rows + vocab)
+    check_all(p, weight)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows, vocab", [(3, 1), (3, 3), (3, 63), (3, 64), (3, 65), (3, 130),
+                                         (257, 131), (2, 2049), (3, 65600), (1, 262150)])
+def test_every_place_in_a_cache_line(rows, vocab, dtype):
+    """Logits from every value of a cache line on, the gradient elsewhere in one; what lies
+    around it stays."""
+    p, weight = problem(rows, vocab, min(4, vocab), dtype, seed=vocab)
+    p["ids"][0, 0], p["ids"][rows - 1, 0] = 0, vocab - 1
+    want = reference(p, weight)
+    z, stride = p["logits"], vocab + 3
+    line = 128 // dtype.itemsize
+    for first in range(line if vocab < 3000 else 5):
+        wide = torch.full((first + rows * stride + line,), math.nan, dtype=dtype, device="cuda")
+        p["logits"] = wide.as_strided((rows, vocab), (stride, 1), first)
+        p["logits"].copy_(z)
+        around = torch.full((line + rows * stride,), 7.0, dtype=dtype, device="cuda")
+        at = (5 * first + 2) % line
+        grad = around.as_strided((rows, vocab), (stride, 1), at)
+        d = forward(p)
+        R.check_distill(d._asdict(), want)
+        for call in (lambda: forward(p, weight, grad=grad).grad,
+                     lambda: backward(p, weight, d, grad=grad)):
+            around.fill_(7.0)
+            R.check_distill(dict(grad=call()), want)
+            grad.fill_(7.0)
+            assert bool((around == 7.0).all())
 
 
 @pytest.mark.parametrize("top", [1, 2, 63, 64, 65, 255, 256, 257, 1000, 1024])
@@ -227,6 +267,7 @@ def test_a_label_is_cross_entropy():
     z64 = z.double().requires_grad_()
     loss = torch.nn.functional.cross_entropy(z64, labels, ignore_index=-1, reduction="none")
     loss.sum().backward()
+    loss = loss.detach()
     assert float((d.loss - loss).abs().max()) <= 2 * R.SUM + 2.0 ** -24 * float(loss.max())
     assert float((d.grad - z64.grad).abs().max()) <= R.SHARE + 2.0 ** -24
 
