@@ -241,6 +241,7 @@ __global__ __launch_bounds__(kChooseThreads) void beam_choose_kernel(const Choos
   __shared__ ChooseLds l;
   __shared__ double lse[ENGRAM_BEAM_MAX];    // NaN: no candidate but a finished beam's
   __shared__ double score[ENGRAM_BEAM_MAX];
+  __shared__ bool done[ENGRAM_BEAM_MAX];     // (out_scores and out_finished may be the inputs)
   __shared__ int64_t group_at[kChooseGroups];  // of each chosen group: its first value
   __shared__ int64_t group_end[kChooseGroups];  // what it ends before
   __shared__ int group_beam[kChooseGroups];
@@ -251,10 +252,6 @@ __global__ __launch_bounds__(kChooseThreads) void beam_choose_kernel(const Choos
   const auto value_of = [&](int w, float z) {
     const double v = score[w] + ((double)z - lse[w]);
     return v == v ? v : kNone;
-  };
-  const auto finished = [&](int w) {
-    return c.finished != nullptr && c.finished[first_row + w] != 0 &&
-           __builtin_isfinite(score[w]);
   };
   // i / groups by the whole part of 2^32 / groups, which is at most one too small
   const auto beam_of = [&](uint32_t i) {
@@ -269,7 +266,7 @@ __global__ __launch_bounds__(kChooseThreads) void beam_choose_kernel(const Choos
       [&](int i, float z) {
         const int w = beam_of(i);
         if (lse[w] == lse[w]) return value_of(w, z);
-        return i == w * groups && finished(w) ? score[w] : kNone;
+        return i == w * groups && done[w] ? score[w] : kNone;
       },
       [&](int i) { return (int64_t)i; },
       [&] {
@@ -284,6 +281,8 @@ __global__ __launch_bounds__(kChooseThreads) void beam_choose_kernel(const Choos
           if (t % kWave == 0) {
             lse[w] = v;
             score[w] = c.scores[row];
+            done[w] = c.finished != nullptr && c.finished[row] != 0 &&
+                      __builtin_isfinite(c.scores[row]);
           }
         }
         __syncthreads();
@@ -332,7 +331,7 @@ __global__ __launch_bounds__(kChooseThreads) void beam_choose_kernel(const Choos
     c.out_parents[o] = w;
     c.out_tokens[o] = v;
     if (c.out_finished != nullptr)
-      c.out_finished[o] = there && (v == c.eos || finished((int)w));
+      c.out_finished[o] = there && (v == c.eos || done[w]);
   }
 }
 

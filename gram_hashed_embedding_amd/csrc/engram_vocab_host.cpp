@@ -55,6 +55,12 @@ extern "C" int engram_distill(const engram_distill_args *a) {
   if (a->d_loss == nullptr && a->d_lse == nullptr && a->d_lse_rest == nullptr &&
       a->d_grad == nullptr)
     return ENGRAM_EINVAL;
+  // (a row's statistics are written while other blocks still read its inputs)
+  const float *const outs[] = {a->d_loss, a->d_lse, a->d_lse_rest};
+  for (int i = 0; i < 3; ++i)
+    if (outs[i] != nullptr && (outs[i] == a->d_grad_loss || outs[i] == a->d_teacher_lse ||
+                               outs[i] == outs[(i + 1) % 3]))
+      return ENGRAM_EINVAL;
   const size_t need = distill_workspace(a->rows, a->vocab, a->d_grad != nullptr);
   if (need > 0 && (a->d_workspace == nullptr || !aligned16(a->d_workspace) ||
                    a->workspace_bytes < need))
@@ -103,6 +109,9 @@ extern "C" int engram_beam_select(const void *d_logits, int32_t type, int64_t lo
   if (d_logits == nullptr || d_scores == nullptr || d_out_scores == nullptr ||
       d_out_parents == nullptr || d_out_tokens == nullptr)
     return ENGRAM_EINVAL;
+  if (count != beams &&
+      (d_out_scores == d_scores || (d_finished != nullptr && d_out_finished == d_finished)))
+    return ENGRAM_EINVAL;
   if (d_workspace == nullptr || !aligned16(d_workspace) ||
       workspace_bytes < engram_beam_select_workspace(batch, beams, vocab))
     return ENGRAM_EWORKSPACE;
@@ -148,7 +157,8 @@ extern "C" int engram_beam_fork(const int64_t *d_parents, const int64_t *d_slots
   // (without explicit slots every beam has one of its own)
   if (pools > 0 && d_slots == nullptr && slot_count < batch * beams) return ENGRAM_EINVAL;
   if (batch == 0) return ENGRAM_OK;
-  if (d_parents == nullptr || d_new_slots == nullptr || d_new_slots == d_slots)
+  if (d_parents == nullptr || d_new_slots == nullptr || d_new_slots == d_slots ||
+      d_new_slots == d_parents)
     return ENGRAM_EINVAL;
   if (misaligned) return ENGRAM_EALIGN;
   c.parents = d_parents;

@@ -235,7 +235,8 @@ def engram_beam_select(logits, scores, count=None, *, finished=None, eos=-1, out
     fp32 [batch * beams, vocab] or [batch, beams, vocab] (rows may lie apart), scores fp32
     [batch, beams] the beams' log-probabilities so far (-inf: no beam), finished bool [batch,
     beams] those that `eos` has ended.  Entries that nothing is left for have score -inf and
-    parent and token -1."""
+    parent and token -1.  With as many as there are beams out_scores may be scores and
+    out_finished finished."""
     index, rows, vocab, stride, kind = _logits(logits, "logits")
     if not isinstance(scores, torch.Tensor) or scores.dim() != 2:
         raise ValueError("scores must be [batch, beams]")
@@ -370,11 +371,11 @@ def engram_beam_fork(parents, pools=(), *, slots=None, tokens=None, history=None
             out_p = _tensor(new_history, torch.int64, n * new_len, "new_history", index)
             if new_history.shape != (batch, beams, new_len):
                 _check_rows(new_history, (batch, beams, new_len), (new_len,), "new_history")
-    elif new_history is not None or new_len is not None:
-        raise ValueError("new_history and new_len need history")
+    elif tokens is not None or new_history is not None or new_len is not None:
+        raise ValueError("tokens, new_history and new_len need history")
     err_p = _optional(err_count, torch.int64, 1, "err_count", index)
     lists = _LISTS[len(pools)]
     _run(index, "engram_beam_fork", parents_p, slots_p, batch, beams, lists.pack(*addresses),
-         lists.pack(*sizes), len(pools), count, new_p, tokens_p if history is not None else None, history_p, have,
-         out_p, new_len or 0, err_p, _stream_of(index))
+         lists.pack(*sizes), len(pools), count, new_p, tokens_p, history_p, have, out_p,
+         new_len or 0, err_p, _stream_of(index))
     return Fork(new_slots, new_history)

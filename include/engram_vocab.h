@@ -130,6 +130,8 @@ int engram_distill_backward(const engram_distill_args *args);
  *   d_out_scores fp32, d_out_parents int64 (the beam's index in its
  *     sequence), d_out_tokens int64, d_out_finished uint8 (the parent was
  *     finished or the token is eos_id; may be NULL): [batch, count], written.
+ *     With count == beams d_out_scores may be d_scores, and d_out_finished
+ *     d_finished.
  *   The workspace holds engram_beam_select_workspace bytes, 16-byte aligned.
  * Errors: EINVAL, EWORKSPACE.  batch == 0 enqueues nothing.
  */
@@ -157,7 +159,7 @@ int engram_beam_select(const void *d_logits, int32_t type, int64_t logits_stride
  *     Repeated slots race on their contents (in bounds).
  *   h_pools, h_slot_bytes: `pools` (0 to ENGRAM_FORK_MAX_POOLS) device
  *     buffers of slot_count slots of that many bytes (a multiple of 16).
- *   d_new_slots int64 [batch, beams], written; not d_slots.
+ *   d_new_slots int64 [batch, beams], written; not d_slots or d_parents.
  *   d_history int64 [batch, beams, history_len] and d_new_history [batch,
  *     beams, new_len], 1 <= new_len <= history_len + 1, with d_tokens int64
  *     [batch, beams]: new row j is the last new_len values of the parent's

@@ -159,6 +159,18 @@ def test_finished_beams(vocab):
     assert got.parents[0].tolist().index(0) < got.parents[0].tolist().index(2)
 
 
+def test_scores_and_flags_in_place():
+    z, s = logits(5, 6, 900, seed=15)
+    f = torch.rand((5, 6), device="cuda") < 0.4
+    want = V.engram_beam_select(z, s, finished=f, eos=3)
+    got = V.engram_beam_select(z, s, finished=f, eos=3, out_scores=s, out_finished=f)
+    assert got.scores is s and got.finished is f
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    with pytest.raises(V.EngramError):                # another sequence's are read later
+        V.engram_beam_select(z, s, 5, out_scores=s.flatten()[:25].view(5, 5))
+
+
 def test_rows_apart_and_outputs():
     z, s = logits(3, 4, 1003, seed=13)
     wide = torch.full((12, 1040), 99.0, dtype=BF, device="cuda")
@@ -349,8 +361,12 @@ def test_fork_refusals():
     with pytest.raises(ValueError):
         V.engram_beam_fork(parents, pool, tokens=parents, new_len=2,
                            history=torch.zeros((2, 3, 0), dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError):
+        V.engram_beam_fork(parents, pool, tokens=parents)             # without a history
     with pytest.raises(V.EngramError):
         V.engram_beam_fork(parents, [pool, pool])                     # one pool twice
+    with pytest.raises(V.EngramError):
+        V.engram_beam_fork(parents, pool, new_slots=parents)
     with pytest.raises(V.EngramError):
         V.engram_beam_fork(parents, pool[:5])                         # fewer slots than beams
     with pytest.raises(V.EngramError):

@@ -17,7 +17,8 @@ def distill(call, **fields):
     """A full call with some fields replaced."""
     a = abi.EngramDistillArgs(rows=4, vocab=50, top=3, logits_stride=64, grad_stride=50,
                               temperature=1.0, d_logits=A, d_ids=A, d_teacher=A, d_teacher_lse=A,
-                              rest=1, d_grad_loss=A, d_loss=A, d_lse=A, d_lse_rest=A, d_grad=B)
+                              rest=1, d_grad_loss=A + 64, d_loss=C, d_lse=C + 64,
+                              d_lse_rest=C + 128, d_grad=B)
     for k, v in fields.items():
         setattr(a, k, v)
     return call(ctypes.byref(a))
@@ -36,7 +37,9 @@ SHARED = [
 
 
 def case_distill_rejects(lib):
-    for fields in SHARED + [dict(d_grad=None)]:
+    for fields in SHARED + [dict(d_grad=None), dict(d_loss=A), dict(d_lse=A + 64),
+                            dict(d_lse_rest=A), dict(d_lse=C), dict(d_lse_rest=C),
+                            dict(d_lse_rest=C + 64)]:
         assert distill(lib.engram_distill, **fields) == INVALID, fields
     assert distill(lib.engram_distill, d_loss=None, d_lse=None, d_lse_rest=None, d_grad=None,
                    d_grad_loss=None) == INVALID
@@ -77,7 +80,7 @@ def case_distill_workspace(lib):
 
 def select(call, **fields):
     a = dict(logits=A, type=abi.BF16, stride=64, scores=A, finished=A, eos=3, batch=2, beams=3,
-             vocab=50, count=4, out_scores=A, parents=A, tokens=A, out_finished=A, workspace=C,
+             vocab=50, count=4, out_scores=B, parents=B, tokens=B, out_finished=B, workspace=C,
              size=1 << 20, stream=None)
     a.update(fields)
     return call(*a.values())
@@ -89,7 +92,8 @@ def case_select_rejects(lib):
                    dict(beams=abi.BEAM_MAX + 1), dict(vocab=0), dict(vocab=1 << 31, stride=1 << 31),
                    dict(count=0), dict(count=abi.BEAM_MAX + 1), dict(eos=-1), dict(eos=-2),
                    dict(eos=50), dict(logits=None), dict(scores=None), dict(out_scores=None),
-                   dict(parents=None), dict(tokens=None), dict(batch=1 << 60)):
+                   dict(parents=None), dict(tokens=None), dict(batch=1 << 60),
+                   dict(out_scores=A), dict(out_finished=A)):
         assert select(call, **fields) == INVALID, fields
     for fields in (dict(workspace=None), dict(workspace=ODD), dict(size=16)):
         assert select(call, **fields) == WORKSPACE, fields
@@ -112,8 +116,8 @@ def fork(call, held=((B, 64),), **fields):
 
 def case_fork_rejects(lib):
     call = lib.engram_beam_fork
-    for fields in (dict(parents=None), dict(new_slots=None), dict(new_slots=C), dict(batch=-1),
-                   dict(beams=0), dict(beams=abi.BEAM_MAX + 1), dict(slot_count=-1), dict(n=-1),
+    for fields in (dict(parents=None), dict(new_slots=None), dict(new_slots=C), dict(new_slots=A),
+                   dict(batch=-1), dict(beams=0), dict(beams=abi.BEAM_MAX + 1), dict(slot_count=-1), dict(n=-1),
                    dict(n=abi.FORK_MAX_POOLS + 1), dict(pools=None), dict(sizes=None),
                    dict(tokens=None), dict(history=None), dict(new_history=None),
                    dict(new_history=A), dict(new_len=0), dict(new_len=6), dict(history_len=-1),
