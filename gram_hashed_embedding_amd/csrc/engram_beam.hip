@@ -39,7 +39,7 @@ __device__ __forceinline__ bool beam_live(const float *scores, const uint8_t *fi
 }
 
 // A block to a segment of a beam's logits.  Memory bounds it: 512 beams of 151,936 bf16 values
-// are read in 28 us (5.5 TB/s); 4 chunks a lane and step instead of 2 are no faster.  The
+// are read in 29 to 32 us (5.4 to 4.9 TB/s); 4 chunks a lane and step instead of 2 are no faster.  The
 // groups' maxima wait in LDS and are written 4 bytes a lane next to each other at the end,
 // not by every 16th lane in between.  Groups begin at whole cache lines: 4096 beams of 50,257
 // bf16 values take 97 us for a selection, 108 if they begin with the row.  One beam or a few: 4 to 6 us, a block's own latency.

@@ -329,14 +329,15 @@ extern __shared__ __align__(16) char lds[];
 //
 // Without GRAD it is one pass: 4096 x 151,936 bf16 245 us (5.1 TB/s), 4096 x 50,257 83 us
 // (5.0), 1031 x 50,257 27 us (3.9: four blocks a CU and no second round of them, so that the
-// teacher's row before it and the joins behind it are not hidden).  With GRAD 4096 x 151,936
-// bf16 takes 527 us, 4.7 TB/s of the floor's bytes, its blocks reading and writing in turn.
-// Tried instead for these 2.5 GB: the row held in registers from one pass to the other, so
-// that nothing is read twice, 566 us (304 KB leave a CU one block, whose joins then stall
-// it), the same with persistent blocks 610; all rows scanned, then written, 128 to 1024 rows
-// at a time 721 to 1114; ordinary stores 618 against 534 in turn (the gradient pushes rows
-// out of the Infinity Cache); the second pass backwards, or 1 or 4 chunks a lane and step,
-// no change.
+// teacher's row before it and the joins behind it are not hidden), 16,384 x 1000 34 us (a
+// wavefront to a row, each waiting for its teacher's entries and their logits in turn).  With
+// GRAD 4096 x 151,936 bf16 takes 527 us, 4.7 TB/s of the floor's bytes, its blocks reading and
+// writing in turn.  Tried instead for these 2.5 GB: the row held in registers from one pass to
+// the other, so that nothing is read twice, 566 us (304 KB leave a CU one block, whose joins
+// then stall it), the same with persistent blocks 610; all rows scanned, then written, 128 to
+// 1024 rows at a time 721 to 1114; ordinary stores 618 against 534 in turn (the gradient
+// pushes rows out of the Infinity Cache); the second pass backwards, or 1 or 4 chunks a lane
+// and step, no change.
 //
 // Chunks start at whole cache lines of the logits, which the gradient usually shares: with
 // the row's first value at the first chunk 4096 x 50,257 bf16 took 226 us with its gradient
@@ -462,9 +463,9 @@ __global__ __launch_bounds__(kWave) void distill_finish_kernel(const DistillArgs
 // 124 against 110 timed alike), 16,384 x 32,000 bf16 366 (5.7), 4096 x 151,936 bf16 470
 // (5.3), 4096 x 50,257 bf16 149 (5.5; 179 without the alignment to cache lines).  With
 // PARTS, 64 x 151,936 bf16: 11.8 us, latency as in the scan.
-template <class T, bool PARTS>
-__global__ __launch_bounds__(kScanThreads) void distill_backward_kernel(const DistillArgs a,
-                                                                        const int64_t segs) {
+template <class T, int THREADS, bool PARTS>
+__global__ __launch_bounds__(THREADS) void distill_backward_kernel(const DistillArgs a,
+                                                                   const int64_t segs) {
   constexpr int N = distill_held_backward(sizeof(T));
   __shared__ RowInfo info;
   const int64_t row = blockIdx.x / segs, seg = blockIdx.x - row * segs;
@@ -472,7 +473,7 @@ __global__ __launch_bounds__(kScanThreads) void distill_backward_kernel(const Di
   const T *z = static_cast<const T *>(a.logits) + row * a.stride;
   T *grad = static_cast<T *>(a.grad) + row * a.grad_stride;
   // whole cache lines are shared out; the first segment has the values before them too, the
-  // last those behind: one to each lane of a wavefront
+  // last those behind: one of each to a lane of the block's last wavefront
   const int lead = lead_of(z, a.vocab);
   const int64_t lines = (a.vocab - lead) / kLineValues;
   const int64_t body = lead + lines * seg / segs * kLineValues;
@@ -483,12 +484,13 @@ __global__ __launch_bounds__(kScanThreads) void distill_backward_kernel(const Di
   Chunk<T> r[N];
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    const int i = 8 * (k * kScanThreads + thread);
+    const int i = 8 * (k * THREADS + thread);
     if (i < n) r[k].template load<true>(z + body + i);
   }
-  const int64_t side = thread < kWave ? lo + thread : end + thread - kWave;
-  const bool has_side = thread < kWave ? side < body : thread < 2 * kWave && side < hi;
-  const float one = has_side ? Chunk<T>::one(z[side]) : kNegInf;
+  const int lane = thread - (THREADS - kWave);
+  const bool before = lane >= 0 && lo + lane < body, behind = lane >= 0 && end + lane < hi;
+  const float first = before ? Chunk<T>::one(z[lo + lane]) : kNegInf;
+  const float last = behind ? Chunk<T>::one(z[end + lane]) : kNegInf;
   Entries e(lds, a.top);
   if (thread < kWave)
     read_target<T, false>(a, row, lo, hi, lo, e, &info, !PARTS && seg == 0 ? a.err : nullptr);
@@ -518,12 +520,12 @@ __global__ __launch_bounds__(kScanThreads) void distill_backward_kernel(const Di
     scale = lse == -__builtin_inf() ? 0.0 : 1.0;
   }
   if (g.zero) {
-    write_zeros(grad, lo, hi, kScanThreads);
+    write_zeros(grad, lo, hi, THREADS);
     return;
   }
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    const int i = 8 * (k * kScanThreads + thread);
+    const int i = 8 * (k * THREADS + thread);
     if (i < n) {
       float v[8];
       r[k].values(v);
@@ -531,7 +533,8 @@ __global__ __launch_bounds__(kScanThreads) void distill_backward_kernel(const Di
       Chunk<T>::store_once(grad + body + i, v);
     }
   }
-  if (has_side) Chunk<T>::store_one(grad + side, gradient_value<T>(one, g, a.c));
+  if (before) Chunk<T>::store_one(grad + lo + lane, gradient_value<T>(first, g, a.c));
+  if (behind) Chunk<T>::store_one(grad + end + lane, gradient_value<T>(last, g, a.c));
   __syncthreads();
   if (thread < kWave) write_named<T>(a, grad, lo, hi, e, info, below, scale);
 }
@@ -576,28 +579,54 @@ void enqueue_rows(const DistillArgs &a, hipStream_t stream) {
     hipLaunchKernelGGL((distill_row_kernel<T, THREADS, false>), grid, block, bytes, stream, a);
 }
 
-template <class T, bool PARTS>
+template <class T, int THREADS, bool PARTS>
 int enqueue_backward(const DistillArgs &a, hipStream_t stream) {
-  const int64_t most = 8 * kScanThreads * distill_held_backward(sizeof(T));  // values
+  const int64_t most = 8 * THREADS * distill_held_backward(sizeof(T));  // values
   const int64_t segs = ceil_div(a.vocab, most);
   if (!grid_fits(a.rows * segs, kScanThreads)) return ENGRAM_EINVAL;
-  hipLaunchKernelGGL((distill_backward_kernel<T, PARTS>), dim3((unsigned)(a.rows * segs)),
-                     dim3(kScanThreads), lds_bytes(a.top, most + 2 * kLead), stream, a, segs);
+  hipLaunchKernelGGL((distill_backward_kernel<T, THREADS, PARTS>), dim3((unsigned)(a.rows * segs)),
+                     dim3(THREADS), lds_bytes(a.top, most + 2 * kLead), stream, a, segs);
   return launch_status();
 }
+// A row that a wavefront holds (8192 bytes) goes by one: 16,384 rows of 2000 bytes in bf16 35 us,
+// by 256 threads 75, 8000 bytes 64 and 86 (fp32 34 and 69, 72 and 83); the teacher's row is each
+// block's first work.  Longer ones take as long either way, and more for more entries in
+// narrower blocks, each of which reads them: fp32 rows of 128,000 bytes 885 by 64 threads and
+// 829 by 256.
+template <class T>
+int enqueue_kept(const DistillArgs &a, hipStream_t stream) {
+  if (a.vocab <= 8 * kWave * distill_held_backward(sizeof(T)))
+    return enqueue_backward<T, kWave, false>(a, stream);
+  return enqueue_backward<T, kScanThreads, false>(a, stream);
+}
 
-// Bytes of a row up to which a CU's eight blocks of 256 threads, or four of 512, keep the
-// rows in flight (2048 or 1024 of them) within 112 MB, about half the Infinity Cache, so that
-// the second read finds them there; narrower blocks are quicker at their joins and more of
-// them overlap.  4096 rows with their gradient, us by 256 / 512 / 1024 threads: bf16 16,000
-// values 68 / 84 / 112, 24,000 96 / 101 / 136, 32,000 126 / 120 / 144, 40,000 158 / 145 / 160,
-// 60,000 253 / 230 / 218, 98,000 421 / 382 / 364, 151,936 646 / 548 / 538; fp32 16,000 141 /
-// 128 / 127, 32,000 276 / 262 / 230.
-constexpr int64_t kDistillRow256 = 55000, kDistillRow512 = 110000;
-// Rows up to which each has a CU of its own and its passes gain by every thread: 256 x 32,000
-// bf16 17.4 us by 1024 threads and 19.6 by 256 (without a gradient 13.3 and 14.2), but 512 x
-// 8000 17.7 and 15.5, 768 x 32,000 35.5 and 27.5, 1031 x 50,257 77.7 and 69.6 (40.4, 34.2).
-constexpr int64_t kDistillWideRows = 256;
+// Threads of a row's block.  Few rows have a CU each and gain by every thread; of many, narrow
+// blocks are quicker at what is not the vocabulary's, and more of them overlap.  us with / without
+// a gradient, calls of a graph, bf16 (fp32 likewise by its bytes), 64 / 128 / 256 / 512 / 1024:
+//   256 rows of 8000 bytes    14.3  12.5  11.9  12.5  14.0     11.2  10.1  10.0  10.0  10.4
+//              24,000         21.6  16.7  14.6  14.1  14.0     15.1  12.4  11.3  10.7  10.5
+//              64,000         37.5  25.1  19.9  17.4  16.8     23.0  17.0  14.1  12.8  12.1
+//   1500 rows of 2000         13.8  15.2  17.0  26.2  43.3     11.1  11.5  12.4  18.2  30.3
+//                8000         19.1  18.3  18.3  25.9  42.1     14.0  13.6  13.5  18.6  29.1
+//              32,000         34.5  30.5  29.2  32.8  42.6     21.7  19.3  19.1  22.6  29.4
+//   16,384 rows of 2000       46    67    103   212   400      34    47    71    147   282
+//                8000         76    90    115   217   384      47    57    76    149   264
+//              16,000         134   126   148   225   395      64    74    90    150   263
+//              32,000         265   246   230   290   438      109   106   122   175   279
+//              64,000         551   485   453   431   542      197   196   186   220   317
+// With a gradient long rows are also kept from crowding each other out of the Infinity Cache
+// before they are read again: 2048 of them in flight by 256 threads, 1024 by 512 and 512 by
+// 1024, to stay within 112 MB.  4096 rows, us by 256 / 512 / 1024 threads: 80,000 bytes 158 /
+// 145 / 160, 120,000 253 / 230 / 218, 196,000 421 / 382 / 364, 303,872 646 / 548 / 538.
+constexpr int64_t kDistillManyRows = 2048;
+int distill_threads(int64_t rows, int64_t bytes, bool grad) {
+  if (rows <= 256) return bytes <= 12000 ? 256 : bytes <= 48000 ? 512 : 1024;
+  const bool many = rows > kDistillManyRows;
+  if (bytes <= (!many ? 4000 : grad ? 9000 : 20000)) return 64;
+  if (many && bytes <= (grad ? 20000 : 40000)) return 128;
+  if (!grad || bytes <= 55000) return 256;
+  return bytes <= 110000 ? 512 : 1024;
+}
 
 template <class T>
 int enqueue(const engram_distill_args &h) {
@@ -608,20 +637,20 @@ int enqueue(const engram_distill_args &h) {
   if (!grid_fits(h.rows, 1024) || !grid_fits(h.rows * shape.segs, kScanThreads))
     return ENGRAM_EINVAL;
   if (!distill_cut(h.rows, h.vocab, grad)) {
-    const int64_t bytes = h.vocab * (int64_t)sizeof(T);
-    if (h.rows <= kDistillWideRows || (grad && bytes > kDistillRow512))
-      enqueue_rows<T, 1024>(plain, stream);
-    else if (grad && bytes > kDistillRow256)
-      enqueue_rows<T, 512>(plain, stream);
-    else
-      enqueue_rows<T, 256>(plain, stream);
+    switch (distill_threads(h.rows, h.vocab * (int64_t)sizeof(T), grad)) {
+      case 64: enqueue_rows<T, 64>(plain, stream); break;
+      case 128: enqueue_rows<T, 128>(plain, stream); break;
+      case 256: enqueue_rows<T, 256>(plain, stream); break;
+      case 512: enqueue_rows<T, 512>(plain, stream); break;
+      default: enqueue_rows<T, 1024>(plain, stream);
+    }
     return launch_status();
   }
   DistillArgs a = plain;
   a.parts = static_cast<DistillPart *>(h.d_workspace);
   hipLaunchKernelGGL(distill_scan_kernel<T>, dim3((unsigned)(h.rows * shape.segs)),
                      dim3(kScanThreads), lds_bytes(h.top, shape.seg_len), stream, a);
-  if (grad) return enqueue_backward<T, true>(a, stream);
+  if (grad) return enqueue_backward<T, kScanThreads, true>(a, stream);
   hipLaunchKernelGGL(distill_finish_kernel<T>, dim3((unsigned)h.rows), dim3(kWave),
                      lds_bytes(h.top, 0), stream, a);
   return launch_status();
@@ -637,6 +666,6 @@ int engram::launch_distill(const engram_distill_args &h) {
 int engram::launch_distill_backward(const engram_distill_args &h) {
   const DistillArgs a = device_args(h, ScanShape{});
   const hipStream_t stream = as_stream(h.stream);
-  return h.logits_type == ENGRAM_BF16 ? enqueue_backward<uint16_t, false>(a, stream)
-                                      : enqueue_backward<float, false>(a, stream);
+  return h.logits_type == ENGRAM_BF16 ? enqueue_kept<uint16_t>(a, stream)
+                                      : enqueue_kept<float>(a, stream);
 }

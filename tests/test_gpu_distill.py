@@ -92,10 +92,15 @@ def test_many_rows(rows, vocab):
     check_all(p, weight)
 
 
-# rows up to 256 by blocks of 1024 threads; with a gradient more of up to 55,000 bytes by 256,
-# up to 110,000 by 512, longer ones by 1024; up to 128 rows of 65,536 values or more cut, and
-# all past 2^18
+# rows up to 256 by blocks of 256, 512 and 1024 threads (12,000, 48,000 bytes), up to 2048 by 64
+# and 256 (4000), more by 64, 128 and 256 (9000 and 20,000 with a gradient, 20,000 and 40,000
+# without); with a gradient longer ones by 512 and 1024 (55,000, 110,000); gradients from the
+# statistics by 64 and 256 (8192); up to 128 rows of 65,536 values or more cut, and all past 2^18
 @pytest.mark.parametrize("rows, vocab, dtype", [
+    (7, 4096, BF), (7, 4097, BF), (7, 6000, BF), (7, 6001, BF), (7, 24000, BF), (7, 24001, BF),
+    (256, 3000, F32), (256, 3001, F32), (257, 2000, BF), (257, 2001, BF), (2048, 1000, F32),
+    (2048, 1001, F32), (2049, 4500, BF), (2049, 4501, BF), (2049, 2250, F32), (2049, 2251, F32),
+    (2049, 10000, BF), (2049, 10001, BF), (2049, 20000, BF), (2049, 20001, BF), (2049, 10001, F32),
     (256, 2049, BF), (257, 2049, BF), (257, 27500, BF), (257, 27501, BF), (257, 55000, BF),
     (257, 55001, BF), (257, 13750, F32), (257, 13751, F32), (257, 27500, F32), (257, 27501, F32),
     (128, 65535, BF), (128, 65536, BF), (129, 65536, BF), (128, 65537, F32), (129, 65537, F32),
