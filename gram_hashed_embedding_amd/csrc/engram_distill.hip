@@ -67,15 +67,19 @@ struct RowInfo {
 
 // Reads the teacher's row, by one wavefront: e and *info, for the values [lo, hi) of the
 // vocabulary, of which first_bit (kLead before lo at most) has the first bit.  Entries of one id
-// become one, the first, with their sum in their order.  WHOLE: the statistics' sum over the
-// named logits too.
+// become one, the first, with their sum.  WHOLE: the statistics' sum over the named logits too.
 template <class T, bool WHOLE>
 __device__ __forceinline__ void read_target(const DistillArgs &a, int64_t row, int64_t lo,
                                             int64_t hi, int64_t first_bit, Entries e,
                                             RowInfo *info, int64_t *err) {
   const double T_ = a.temperature;
   const int top = (int)a.top, lane = threadIdx.x;
+  const T *z = static_cast<const T *>(a.logits) + row * a.stride;
+  // (loaded here, their latency is beside that of the ids)
+  const float whole = a.teacher_lse != nullptr ? a.teacher_lse[row] : 0.0f;
+  const float weight = a.grad_loss != nullptr ? a.grad_loss[row] : 0.0f;
   double most = -__builtin_inf();
+  float max = kNegInf;
   int bad = 0;
   bool used = false;
   for (int j = lane; j < top; j += kWave) {
@@ -96,15 +100,13 @@ __device__ __forceinline__ void read_target(const DistillArgs &a, int64_t row, i
   wave_sync();
   double ref;
   if (a.teacher_lse != nullptr) {
-    ref = a.teacher_lse[row];
+    ref = whole;
   } else {
     ref = wave_max(most);
     if (ref == -__builtin_inf()) ref = 0.0;
   }
-  const T *z = static_cast<const T *>(a.logits) + row * a.stride;
   double sum = 0.0;
-  float max = kNegInf;
-  bool again = false;
+  uint32_t again = 0;  // a bit for each of the lane's entries
   for (int j = lane; j < top; j += kWave) {
     const int32_t id = e.ids[j];
     const bool here = id >= lo && id < hi;
@@ -112,7 +114,7 @@ __device__ __forceinline__ void read_target(const DistillArgs &a, int64_t row, i
     const double p = id >= 0 ? exp64(e.p[j] - ref) : 0.0;
     if (here) {
       const uint32_t at = (uint32_t)(id - first_bit), bit = 1u << (at & 31);
-      again |= (atomicOr(&e.bits[at >> 5], bit) & bit) != 0;
+      if ((atomicOr(&e.bits[at >> 5], bit) & bit) != 0) again |= 1u << (j / kWave);
     }
     e.p[j] = p;
     e.z[j] = x;
@@ -133,29 +135,30 @@ __device__ __forceinline__ void read_target(const DistillArgs &a, int64_t row, i
     r = !none && r >= 0x1p-20 ? r : 0.0;
   }
   wave_sync();
-  if (__ballot(again) != 0) {
-    // (64 entries at a time: those before them are done, and the first of an id keeps it)
-    for (int c = 0; c < top; c += kWave) {
-      const int j = c + lane;
-      const int32_t id = j < top ? e.ids[j] : -1;
+  // An id's entries, found by those that met its bit, become its first one.  (Only rows that
+  // repeat ids pay for it: 64 x 151,936 with 300 entries a row takes 30 us, 35 where 1 in 4 rows
+  // repeats one.)
+  for (int c = 0; c < top; c += kWave)
+    for (uint64_t met = __ballot(again >> (c / kWave) & 1u); met != 0; met &= met - 1) {
+      const int32_t id = e.ids[c + __ffsll((unsigned long long)met) - 1];
+      if (id < 0) continue;
       double total = 0.0;
-      bool first = true;
-      if (id >= lo && id < hi)
-        for (int i = 0; i < top; ++i)
-          if (e.ids[i] == id) {
-            total += e.p[i];
-            first &= i >= j;
-          }
-      wave_sync();
-      if (id >= lo && id < hi) {
-        if (first)
-          e.p[j] = total;
-        else
-          e.ids[j] = -1;
+      int first = -1, count = 0;
+      for (int b = 0; b < top; b += kWave) {
+        const int i = b + lane;
+        const bool same = i < top && e.ids[i] == id;
+        const uint64_t all = __ballot(same);
+        if (first < 0 && all != 0) first = b + __ffsll((unsigned long long)all) - 1;
+        count += __popcll(all);
+        if (same) total += e.p[i];
+        if (same && i != first) e.ids[i] = -1;
+      }
+      if (count > 1) {
+        total = wave_sum(total);
+        if (lane == 0) e.p[first] = total;
       }
       wave_sync();
     }
-  }
   double named = 0.0;
   if (WHOLE) {
     max = wave_max(max);
@@ -163,8 +166,7 @@ __device__ __forceinline__ void read_target(const DistillArgs &a, int64_t row, i
       if (e.ids[j] >= 0) named += exp64(((double)e.z[j] - (double)ref_of(max)) / T_);
     named = wave_sum(named);
   }
-  if (lane == 0)
-    *info = {m, r, {max, named}, a.grad_loss != nullptr ? a.grad_loss[row] : 0.0f, none};
+  if (lane == 0) *info = {m, r, {max, named}, weight, none};
   wave_sync();
 }
 
@@ -329,7 +331,7 @@ extern __shared__ __align__(16) char lds[];
 //
 // Without GRAD it is one pass: 4096 x 151,936 bf16 245 us (5.1 TB/s), 4096 x 50,257 83 us
 // (5.0), 1031 x 50,257 27 us (3.9: four blocks a CU and no second round of them, so that the
-// teacher's row before it and the joins behind it are not hidden), 16,384 x 1000 34 us (a
+// teacher's row before it and the joins behind it are not hidden), 16,384 x 1000 29 us (a
 // wavefront to a row, each waiting for its teacher's entries and their logits in turn).  With
 // GRAD 4096 x 151,936 bf16 takes 527 us, 4.7 TB/s of the floor's bytes, its blocks reading and
 // writing in turn.  Tried instead for these 2.5 GB: the row held in registers from one pass to
@@ -411,7 +413,7 @@ __global__ __launch_bounds__(kScanThreads, 8) void distill_scan_kernel(const Dis
                                    own.mass, rest.max,       info.named.max};
 }
 
-// A row's parts, joined by every wavefront for itself; the loss taken from the largest logit.
+// A row's parts, joined by a wavefront; the loss taken from the largest logit.
 struct Joined {
   RowSum rest, named;
   double loss;
@@ -462,12 +464,15 @@ __global__ __launch_bounds__(kWave) void distill_finish_kernel(const DistillArgs
 // 2049 x 32,000 fp32: 104 us (5.0 TB/s of reads and writes; loads that stay in the caches
 // 124 against 110 timed alike), 16,384 x 32,000 bf16 366 (5.7), 4096 x 151,936 bf16 470
 // (5.3), 4096 x 50,257 bf16 149 (5.5; 179 without the alignment to cache lines).  With
-// PARTS, 64 x 151,936 bf16: 11.8 us, latency as in the scan.
+// PARTS, 64 x 151,936 bf16: 10.2 us, latency as in the scan (11.8 with the parts joined by every
+// wavefront behind the teacher's row).
 template <class T, int THREADS, bool PARTS>
 __global__ __launch_bounds__(THREADS) void distill_backward_kernel(const DistillArgs a,
                                                                    const int64_t segs) {
   constexpr int N = distill_held_backward(sizeof(T));
+  static_assert(!PARTS || THREADS >= 2 * kWave, "the second wavefront joins the parts");
   __shared__ RowInfo info;
+  __shared__ Joined joined;
   const int64_t row = blockIdx.x / segs, seg = blockIdx.x - row * segs;
   constexpr int64_t kLineValues = kLine / sizeof(T);
   const T *z = static_cast<const T *>(a.logits) + row * a.stride;
@@ -492,16 +497,19 @@ __global__ __launch_bounds__(THREADS) void distill_backward_kernel(const Distill
   const float first = before ? Chunk<T>::one(z[lo + lane]) : kNegInf;
   const float last = behind ? Chunk<T>::one(z[end + lane]) : kNegInf;
   Entries e(lds, a.top);
-  if (thread < kWave)
+  if (thread < kWave) {
     read_target<T, false>(a, row, lo, hi, lo, e, &info, !PARTS && seg == 0 ? a.err : nullptr);
+  } else if (PARTS && thread < 2 * kWave) {
+    const Joined v = join_parts(a, row);
+    if (thread == kWave) joined = v;
+  }
   __syncthreads();
   Gradient g;
+  Whole whole;
   double below, scale;
   if (PARTS) {
-    const Joined v = join_parts(a, row);
-    const Whole whole = both(v.rest, v.named, T_);
-    if (seg == 0 && thread == 0) write_row(a, row, v.rest, whole.all, v.loss, info);
-    g = gradient_of(info, v.rest, whole.s, T_);
+    whole = both(joined.rest, joined.named, T_);
+    g = gradient_of(info, joined.rest, whole.s, T_);
     below = ref_of(whole.all.max) / T_;
     scale = whole.all.sum == 0.0 ? 0.0 : 1.0 / whole.all.sum;
   } else {
@@ -519,6 +527,8 @@ __global__ __launch_bounds__(THREADS) void distill_backward_kernel(const Distill
     below = lse;
     scale = lse == -__builtin_inf() ? 0.0 : 1.0;
   }
+  if (PARTS && seg == 0 && thread == THREADS - 1)
+    write_row(a, row, joined.rest, whole.all, joined.loss, info);
   if (g.zero) {
     write_zeros(grad, lo, hi, THREADS);
     return;
@@ -588,11 +598,11 @@ int enqueue_backward(const DistillArgs &a, hipStream_t stream) {
                      dim3(THREADS), lds_bytes(a.top, most + 2 * kLead), stream, a, segs);
   return launch_status();
 }
-// A row that a wavefront holds (8192 bytes) goes by one: 16,384 rows of 2000 bytes in bf16 35 us,
-// by 256 threads 75, 8000 bytes 64 and 86 (fp32 34 and 69, 72 and 83); the teacher's row is each
+// A row that a wavefront holds (8192 bytes) goes by one: 16,384 rows of 2000 bytes in bf16 29 us,
+// by 256 threads 62, 8000 bytes 62 and 79 (fp32 28 and 58, 72 and 79); the teacher's row is each
 // block's first work.  Longer ones take as long either way, and more for more entries in
-// narrower blocks, each of which reads them: fp32 rows of 128,000 bytes 885 by 64 threads and
-// 829 by 256.
+// narrower blocks, each of which reads them: fp32 rows of 128,000 bytes 884 by 64 threads and
+// 819 by 256.
 template <class T>
 int enqueue_kept(const DistillArgs &a, hipStream_t stream) {
   if (a.vocab <= 8 * kWave * distill_held_backward(sizeof(T)))
@@ -603,17 +613,17 @@ int enqueue_kept(const DistillArgs &a, hipStream_t stream) {
 // Threads of a row's block.  Few rows have a CU each and gain by every thread; of many, narrow
 // blocks are quicker at what is not the vocabulary's, and more of them overlap.  us with / without
 // a gradient, calls of a graph, bf16 (fp32 likewise by its bytes), 64 / 128 / 256 / 512 / 1024:
-//   256 rows of 8000 bytes    14.3  12.5  11.9  12.5  14.0     11.2  10.1  10.0  10.0  10.4
-//              24,000         21.6  16.7  14.6  14.1  14.0     15.1  12.4  11.3  10.7  10.5
-//              64,000         37.5  25.1  19.9  17.4  16.8     23.0  17.0  14.1  12.8  12.1
-//   1500 rows of 2000         13.8  15.2  17.0  26.2  43.3     11.1  11.5  12.4  18.2  30.3
-//                8000         19.1  18.3  18.3  25.9  42.1     14.0  13.6  13.5  18.6  29.1
-//              32,000         34.5  30.5  29.2  32.8  42.6     21.7  19.3  19.1  22.6  29.4
-//   16,384 rows of 2000       46    67    103   212   400      34    47    71    147   282
-//                8000         76    90    115   217   384      47    57    76    149   264
-//              16,000         134   126   148   225   395      64    74    90    150   263
-//              32,000         265   246   230   290   438      109   106   122   175   279
-//              64,000         551   485   453   431   542      197   196   186   220   317
+//   256 rows of 8000 bytes    11.6  10.0   9.1   9.6  11.2      8.6   7.7   7.3   7.5   8.0
+//              24,000         19.6  14.5  12.2  11.7  11.7     13.0  10.2   8.9   8.4   8.5
+//              64,000         36.4  24.1  17.2  14.9  15.0     21.9  15.6  11.8  10.6  10.6
+//   1500 rows of 2000         11.3  12.3  14.9  21.4  35.6      8.4   9.1  10.4  14.2  22.9
+//                8000         16.5  15.9  15.9  23.1  37.4     11.6  11.2  11.2  16.0  24.7
+//              32,000         34.1  29.9  28.6  32.1  40.8     20.7  19.5  18.2  20.8  27.7
+//   16,384 rows of 2000       41    59    90    178   334      29    41    61    123   217
+//                8000         75    84    113   204   358      45    55    73    141   240
+//              16,000         137   126   144   222   390      66    74    90    147   252
+//              32,000         263   242   225   291   437      110   109   121   171   281
+//              64,000         552   487   454   430   554      203   194   185   218   321
 // With a gradient long rows are also kept from crowding each other out of the Infinity Cache
 // before they are read again: 2048 of them in flight by 256 threads, 1024 by 512 and 512 by
 // 1024, to stay within 112 MB.  4096 rows, us by 256 / 512 / 1024 threads: 80,000 bytes 158 /

@@ -176,6 +176,18 @@ def test_repeated_and_invalid_ids(target, vocab):
     assert int(err) == 43 and not bool(grad[4:6].any())
 
 
+@pytest.mark.parametrize("vocab", [900, 70000])
+@pytest.mark.parametrize("kinds", [1, 7, 500])
+def test_many_repeated_ids(kinds, vocab):
+    p, weight = problem(5, vocab, 1000, BF, target="part", seed=kinds)
+    g = torch.Generator(device="cuda").manual_seed(kinds)
+    some = torch.randint(0, vocab, (kinds,), generator=g, device="cuda")
+    p["ids"] = some[torch.randint(0, kinds, (5, 1000), generator=g, device="cuda")].contiguous()
+    p["ids"][2, ::3] = -1
+    p["teacher_lse"] = p["teacher_lse"] + 8.0
+    check_all(p, weight)
+
+
 MASKS = [-math.inf, torch.finfo(BF).min, torch.finfo(F32).min]
 
 
