@@ -70,7 +70,7 @@ __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(const ScanArgs 
     for (int u = 0; u < U; ++u) {
       const float own = max8(kNegInf, z[u]);
       m = max3(m, own, kNegInf);
-      const float most = lanes_max_of<16>(own + 0.0f);
+      const float most = lanes_max_of<16>(own);
       const int64_t i = at + u * kScanTile + 8 * threadIdx.x;
       if (threadIdx.x % 16 == 0 && i < hi) most_of[(i - lo) / kBeamGroup] = most;
     }

@@ -21,13 +21,11 @@ constexpr float kNegInf = -__builtin_inff();
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// max(a, b, c) in one instruction (fmaxf quiets its operands first).  Its result goes to
-// ordinary instructions only: the compiler does not know it for a vector instruction, and
-// would leave no wait states before one that moves data across lanes.
+// max(a, b, c) in one instruction, v_maximum3_f32; NaN if any is one.  (fmaxf quiets its
+// operands first.  The compiler has to know the instruction: it puts wait states between a
+// vector instruction and one that moves its result across lanes.)
 __device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-  return r;
+  return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
 }
 
 // Eight values at any address of their type: the loads and stores are 16 bytes wide
@@ -237,7 +235,8 @@ struct RowSum {
 __device__ __forceinline__ double moved(double s, float max, float ref, Scale c) {
   return max == kNegInf ? s : s * (double)exp_scaled(max - ref, c);
 }
-// The lanes' running sums over a block of WAVES wavefronts, in a fixed order: one barrier, after which every wavefront joins the others' for itself.
+// The lanes' running sums over a block of WAVES wavefronts, in a fixed order: one barrier, after
+// which every wavefront joins the others' for itself.
 template <int WAVES>
 struct JoinLds {
   float max[WAVES];
