@@ -65,6 +65,43 @@ struct RowInfo {
   int none;      // no target
 };
 
+// The sum over the named logits in the block's part, by one wavefront; max: each lane's largest.
+__device__ __forceinline__ RowSum named_sum(const DistillArgs &a, Entries e, float max) {
+  double sum = 0.0;
+  max = wave_max(max);
+  for (int j = threadIdx.x; j < (int)a.top; j += kWave)
+    if (e.ids[j] >= 0) sum += exp64(((double)e.z[j] - (double)ref_of(max)) / a.temperature);
+  return {max, wave_sum(sum)};
+}
+
+// An id's entries, found by those that met its bit (`again`, one for each of the lane's entries),
+// become its first one, with their sum.  (Only rows that repeat ids pay for it: 64 x 151,936 with
+// 300 entries a row takes 30 us, 35 where 1 in 4 rows repeats one.)
+__device__ __forceinline__ void merge_repeated(int top, Entries e, uint32_t again) {
+  const int lane = threadIdx.x;
+  for (int c = 0; c < top; c += kWave)
+    for (uint64_t met = __ballot(again >> (c / kWave) & 1u); met != 0; met &= met - 1) {
+      const int32_t id = e.ids[c + __ffsll((unsigned long long)met) - 1];
+      if (id < 0) continue;
+      double total = 0.0;
+      int first = -1, count = 0;
+      for (int b = 0; b < top; b += kWave) {
+        const int i = b + lane;
+        const bool same = i < top && e.ids[i] == id;
+        const uint64_t all = __ballot(same);
+        if (first < 0 && all != 0) first = b + __ffsll((unsigned long long)all) - 1;
+        count += __popcll(all);
+        if (same) total += e.p[i];
+        if (same && i != first) e.ids[i] = -1;
+      }
+      if (count > 1) {
+        total = wave_sum(total);
+        if (lane == 0) e.p[first] = total;
+      }
+      wave_sync();
+    }
+}
+
 // Reads the teacher's row, by one wavefront: e and *info, for the values [lo, hi) of the
 // vocabulary, of which first_bit (kLead before lo at most) has the first bit.  Entries of one id
 // become one, the first, with their sum.  WHOLE: the statistics' sum over the named logits too.
@@ -135,38 +172,10 @@ __device__ __forceinline__ void read_target(const DistillArgs &a, int64_t row, i
     r = !none && r >= 0x1p-20 ? r : 0.0;
   }
   wave_sync();
-  // An id's entries, found by those that met its bit, become its first one.  (Only rows that
-  // repeat ids pay for it: 64 x 151,936 with 300 entries a row takes 30 us, 35 where 1 in 4 rows
-  // repeats one.)
-  for (int c = 0; c < top; c += kWave)
-    for (uint64_t met = __ballot(again >> (c / kWave) & 1u); met != 0; met &= met - 1) {
-      const int32_t id = e.ids[c + __ffsll((unsigned long long)met) - 1];
-      if (id < 0) continue;
-      double total = 0.0;
-      int first = -1, count = 0;
-      for (int b = 0; b < top; b += kWave) {
-        const int i = b + lane;
-        const bool same = i < top && e.ids[i] == id;
-        const uint64_t all = __ballot(same);
-        if (first < 0 && all != 0) first = b + __ffsll((unsigned long long)all) - 1;
-        count += __popcll(all);
-        if (same) total += e.p[i];
-        if (same && i != first) e.ids[i] = -1;
-      }
-      if (count > 1) {
-        total = wave_sum(total);
-        if (lane == 0) e.p[first] = total;
-      }
-      wave_sync();
-    }
-  double named = 0.0;
-  if (WHOLE) {
-    max = wave_max(max);
-    for (int j = lane; j < top; j += kWave)
-      if (e.ids[j] >= 0) named += exp64(((double)e.z[j] - (double)ref_of(max)) / T_);
-    named = wave_sum(named);
-  }
-  if (lane == 0) *info = {m, r, {max, named}, weight, none};
+  merge_repeated(top, e, again);
+  RowSum named = {kNegInf, 0.0};
+  if (WHOLE) named = named_sum(a, e, max);
+  if (lane == 0) *info = {m, r, named, weight, none};
   wave_sync();
 }
 
@@ -456,47 +465,171 @@ __global__ __launch_bounds__(kWave) void distill_finish_kernel(const DistillArgs
   if (threadIdx.x == 0) write_row(a, row, v.rest, whole.all, v.loss, info);
 }
 
+// Whether a row's kept logarithms are too coarse to take its gradient from.  Half a step of fp32
+// is a relative error of every exponential: 2^-19 below 64, and 2^-15 below 1024, which is 1/64 of
+// the rounding of a bf16 gradient.  Beside a mask's lowest value nothing is left of the sum's own
+// logarithm, and the quotient by a temperature below 1 may be past fp32.  (-inf is exact
+// otherwise: an empty sum.)
+template <class T>
+__device__ __forceinline__ bool coarse(float lse, double temperature) {
+  return __builtin_fabsf(lse) >= (sizeof(T) == 2 ? 1024.0f : 64.0f) &&
+         !(lse == kNegInf && temperature >= 1.0);
+}
+template <class T>
+__device__ __forceinline__ bool coarse_row(const DistillArgs &a, int64_t row) {
+  return coarse<T>(a.lse[row], a.temperature) ||
+         (a.rest && coarse<T>(a.lse_rest[row], a.temperature));
+}
+
+// The gradient of a whole row by one block, from sums of its own that it takes first, `part`
+// values at a time (as many as e has bits for).  One block, because the gradient may take the
+// logits' place.  With every row coarse (temperature 0.001) 4096 x 151,936 bf16 take 937 us (415
+// with none), 4096 x 50,257 348 (142), 2049 x 32,000 fp32 188 (102), 16,384 x 1000 bf16 132 (30).
+template <class T, int THREADS>
+__device__ __forceinline__ void write_row_anew(const DistillArgs &a, int64_t row, int64_t part,
+                                               Entries e, RowInfo *info,
+                                               JoinLds<THREADS / kWave> &join) {
+  const T *z = static_cast<const T *>(a.logits) + row * a.stride;
+  T *grad = static_cast<T *>(a.grad) + row * a.grad_stride;
+  const uint8_t *bytes = reinterpret_cast<const uint8_t *>(e.bits);
+  const int thread = threadIdx.x, top = (int)a.top;
+  if (thread < kWave) read_target<T, false>(a, row, 0, 0, 0, e, info, nullptr);
+  RowSum own = {kNegInf, 0.0};
+  for (int64_t lo = 0; lo < a.vocab; lo += part) {
+    const int64_t hi = lo + part < a.vocab ? lo + part : a.vocab;
+    __syncthreads();  // (the bits of the part before were read)
+    if (thread < kWave) {
+      for (int i = thread; i < (int)((hi - lo + 31) / 32); i += kWave) e.bits[i] = 0u;
+      wave_sync();
+      uint32_t again = 0;
+      for (int j = thread; j < top; j += kWave) {
+        const int32_t id = e.ids[j];
+        if (id < lo || id >= hi) continue;
+        const uint32_t at = (uint32_t)(id - lo), bit = 1u << (at & 31);
+        if ((atomicOr(&e.bits[at >> 5], bit) & bit) != 0) again |= 1u << (j / kWave);
+        e.z[j] = Chunk<T>::one(z[id]);
+      }
+      wave_sync();
+      merge_repeated(top, e, again);
+    }
+    __syncthreads();
+    Running run;
+    const int n = (int)(hi - lo);
+    for (int i = 8 * thread; i + 8 <= n; i += 8 * THREADS) {
+      float v[8];
+      Chunk<T> r;
+      r.load(z + lo + i);
+      r.values(v);
+      leave_out(v, bytes[i >> 3]);
+      const float ref = run.raise(max8(run.max, v), a.c);
+      run.add(v, ref, a.c);
+    }
+    const int tail = n / 8 * 8 + thread;
+    if (tail < n && (bytes[tail >> 3] >> (tail & 7) & 1) == 0) {
+      const float one = Chunk<T>::one(z[lo + tail]);
+      const float ref = run.raise(max3(run.max, one, kNegInf), a.c);
+      run.sum += exp_scaled(one - ref, a.c);
+    }
+    const float m = max3(own.max, run.max, kNegInf);
+    own = {m, moved(own.sum, own.max, ref_of(m), a.c) +
+                  moved(run.sum, run.max, ref_of(m), a.c)};
+  }
+  const RowSum rest = block_join(own, a.c, join);
+  if (thread < kWave) {
+    float most = kNegInf;
+    for (int j = thread; j < top; j += kWave)
+      if (e.ids[j] >= 0) most = __builtin_fmaxf(most, e.z[j]);
+    const RowSum named = named_sum(a, e, most);
+    if (thread == 0) info->named = named;
+  }
+  __syncthreads();
+  const Whole whole = both(rest, info->named, a.temperature);
+  const Gradient g = gradient_of(*info, rest, whole.s, a.temperature);
+  if (g.zero) {
+    write_zeros(grad, 0, a.vocab, THREADS);
+    return;
+  }
+  for (int64_t i = 8 * thread; i + 8 <= a.vocab; i += 8 * THREADS) {
+    float v[8];
+    Chunk<T> r;
+    r.load(z + i);
+    r.values(v);
+    gradient_values<T>(v, g, a.c);
+    Chunk<T>::store_once(grad + i, v);
+  }
+  const int64_t tail = a.vocab / 8 * 8 + thread;
+  if (tail < a.vocab)
+    Chunk<T>::store_one(grad + tail, gradient_value<T>(Chunk<T>::one(z[tail]), g, a.c));
+  __syncthreads();
+  if (thread < kWave)
+    write_named<T>(a, grad, 0, a.vocab, e, *info, ref_of(whole.all.max) / a.temperature,
+                   whole.all.sum == 0.0 ? 0.0 : 1.0 / whole.all.sum);
+}
+
+// The coarse rows among `index`, index + blocks, ... (64 of them) by a block, one after another.
+// (They are shared out without a word between blocks; every wavefront finds the same ones.)
+template <class T, int THREADS>
+__device__ __forceinline__ void write_coarse_rows(const DistillArgs &a, uint32_t index,
+                                                  uint32_t blocks, int64_t part, Entries e,
+                                                  RowInfo *info,
+                                                  JoinLds<THREADS / kWave> &join) {
+  const int64_t mine = index + (int64_t)(threadIdx.x % kWave) * blocks;
+  uint64_t left = __ballot(mine < a.rows && coarse_row<T>(a, mine) && a.grad_loss[mine] != 0.0f);
+  for (; left != 0; left &= left - 1) {
+    const uint32_t nth = __ffsll((unsigned long long)left) - 1;
+    write_row_anew<T, THREADS>(a, index + nth * blocks, part, e, info, join);
+    __syncthreads();  // (before e and *info are written again)
+  }
+}
+
 // A block to a segment of a row: its gradient, from the statistics that were kept or, with
 // PARTS, from the parts that distill_scan_kernel left (the first segment's block then also
 // writes the row's loss and statistics).  The segment's values are in registers while the
 // teacher's row is read.
 //
-// 2049 x 32,000 fp32: 104 us (5.0 TB/s of reads and writes; loads that stay in the caches
-// 124 against 110 timed alike), 16,384 x 32,000 bf16 366 (5.7), 4096 x 151,936 bf16 470
-// (5.3), 4096 x 50,257 bf16 149 (5.5; 179 without the alignment to cache lines).  With
+// 2049 x 32,000 fp32: 102 us (5.1 TB/s of reads and writes; loads that stay in the caches
+// 124 against 110 timed alike), 16,384 x 32,000 bf16 363 (5.8), 4096 x 151,936 bf16 415
+// (6.0), 4096 x 50,257 bf16 142 (5.8; 179 and 149 without and with the alignment to cache lines,
+// timed alike).  Its 80 registers leave 6 wavefronts to a SIMD; of 5, 1031 x 50,257 bf16 took 41.6
+// us instead of 39.4.  With
 // PARTS, 64 x 151,936 bf16: 10.2 us, latency as in the scan (11.8 with the parts joined by every
 // wavefront behind the teacher's row).
 template <class T, int THREADS, bool PARTS>
 __global__ __launch_bounds__(THREADS) void distill_backward_kernel(const DistillArgs a,
-                                                                   const int64_t segs) {
+                                                                   const uint32_t segs,
+                                                                   const uint32_t blocks) {
   constexpr int N = distill_held_backward(sizeof(T));
   static_assert(!PARTS || THREADS >= 2 * kWave, "the second wavefront joins the parts");
   __shared__ RowInfo info;
   __shared__ Joined joined;
-  const int64_t row = blockIdx.x / segs, seg = blockIdx.x - row * segs;
-  constexpr int64_t kLineValues = kLine / sizeof(T);
+  __shared__ JoinLds<THREADS / kWave> join;
+  Entries e(lds, a.top);
+  if (!PARTS && blockIdx.x >= blocks) {
+    write_coarse_rows<T, THREADS>(a, blockIdx.x - blocks, gridDim.x - blocks, 8 * THREADS * N, e,
+                                  &info, join);
+    return;
+  }
+  const int64_t row = blockIdx.x / segs;
+  const uint32_t seg = blockIdx.x - (uint32_t)row * segs;
+  const double T_ = a.temperature;
+  constexpr int kLineValues = kLine / sizeof(T);
   const T *z = static_cast<const T *>(a.logits) + row * a.stride;
   T *grad = static_cast<T *>(a.grad) + row * a.grad_stride;
   // whole cache lines are shared out; the first segment has the values before them too, the
   // last those behind: one of each to a lane of the block's last wavefront
   const int lead = lead_of(z, a.vocab);
-  const int64_t lines = (a.vocab - lead) / kLineValues;
-  const int64_t body = lead + lines * seg / segs * kLineValues;
-  const int64_t end = lead + lines * (seg + 1) / segs * kLineValues;
+  const uint32_t lines = (uint32_t)(a.vocab - lead) / kLineValues;
+  const uint32_t each = lines / segs, more = lines - each * segs;  // (the first `more` one more)
+  const int64_t body = lead + (int64_t)(each * seg + (seg < more ? seg : more)) * kLineValues;
+  const int n = (int)(each + (seg < more)) * kLineValues, thread = threadIdx.x;
+  const int64_t end = body + n;
   const int64_t lo = seg == 0 ? 0 : body, hi = seg + 1 == segs ? a.vocab : end;
-  const double T_ = a.temperature;
-  const int n = (int)(end - body), thread = threadIdx.x;
   Chunk<T> r[N];
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     const int i = 8 * (k * THREADS + thread);
     if (i < n) r[k].template load<true>(z + body + i);
   }
-  const int lane = thread - (THREADS - kWave);
-  const bool before = lane >= 0 && lo + lane < body, behind = lane >= 0 && end + lane < hi;
-  const float first = before ? Chunk<T>::one(z[lo + lane]) : kNegInf;
-  const float last = behind ? Chunk<T>::one(z[end + lane]) : kNegInf;
-  Entries e(lds, a.top);
   if (thread < kWave) {
     read_target<T, false>(a, row, lo, hi, lo, e, &info, !PARTS && seg == 0 ? a.err : nullptr);
   } else if (PARTS && thread < 2 * kWave) {
@@ -526,6 +659,7 @@ __global__ __launch_bounds__(THREADS) void distill_backward_kernel(const Distill
     g.zero = info.weight == 0.0f || info.none != 0;
     below = lse;
     scale = lse == -__builtin_inf() ? 0.0 : 1.0;
+    if (!g.zero && coarse_row<T>(a, row)) return;  // (one of the last blocks has it)
   }
   if (PARTS && seg == 0 && thread == THREADS - 1)
     write_row(a, row, joined.rest, whole.all, joined.loss, info);
@@ -533,6 +667,10 @@ __global__ __launch_bounds__(THREADS) void distill_backward_kernel(const Distill
     write_zeros(grad, lo, hi, THREADS);
     return;
   }
+  const int lane = thread - (THREADS - kWave);
+  const bool before = lane >= 0 && lo + lane < body, behind = lane >= 0 && end + lane < hi;
+  const float first = before ? Chunk<T>::one(z[lo + lane]) : kNegInf;
+  const float last = behind ? Chunk<T>::one(z[end + lane]) : kNegInf;
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     const int i = 8 * (k * THREADS + thread);
@@ -589,13 +727,25 @@ void enqueue_rows(const DistillArgs &a, hipStream_t stream) {
     hipLaunchKernelGGL((distill_row_kernel<T, THREADS, false>), grid, block, bytes, stream, a);
 }
 
+// Blocks for the rows whose statistics are coarse: four to a CU, each of at most 64 rows.  They
+// are the last ones of the launch and as a rule find nothing to do (2049 x 32,000 fp32 101.8 us,
+// 103.1 without them; 4096 x 50,257 bf16 142.4 and 139.4).  Tried instead: the look at a row's
+// statistics before each block's first chunks 107.9 and 143.5, a launch of its own 106.8 and 140.7
+// and 2.5 us more for any call.
+inline int64_t coarse_blocks(int64_t rows) {
+  const int64_t least = ceil_div(rows, kWave), want = least < 1024 ? 1024 : least;
+  return want < rows ? want : rows;
+}
+// (PARTS: none, the statistics are the call's own.)
 template <class T, int THREADS, bool PARTS>
 int enqueue_backward(const DistillArgs &a, hipStream_t stream) {
   const int64_t most = 8 * THREADS * distill_held_backward(sizeof(T));  // values
-  const int64_t segs = ceil_div(a.vocab, most);
-  if (!grid_fits(a.rows * segs, kScanThreads)) return ENGRAM_EINVAL;
-  hipLaunchKernelGGL((distill_backward_kernel<T, THREADS, PARTS>), dim3((unsigned)(a.rows * segs)),
-                     dim3(THREADS), lds_bytes(a.top, most + 2 * kLead), stream, a, segs);
+  const int64_t segs = ceil_div(a.vocab, most), blocks = a.rows * segs;
+  const int64_t all = blocks + (PARTS ? 0 : coarse_blocks(a.rows));
+  if (!grid_fits(all, kScanThreads)) return ENGRAM_EINVAL;
+  hipLaunchKernelGGL((distill_backward_kernel<T, THREADS, PARTS>), dim3((unsigned)all),
+                     dim3(THREADS), lds_bytes(a.top, most + 2 * kLead), stream, a, (uint32_t)segs,
+                     (uint32_t)blocks);
   return launch_status();
 }
 // A row that a wavefront holds (8192 bytes) goes by one: 16,384 rows of 2000 bytes in bf16 29 us,

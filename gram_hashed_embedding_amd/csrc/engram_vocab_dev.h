@@ -130,7 +130,7 @@ struct Running {
 // exp in fp64 by its series around 0 (|r| <= ln(2) / 2: the 11th power's term is
 // 2e-13), in few registers.
 __device__ __forceinline__ double exp64(double x) {
-  x = x < -800.0 ? -800.0 : x;  // (0; a NaN stays one)
+  x = x < -800.0 ? -800.0 : x > 800.0 ? 800.0 : x;  // (0 and +inf; a NaN stays one)
   const double n = rint(x * 1.44269504088896340736);
   const double r = fma(-n, 0.693147180559945309417, x);
   double p = 1.0 / 3628800.0;
@@ -242,8 +242,9 @@ struct JoinLds {
   float max[WAVES];
   double sum[WAVES];
 };
-template <int WAVES>
-__device__ __forceinline__ RowSum block_join(const Running &run, Scale c, JoinLds<WAVES> &l) {
+// (RUN: a Running, or a RowSum of several.)
+template <int WAVES, class RUN>
+__device__ __forceinline__ RowSum block_join(const RUN &run, Scale c, JoinLds<WAVES> &l) {
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const float own = wave_max(run.max);
   const double part = wave_sum(moved(run.sum, run.max, ref_of(own), c));

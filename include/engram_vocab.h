@@ -61,7 +61,7 @@ extern "C" {
  * fp64; a term of less than 2^-126 of the largest is lost.  The gradient is
  * rounded once to the logits' type.
  *   rows (up to 4,194,303, and rows * ceil(vocab / 16384) for a gradient up to
- *     16,777,215, / 8192 for fp32: a launch's threads), vocab (1 to 2^30), top
+ *     16,500,000, / 8192 for fp32: a launch's threads), vocab (1 to 2^30), top
  *     (1 to ENGRAM_DISTILL_MAX_TOP).
  *   d_logits of logits_type, rows logits_stride values apart.
  *   d_ids int64 [rows, top]: -1 marks an unused entry; other ids outside
@@ -78,9 +78,13 @@ extern "C" {
  *   where that is not 0.
  * engram_distill_backward -- the gradient alone, from the d_lse (and, with
  *   rest, d_lse_rest) that engram_distill wrote: q = exp(z / temperature - lse),
- *   q / s = exp(z / temperature - lse_rest).  (Where every logit of a sum is a
- *   mask's lowest value, its fp32 logarithm does not hold that of their number,
- *   and each such exponential is 1.)  No workspace; d_loss is NULL.
+ *   q / s = exp(z / temperature - lse_rest).  A logarithm's rounding to fp32 is
+ *   a relative error of these: 2^-19 below 64 and, used for bf16 logits only,
+ *   2^-15 below 1024.  A row with a larger one (a low temperature, logits all
+ *   at a mask's lowest value or far from 0; at a temperature below 1 an
+ *   infinite one too) is summed again by one block, its gradient as exact as
+ *   engram_distill's and two to four times as long.  No workspace; d_loss is
+ *   NULL.
  * Errors: EINVAL, EWORKSPACE.  rows == 0 enqueues nothing.
  */
 typedef struct engram_distill_args {
