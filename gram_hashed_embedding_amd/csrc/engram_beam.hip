@@ -300,7 +300,8 @@ __global__ __launch_bounds__(kChooseThreads) void beam_choose_kernel(const Choos
     const int lead = lead_of(z, c.vocab);
     group_beam[t] = w;
     group_at[t] = g == 0 ? 0 : lead + (g - 1) * kBeamGroup;
-    group_end[t] = g == 0 ? lead : c.vocab;
+    // (of a finished beam nothing is read)
+    group_end[t] = lse[w] != lse[w] ? 0 : g == 0 ? lead : c.vocab;
   }
   __syncthreads();
   const int listed = list_best(
