@@ -239,7 +239,9 @@ struct ChooseArgs {
 template <class T>
 __global__ __launch_bounds__(kChooseThreads) void beam_choose_kernel(const ChooseArgs a) {
   __shared__ ChooseLds l;
-  __shared__ double lse[ENGRAM_BEAM_MAX];    // NaN: no candidate but a finished beam's
+  // lse, in two parts: beside a mask's lowest value nothing would be left of the sum's logarithm
+  __shared__ double top[ENGRAM_BEAM_MAX];    // the largest logit
+  __shared__ double lse[ENGRAM_BEAM_MAX];    // from there; NaN: no candidate but a finished beam's
   __shared__ double score[ENGRAM_BEAM_MAX];
   __shared__ bool done[ENGRAM_BEAM_MAX];     // (out_scores and out_finished may be the inputs)
   __shared__ int64_t group_at[kChooseGroups];  // of each chosen group: its first value
@@ -250,7 +252,7 @@ __global__ __launch_bounds__(kChooseThreads) void beam_choose_kernel(const Choos
   const int t = threadIdx.x, beams = (int)c.beams, count = (int)c.count;
   const int groups = (int)a.groups;
   const auto value_of = [&](int w, float z) {
-    const double v = score[w] + ((double)z - lse[w]);
+    const double v = score[w] + (((double)z - top[w]) - lse[w]);
     return v == v ? v : kNone;
   };
   // i / groups by the whole part of 2^32 / groups, which is at most one too small
@@ -273,12 +275,15 @@ __global__ __launch_bounds__(kChooseThreads) void beam_choose_kernel(const Choos
         // each beam's lse, a wavefront to a beam
         for (int w = t / kWave; w < beams; w += kChooseThreads / kWave) {
           const int64_t row = first_row + w;
-          double v = __builtin_nan("");
+          double m = 0.0, v = __builtin_nan("");
           if (beam_live(c.scores, c.finished, row)) {
-            v = log_sum(wave_join(c.parts + row * a.segs, a.segs, a.log2e), 1.0);
-            if (!__builtin_isfinite(v)) v = __builtin_nan("");
+            const RowSum sum = wave_join(c.parts + row * a.segs, a.segs, a.log2e);
+            m = sum.max;
+            v = log64(sum.sum);
+            if (!__builtin_isfinite(m) || !__builtin_isfinite(v)) v = __builtin_nan("");
           }
           if (t % kWave == 0) {
+            top[w] = m;
             lse[w] = v;
             score[w] = c.scores[row];
             done[w] = c.finished != nullptr && c.finished[row] != 0 &&

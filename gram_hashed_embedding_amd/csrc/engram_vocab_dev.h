@@ -268,10 +268,6 @@ __device__ __forceinline__ RowSum wave_join(const ScanPart *parts, int64_t n, Sc
     s += moved(parts[i].sum, parts[i].max, ref_of(m), c);
   return {m, wave_sum(s)};
 }
-// log of the sum of exp(z / temperature): -inf for none.
-__device__ __forceinline__ double log_sum(const RowSum &v, double temperature) {
-  return ref_of(v.max) / temperature + log64(v.sum);
-}
 
 // -------------------------------------------------------- reading a segment --
 // The values [lo, hi) of a row by a block, U chunks a lane at a time: use(at, z) is

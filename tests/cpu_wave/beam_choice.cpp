@@ -100,6 +100,24 @@ void finished_rows(int64_t vocab, size_t at) {
         "finished beams, " + std::to_string(vocab) + " values, " + std::to_string(at));
 }
 
+// Beams whose logits are all a mask's lowest value: each id has 1 / vocab of the probability,
+// below what the other beam offers, equal ones by place.
+template <class T>
+void masked_beams(int64_t vocab, float mask) {
+  Logits<T> z(3, vocab, 0);
+  for (int64_t v = 0; v < vocab; ++v) {
+    z.row(0)[v] = z.row(2)[v] = value<T>(mask);
+    z.row(1)[v] = value<T>(v == vocab / 2 ? 9.0f : v == 1 ? 8.0f : 0.0f);
+  }
+  const Chosen c = choose(z.first, z.stride, {-5.0f, -5.5f, -5.25f}, {}, -1, 3, vocab, 5);
+  const double log = ::log((double)vocab);
+  bool ok = c.parents[0] == 1 && c.tokens[0] == vocab / 2 && c.parents[1] == 1 && c.tokens[1] == 1;
+  for (int k = 2; k < 5; ++k)
+    ok &= c.parents[k] == 0 && c.tokens[k] == k - 2 &&
+          fabs((double)c.scores[k] + 5.0 + log) < 1e-5;
+  check(ok, "masked beams, " + std::to_string(vocab) + " values at " + std::to_string(mask));
+}
+
 }  // namespace
 
 int main(int, char **argv) {
@@ -110,5 +128,12 @@ int main(int, char **argv) {
         finished_rows<uint16_t>(vocab, at);
         finished_rows<float>(vocab, at);
       }
+  if (which == "masked")
+    for (int64_t vocab : {1000, 9000}) {
+      masked_beams<uint16_t>(vocab, __uint_as_float(0xff7f0000u));
+      masked_beams<float>(vocab, __uint_as_float(0xff7fffffu));
+      masked_beams<float>(vocab, -1e30f);
+      masked_beams<float>(vocab, -1e9f);
+    }
   return failed;
 }

@@ -30,3 +30,8 @@ def run(tmp_path, which):
 def test_finished_beams_are_not_read(tmp_path):
     """Their rows' pages are taken away."""
     assert run(tmp_path, "finished") == 24
+
+
+def test_beams_of_a_masks_lowest_value(tmp_path):
+    """Their ids share the beam's probability, whose logarithm a logit of 1e30 does not hold."""
+    assert run(tmp_path, "masked") == 8
