@@ -5,12 +5,11 @@
 //
 // Selection.  One pass over the logits (beam_scan_kernel) leaves each segment's
 // sum of exponentials and the largest logit of every kBeamGroup adjacent
-// values, counted from the first whole cache line; those before it are a row's
-// group 0, which may be empty.  The `count` best candidates lie in the `count`
-// best groups (by their largest value, equal ones by place: the candidate before
-// which `count` others come cannot be one of the first `count`), so
-// beam_choose_kernel, a block to a sequence, finds those among 1/128 of the
-// values, reads them again and takes the best of `count` times 128 candidates.  Both choices are exact in fp64.
+// values.  The `count` best candidates lie in the `count` best groups (by their
+// largest value, equal ones by place: the candidate before which `count` others
+// come cannot be one of the first `count`), so beam_choose_kernel, a block to a
+// sequence, finds those among 1/128 of the values, reads them again and takes
+// the best of `count` times 128 candidates.  Both choices are exact in fp64.
 //
 // Reordering.  A new beam that is the first child of its parent keeps the
 // parent's slot; only the others' states are copied, into slots of beams that
@@ -39,31 +38,24 @@ __device__ __forceinline__ bool beam_live(const float *scores, const uint8_t *fi
 }
 
 // A block to a segment of a beam's logits.  Memory bounds it: 512 beams of 151,936 bf16 values
-// are read in 29 to 32 us (5.4 to 4.9 TB/s); 4 chunks a lane and step instead of 2 are no faster.  The
-// groups' maxima wait in LDS and are written 4 bytes a lane next to each other at the end,
-// not by every 16th lane in between.  Groups begin at whole cache lines: 4096 beams of 50,257
-// bf16 values take 97 us for a selection, 108 if they begin with the row.  One beam or a few: 4 to 6 us, a block's own latency.
+// are read in 29 to 32 us (5.4 to 4.9 TB/s); 4 chunks a lane and step instead of 2 are no faster.
+// The groups' maxima wait in LDS and are written 4 bytes a lane next to each other at the end, not
+// by every 16th lane in between.  Chunks start with the row, wherever it lies, so that beams with
+// equal logits have equal sums to the last bit and tie as they should; from whole cache lines on
+// a selection among 4096 beams of 50,257 bf16 values takes 95 us instead of 106, of 50,256 94
+// instead of 98, 512 beams of 151,935 43.5 instead of 47.7.  One beam or a few: 4 to 6 us, a
+// block's own latency.
 template <class T>
 __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(const ScanArgs a) {
   __shared__ JoinLds<kScanThreads / kWave> join;
-  __shared__ float most_of[kBeamMaxSeg / kBeamGroup];  // but of group 0
+  __shared__ float most_of[kBeamMaxSeg / kBeamGroup];
   const int64_t row = blockIdx.x / a.segs, seg = blockIdx.x - row * a.segs;
   if (!beam_live(a.scores, a.finished, row)) return;
   const T *z = static_cast<const T *>(a.logits) + row * a.stride;
-  const int lead = lead_of(z, a.vocab);
-  int64_t lo = lead + seg * a.seg_len, hi = lo + a.seg_len;
-  lo = lo < a.vocab ? lo : a.vocab;
-  hi = hi < a.vocab ? hi : a.vocab;
+  const int64_t lo = seg * a.seg_len, hi = lo + a.seg_len < a.vocab ? lo + a.seg_len : a.vocab;
   float *maxima = a.maxima + row * a.groups;
   constexpr int U = sizeof(T) == 2 ? 2 : 1;
   Running run;
-  if (seg == 0 && threadIdx.x < kWave) {
-    const float one = (int)threadIdx.x < lead ? Chunk<T>::one(z[threadIdx.x]) : kNegInf;
-    const float ref = run.raise(one, a.c);
-    run.sum = exp_scaled(one - ref, a.c);
-    const float most = wave_max(one);
-    if (threadIdx.x == 0) maxima[0] = most;
-  }
   each_chunks<T, kScanThreads, U, true>(z, lo, hi, [] {}, [&](int64_t at, float (&z)[U][8]) {
     float m = run.max;
 #pragma unroll
@@ -79,11 +71,8 @@ __global__ __launch_bounds__(kScanThreads) void beam_scan_kernel(const ScanArgs 
     for (int u = 0; u < U; ++u) run.add(z[u], ref, a.c);
   });
   const RowSum s = block_join(run, a.c, join);  // (with a barrier)
-  // (the last group may lie behind the row)
-  const int64_t first = 1 + seg * (a.seg_len / kBeamGroup), behind = a.groups - first;
-  const int n = (int)(behind < a.seg_len / kBeamGroup ? behind : a.seg_len / kBeamGroup);
-  for (int i = threadIdx.x; i < n; i += kScanThreads)
-    maxima[first + i] = i * kBeamGroup < hi - lo ? most_of[i] : kNegInf;
+  const int n = (int)((hi - lo + kBeamGroup - 1) / kBeamGroup);
+  for (int i = threadIdx.x; i < n; i += kScanThreads) maxima[lo / kBeamGroup + i] = most_of[i];
   if (threadIdx.x == 0) a.parts[row * a.segs + seg] = {s.sum, s.max, 0u};
 }
 
@@ -226,7 +215,7 @@ __device__ __forceinline__ void rank_listed(ChooseLds &l, int listed, int count)
 struct ChooseArgs {
   BeamCall c;
   int64_t segs, groups;
-  uint32_t per_group;  // 2^32 / groups, rounded down
+  uint32_t per_group;  // (2^32 - 1) / groups, rounded down
   Scale log2e;
 };
 
@@ -255,7 +244,7 @@ __global__ __launch_bounds__(kChooseThreads) void beam_choose_kernel(const Choos
     const double v = score[w] + (((double)z - top[w]) - lse[w]);
     return v == v ? v : kNone;
   };
-  // i / groups by the whole part of 2^32 / groups, which is at most one too small
+  // i / groups by the whole part of (2^32 - 1) / groups, which is at most one too small
   const auto beam_of = [&](uint32_t i) {
     const uint32_t w = __umulhi(i, a.per_group);
     return (int)(i - w * groups >= (uint32_t)groups ? w + 1 : w);
@@ -301,12 +290,10 @@ __global__ __launch_bounds__(kChooseThreads) void beam_choose_kernel(const Choos
   if (t < chosen) {
     const int at = (int)(ranked ? l.best[t].at : l.list[t].at), w = beam_of(at);
     const int g = at - w * groups;
-    const T *z = static_cast<const T *>(c.logits) + (first_row + w) * c.stride;
-    const int lead = lead_of(z, c.vocab);
     group_beam[t] = w;
-    group_at[t] = g == 0 ? 0 : lead + (g - 1) * kBeamGroup;
+    group_at[t] = (int64_t)g * kBeamGroup;
     // (of a finished beam nothing is read)
-    group_end[t] = lse[w] != lse[w] ? 0 : g == 0 ? lead : c.vocab;
+    group_end[t] = lse[w] != lse[w] ? 0 : c.vocab;
   }
   __syncthreads();
   const int listed = list_best(
@@ -436,7 +423,7 @@ int engram::launch_beam_select(const BeamCall &c, void *stream) {
   const ScanArgs s = {c.logits, c.vocab, c.stride, shape.segs, shape.seg_len, groups, log2e,
                       c.scores, c.finished, c.parts, c.maxima};
   const ChooseArgs a = {c, shape.segs, groups,
-                        (uint32_t)((uint64_t(1) << 32) / groups), log2e};
+                        (uint32_t)(0xffffffffu / groups), log2e};
   const dim3 grid((unsigned)(rows * shape.segs)), block(kScanThreads);
   const dim3 sequences((unsigned)c.batch), wide(kChooseThreads);
   if (c.type == ENGRAM_BF16) {

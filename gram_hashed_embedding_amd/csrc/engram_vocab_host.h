@@ -80,8 +80,7 @@ constexpr int64_t kBeamMaxSeg = int64_t(1) << 18;
 inline ScanShape beam_shape(int64_t rows, int64_t vocab) {
   return scan_shape(rows, vocab, kBeamBlocks, kBeamMaxSeg);
 }
-// (one more: the values before the first whole cache line)
-inline int64_t beam_groups(int64_t vocab) { return 1 + ceil_div(vocab, kBeamGroup); }
+inline int64_t beam_groups(int64_t vocab) { return ceil_div(vocab, kBeamGroup); }
 struct BeamCall {
   const void *logits;
   int32_t type;

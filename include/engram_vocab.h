@@ -119,14 +119,15 @@ int engram_distill_backward(const engram_distill_args *args);
  * With lse[b,w] = log sum_v exp(logits[b,w,v]), the candidate (w, v) of
  * sequence b has the value
  *     scores[b,w] + (logits[b,w,v] - lse[b,w])
- * in fp64 (lse: fp32 terms, summed in fp64 across lanes; its largest logit is
- * taken off first, so that a beam whose logits are all a mask's lowest value
- * keeps the logarithm of their number).  A finished beam has
- * one candidate, (w, eos_id) with the value scores[b,w]; its logits are not
- * read.  The `count` largest values are written in falling order, equal ones
- * by the lower beam and then the lower id.  A value that is -inf or NaN is
- * never taken (a beam whose score or lse is not finite has none): entries
- * that nothing is left for have score -inf, parent -1, token -1.
+ * in fp64 (lse: fp32 terms, summed in fp64 across lanes in an order that the
+ * sizes fix, so that beams with equal logits have equal ones; its largest logit
+ * is taken off first, so that a beam whose logits are all a mask's lowest value
+ * keeps the logarithm of their number).  A finished beam has one candidate, (w,
+ * eos_id) with the value scores[b,w]; its logits are not read.  The `count`
+ * largest values are written in falling order, equal ones by the lower beam and
+ * then the lower id.  A value that is -inf or NaN is never taken (a beam whose
+ * score or lse is not finite has none): entries that nothing is left for have
+ * score -inf, parent -1, token -1.
  *   batch, beams (1 to ENGRAM_BEAM_MAX), vocab (1 to 2^30), count (1 to
  *     ENGRAM_BEAM_MAX).
  *   d_logits [batch * beams] rows of `type`, logits_stride values apart.

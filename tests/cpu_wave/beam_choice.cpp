@@ -6,6 +6,8 @@
 
 #include <sys/mman.h>
 
+#include <algorithm>
+#include <numeric>
 #include <string>
 
 namespace engram {
@@ -118,6 +120,31 @@ void masked_beams(int64_t vocab, float mask) {
   check(ok, "masked beams, " + std::to_string(vocab) + " values at " + std::to_string(mask));
 }
 
+// Beams that are copies of one another, each at another place in a cache line, with equal
+// scores: equal logits have equal values, in the order of beams and then of ids.
+template <class T>
+void equal_beams(int64_t vocab) {
+  const int64_t stride = vocab + 3;
+  std::vector<T> memory(5 * stride + 64);
+  for (size_t at : {0, 1, 13}) {
+    for (int64_t v = 0; v < vocab; ++v) {
+      const T x = value<T>(draw());
+      for (int64_t w = 0; w < 5; ++w) memory[at + w * stride + v] = x;
+    }
+    const Chosen c = choose(memory.data() + at, stride, std::vector<float>(5, -7.0f), {}, -1, 5,
+                            vocab, 10);
+    std::vector<int64_t> order(5 * vocab);
+    std::iota(order.begin(), order.end(), 0);
+    std::stable_sort(order.begin(), order.end(), [&](int64_t i, int64_t j) {
+      return Chunk<T>::one(memory[at + i % vocab]) > Chunk<T>::one(memory[at + j % vocab]);
+    });
+    bool ok = true;
+    for (int k = 0; k < 10; ++k)
+      ok &= c.parents[k] == order[k] / vocab && c.tokens[k] == order[k] % vocab;
+    check(ok, "equal beams, " + std::to_string(vocab) + " values from " + std::to_string(at));
+  }
+}
+
 }  // namespace
 
 int main(int, char **argv) {
@@ -134,6 +161,11 @@ int main(int, char **argv) {
       masked_beams<float>(vocab, __uint_as_float(0xff7fffffu));
       masked_beams<float>(vocab, -1e30f);
       masked_beams<float>(vocab, -1e9f);
+    }
+  if (which == "equal")
+    for (int64_t vocab : {700, 1003, 5001, 20011}) {
+      equal_beams<uint16_t>(vocab);
+      equal_beams<float>(vocab);
     }
   return failed;
 }

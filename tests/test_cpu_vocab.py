@@ -5,6 +5,8 @@ import os
 import re
 import subprocess
 
+import pytest
+
 from tests.test_abi_sanitized import CSRC, ROOT
 from tests.test_cpu_wave import build
 
@@ -18,20 +20,30 @@ def test_no_instruction_is_written_by_hand():
             assert not re.search(r"\b(?:__)?asm(?:__)?\b", code), path
 
 
-def run(tmp_path, which):
-    res = subprocess.run([build(tmp_path, "beam_choice", os.path.join(CSRC, "engram_host.cpp"),
-                                os.path.join(CSRC, "engram_vocab_host.cpp"),
-                                os.path.join(ROOT, "tests", "host_launch_stub.cpp")), which],
-                         capture_output=True, text=True, timeout=300)
-    assert res.returncode == 0, (res.returncode, res.stdout, res.stderr)
-    return res.stdout.count(": ok")
+@pytest.fixture(scope="module")
+def run(tmp_path_factory):
+    """A check of the beams' choice by its name: how many cases of it were right."""
+    exe = build(tmp_path_factory.mktemp("beams"), "beam_choice",
+                os.path.join(CSRC, "engram_host.cpp"), os.path.join(CSRC, "engram_vocab_host.cpp"),
+                os.path.join(ROOT, "tests", "host_launch_stub.cpp"))
+
+    def check(which):
+        res = subprocess.run([exe, which], capture_output=True, text=True, timeout=300)
+        assert res.returncode == 0, (res.returncode, res.stdout, res.stderr)
+        return res.stdout.count(": ok")
+    return check
 
 
-def test_finished_beams_are_not_read(tmp_path):
+def test_finished_beams_are_not_read(run):
     """Their rows' pages are taken away."""
-    assert run(tmp_path, "finished") == 24
+    assert run("finished") == 24
 
 
-def test_beams_of_a_masks_lowest_value(tmp_path):
+def test_beams_of_a_masks_lowest_value(run):
     """Their ids share the beam's probability, whose logarithm a logit of 1e30 does not hold."""
-    assert run(tmp_path, "masked") == 8
+    assert run("masked") == 8
+
+
+def test_equal_beams_by_place(run):
+    """A sum's order does not go by its row's address."""
+    assert run("equal") == 24

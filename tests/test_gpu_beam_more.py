@@ -71,3 +71,22 @@ def test_fewer_allowed_than_asked_for(vocab, beams, mask, dtype):
     z = torch.where(keep, z, torch.full_like(z, mask))
     check(z, s, 64)
     check(z, s, 10)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("vocab, stride", [(400, 400), (1003, 1003), (1003, 1024), (50257, 50257),
+                                           (151936, 151941)])
+def test_beams_that_are_copies(vocab, stride, dtype):
+    """Equal beams tie to the last bit wherever their rows lie: the lower one comes first."""
+    z, _ = logits(2, 1, vocab, dtype, seed=vocab)
+    wide = torch.zeros((13 * stride + 64,), dtype=dtype, device="cuda")
+    s = torch.full((2, 6), -3.0, device="cuda")
+    for first in (0, 1, 7, 32):
+        part = wide.as_strided((12, vocab), (stride, 1), first)
+        part.copy_(z.expand(2, 6, vocab).reshape(12, vocab))
+        got = V.engram_beam_select(part, s, 16)
+        for b in range(2):
+            order = torch.sort(z[b].float().expand(6, vocab).flatten(), descending=True,
+                               stable=True).indices[:16]
+            assert torch.equal(got.parents[b], order // vocab)
+            assert torch.equal(got.tokens[b], order % vocab)
