@@ -23,18 +23,40 @@ KEPT = {F32: 1.0, BF: 1.0 + 2.0 ** -14 / R.SHARE}
 SIZES = [500, 12000, 20000, 70000]
 
 
-def check(p, weight, inplace=True):
-    """The gradient of one call, of kept statistics, and of these in the logits' place."""
+def losses(p, want):
+    """want's losses with each row's largest logit taken off first: beside a mask's lowest value
+    the reference's lse_rest - lse holds nothing of the logarithms of their numbers."""
+    out = want.clone()
+    for t in range(out.numel()):
+        P, named, m, r, none = R.target(p["ids"][t], p["teacher"][t], p["logits"].shape[1],
+                                        p["temperature"],
+                                        None if p["teacher_lse"] is None else p["teacher_lse"][t],
+                                        p["rest"])
+        z = p["logits"][t].double()
+        if none or r == 0.0 or not math.isfinite(float(z.max())):
+            continue
+        z = (z - z.max()) / p["temperature"]
+        lse, on = torch.logsumexp(z, 0), P != 0
+        out[t] = (P[on] * (P[on].log() - (z[on] - lse))).sum()
+        out[t] += r * (math.log(r) - (torch.logsumexp(z[~named], 0) - lse))
+    return out
+
+
+def check(p, weight, loss=True):
+    """The loss and gradient of one call, the gradient of kept statistics, and of these in the
+    logits' place.  loss: what fp32 can hold."""
     want = R.distill(p["logits"], p["ids"], p["teacher"], p["teacher_lse"], p["rest"],
                      p["temperature"], weight)
+    want["loss"] = losses(p, want["loss"])
     d = forward(p, weight)
-    R.check_distill(dict(grad=d.grad), want)
+    R.check_distill(d._asdict() if loss else dict(grad=d.grad), want)
+    if loss:
+        R.check_distill(forward(p)._asdict(), want)
     want["slack"] = want["slack"] * KEPT[p["logits"].dtype]
     grad = backward(p, weight, d)
     R.check_distill(dict(grad=grad), want)
-    if inplace:
-        q = dict(p, logits=p["logits"].clone())
-        assert torch.equal(backward(q, weight, d, grad=q["logits"]), grad)
+    q = dict(p, logits=p["logits"].clone())
+    assert torch.equal(backward(q, weight, d, grad=q["logits"]), grad)
 
 
 @pytest.mark.parametrize("temperature", [0.7, 1.0, 1.1, 1.3, 1.8, 2.7, 3.1])
@@ -58,7 +80,7 @@ def test_masks(vocab, mask, dtype, temperature):
         if target != "kept":                          # no rest: r = 0
             y = torch.where(ids >= 0, p["teacher"].double() / temperature, -math.inf)
             p["teacher_lse"][1:3] = torch.logsumexp(y, 1)[1:3].float()
-        check(p, weight)
+        check(p, weight, loss=temperature >= 1.0)
 
 
 @pytest.mark.parametrize("temperature", [2.0 ** -64, 1e-12, 1e-6, 1e-3, 0.01, 0.05, 0.2, 4e4,
