@@ -120,8 +120,10 @@ __device__ __forceinline__ double value_of_bits(uint32_t k) {
 // largest has at least `count` values at or above it (its leading 20 bits are enough,
 // found bit by bit from ballots).  What reaches it is listed.  Where that is more than
 // the list holds (long runs of equal values), the first `count` are listed one at a
-// time instead, each the first after the one before.  A thread keeps its first kKeep
-// values; their loads go out together.
+// time instead, each the first after the one before: where a mask of a large finite value
+// leaves fewer ids than are asked for, 16 of 4 beams of 151,936 take 0.9 ms instead of 17 us,
+// 64 of 64 beams 2.5 ms instead of 96 us (a mask of -inf has no such candidates).  A thread
+// keeps its first kKeep values; their loads go out together.
 constexpr int kKeep = 12;
 template <class LOGIT, class VALUE, class PLACE, class MEANWHILE>
 __device__ __forceinline__ int list_best(ChooseLds &l, int n, int count, LOGIT logit, VALUE value,
@@ -220,8 +222,8 @@ struct ChooseArgs {
 };
 
 // A block to a sequence.  Its bytes are few (8 beams of 151,936 values: 38 KB of maxima and 24
-// KB of groups read again): it is a chain of loads, barriers and ballots, 9.4 us for one beam
-// and 13.8 for 64 sequences of 8, so it runs once whatever the batch.  What shortened it: the
+// KB of groups read again): it is a chain of loads, barriers and ballots, 10.1 us for 4 beams
+// and 14.2 for 64 sequences of 8, so it runs once whatever the batch.  What shortened it: the
 // loads of a pass all sent before the first is used and behind the beams' sums, no division
 // of 64 bits, and the first choice's groups left unordered (21 to 23 us -> 14).  Of 512
 // threads, tried before that, a whole selection took 56 us where it took 50 of 1024.
@@ -336,7 +338,7 @@ constexpr int64_t kForkChunk = (int64_t)kForkThreads * kForkSteps * 16;  // byte
 // Blocks: `chunks` of every new beam (the pools' slots one after another); the first
 // of them also writes the beam's slot and history.  A block copies 16 KB, 4 loads of 16
 // bytes in flight a lane.  64 x 8 beams with slots of 192 KB, of which about a third are
-// copied: 14.6 us, 4.8 TB/s (70 MB in all, too few for more); a few beams 4.2 us, a launch's
+// copied: 13.5 us, 5.2 TB/s (70 MB in all, too few for more); a few beams 3.9 us, a launch's
 // latency.
 __global__ __launch_bounds__(kForkThreads) void beam_fork_kernel(const ForkCall c,
                                                                  const int64_t chunks) {

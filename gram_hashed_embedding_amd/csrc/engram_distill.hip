@@ -15,8 +15,8 @@
 // three barriers a row at most.
 //
 // For loss and gradient together a block reads its row twice, the second time
-// from the Infinity Cache: the rows in flight are kept within its 256 MB, and
-// the gradient is stored past it (distill_row_kernel).
+// from the Infinity Cache (256 MB) as long as the rows in flight fit it, and the
+// gradient is stored past it (distill_row_kernel, distill_threads).
 //
 // What bounds it is memory: a value costs 2 or 4 bytes and a subtraction, a
 // product, a v_exp_f32 and an addition, so the floor is each logit read once and
@@ -338,8 +338,8 @@ extern __shared__ __align__(16) char lds[];
 // A block to a row: its loss and statistics and, with GRAD, its gradient, for which the row
 // is read again.  8 wavefronts a SIMD in blocks of each size.
 //
-// Without GRAD it is one pass: 4096 x 151,936 bf16 245 us (5.1 TB/s), 4096 x 50,257 83 us
-// (5.0), 1031 x 50,257 27 us (3.9: four blocks a CU and no second round of them, so that the
+// Without GRAD it is one pass: 4096 x 151,936 bf16 228 us (5.5 TB/s), 4096 x 50,257 84 us
+// (4.9), 1031 x 50,257 27 us (3.9: four blocks a CU and no second round of them, so that the
 // teacher's row before it and the joins behind it are not hidden), 16,384 x 1000 29 us (a
 // wavefront to a row, each waiting for its teacher's entries and their logits in turn).  With
 // GRAD 4096 x 151,936 bf16 takes 527 us, 4.7 TB/s of the floor's bytes, its blocks reading and
@@ -775,9 +775,12 @@ int enqueue_kept(const DistillArgs &a, hipStream_t stream) {
 //              32,000         263   242   225   291   437      110   109   121   171   281
 //              64,000         552   487   454   430   554      203   194   185   218   321
 // With a gradient long rows are also kept from crowding each other out of the Infinity Cache
-// before they are read again: 2048 of them in flight by 256 threads, 1024 by 512 and 512 by
-// 1024, to stay within 112 MB.  4096 rows, us by 256 / 512 / 1024 threads: 80,000 bytes 158 /
-// 145 / 160, 120,000 253 / 230 / 218, 196,000 421 / 382 / 364, 303,872 646 / 548 / 538.
+// before they are read again: 2048 of them are in flight by 256 threads, 1024 by 512 and 512 by
+// 1024, up to 112 MB for rows of up to 110,000 bytes.  Longer ones have 512 in flight whatever
+// their length: 156 MB at 303,872 bytes, all of the cache at 500,000, more than it holds above.
+// 4096 rows, us by 256 / 512 / 1024 threads: 80,000 bytes 158 / 145 / 160, 120,000 253 / 230 / 218,
+// 196,000 421 / 382 / 364, 303,872 646 / 548 / 538; by 1024, TB/s of the floor's bytes: 303,872
+// 4.7, 496,640 4.7, 607,744 (2048 rows) 3.7, 993,280 3.7.
 constexpr int64_t kDistillManyRows = 2048;
 int distill_threads(int64_t rows, int64_t bytes, bool grad) {
   if (rows <= 256) return bytes <= 12000 ? 256 : bytes <= 48000 ? 512 : 1024;

@@ -45,8 +45,11 @@ constexpr int distill_held_backward(size_t size) { return size == 2 ? 8 : 4; }
 // A block takes a whole row, but for a few long rows with a gradient, which would leave CUs
 // idle, and where a row's bits (one a value: whether a teacher's row names it) would take
 // more than 32 KB of LDS: those are cut.  Loss and gradient of rows of 151,936 bf16 values,
-// cut / not: 16 rows 21.5 / 32.0 us, 64 rows 25.6 / 32.1, 128 rows 34.7 / 34.4.  The loss
-// alone gains nothing: its one pass is short beside what a second launch costs.
+// cut / not: 16 rows 19.7 / 29.6 us, 64 rows 20.9 / 30.1, 128 rows 28.7 / 35.4, 192 rows
+// 42.8 / 38.1 (fp32: 64 rows 28.8 / 43.8, 128 rows 51.3 / 61.6, 192 rows 70.6 / 77.7).  Of
+// 65,536 fp32 values, 64 rows 19.6 / 20.4, 128 rows 24.5 / 22.4; bf16 rows of that length lose 2
+// to 3 us by it.  The loss alone gains nothing: its one pass is short beside what a second
+// launch costs.
 constexpr int64_t kDistillMaxSeg = int64_t(1) << 18;
 constexpr int64_t kDistillBlocks = 1024;
 constexpr int64_t kDistillFewRows = 128, kDistillFewVocab = 65536;

@@ -192,7 +192,7 @@ def engram_distill_backward(grad_loss, logits, ids, teacher, lse, *, teacher_lse
     """The gradient of engram_distill's loss from the lse that it wrote (and lse_rest, which
     stands for rest), for grad_loss fp32 [...] (0: the row does not count).  grad may be
     logits.  Rows whose lse or lse_rest fp32 holds too coarsely (64 or more in size, for bf16
-    logits 1024) are summed again, which takes two to four times as long."""
+    logits 1024) are summed again, which takes two to six times as long."""
     index, rows, vocab, stride, kind = _logits(logits, "logits")
     lead = logits.shape[:-1]
     top, teacher_kind, ids_p, teacher_p, tlse_p = _entries(logits, ids, teacher, teacher_lse,

@@ -83,7 +83,7 @@ extern "C" {
  *   2^-15 below 1024.  A row with a larger one (a low temperature, logits all
  *   at a mask's lowest value or far from 0; at a temperature below 1 an
  *   infinite one too) is summed again by one block, its gradient as exact as
- *   engram_distill's and two to four times as long.  No workspace; d_loss is
+ *   engram_distill's and two to six times as long.  No workspace; d_loss is
  *   NULL.
  * Errors: EINVAL, EWORKSPACE.  rows == 0 enqueues nothing.
  */

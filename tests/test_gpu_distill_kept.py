@@ -129,6 +129,15 @@ def test_many_coarse_rows(rows, dtype):
     assert bool((off <= tol).all()), float((off - tol).max())
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_long_coarse_rows(dtype):
+    """More values than a block has bits for at a time, ids that repeat across and within parts."""
+    p, weight = problem(2, (1 << 20) + 3, 70, dtype, target="part", temperature=0.02, seed=29)
+    p["ids"][:, 40:60] = p["ids"][:, 3:23]
+    p["teacher_lse"] += 2.0
+    check(p, weight)
+
+
 def test_errors_are_counted_once():
     p, weight = problem(3, 40000, 6, BF, target="kept", temperature=0.001, seed=25)
     p["ids"][0, 1], p["ids"][2, 3] = 40000, -7
