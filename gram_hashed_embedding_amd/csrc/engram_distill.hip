@@ -404,7 +404,7 @@ __global__ __launch_bounds__(THREADS, 8) void distill_row_kernel(const DistillAr
 }
 
 // A block to a segment of a row: its part of the sums and of the loss.  64 x 151,936 bf16,
-// 16 blocks to a row: 11.4 us, of which the bytes are 3; the rest is the launch and the
+// 16 blocks to a row: 11.3 us, of which the bytes are 3; the rest is the launch and the
 // latency of one block's chain (ids, their logits, their sum, the joins).
 template <class T>
 __global__ __launch_bounds__(kScanThreads, 8) void distill_scan_kernel(const DistillArgs a) {
@@ -591,9 +591,8 @@ __device__ __forceinline__ void write_coarse_rows(const DistillArgs &a, uint32_t
 // 124 against 110 timed alike), 16,384 x 32,000 bf16 363 (5.8), 4096 x 151,936 bf16 415
 // (6.0), 4096 x 50,257 bf16 142 (5.8; 179 and 149 without and with the alignment to cache lines,
 // timed alike).  Its 80 registers leave 6 wavefronts to a SIMD; of 5, 1031 x 50,257 bf16 took 41.6
-// us instead of 39.4.  With
-// PARTS, 64 x 151,936 bf16: 10.2 us, latency as in the scan (11.8 with the parts joined by every
-// wavefront behind the teacher's row).
+// us instead of 39.4.  With PARTS, 64 x 151,936 bf16: 9.9 us, latency as in the scan (11.8 with the
+// parts joined by every wavefront behind the teacher's row, timed when it was 10.2).
 template <class T, int THREADS, bool PARTS>
 __global__ __launch_bounds__(THREADS) void distill_backward_kernel(const DistillArgs a,
                                                                    const uint32_t segs,

@@ -179,3 +179,30 @@ def test_in_place_in_fp32(rows, vocab):
     p["logits"] = kept
     again = backward(p, weight, want)
     assert torch.equal(backward(p, weight, want, grad=kept), again)
+
+
+@pytest.mark.parametrize("vocab", [700, 33001])
+def test_captured_and_replayed(vocab):
+    """A captured gradient follows its inputs: none, some and all of the rows coarse."""
+    p, weight = problem(9, vocab, 6, BF, seed=30)
+    d, grad = forward(p), torch.empty_like(p["logits"])
+    backward(p, weight, d, grad=grad)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        backward(p, weight, d, grad=grad)
+    for turn, rows in enumerate((0, 4, 9, 0, 9)):
+        fresh, _ = problem(9, vocab, 6, BF, seed=31 + turn)
+        fresh["logits"][:rows] = torch.finfo(BF).min
+        for name in ("logits", "ids", "teacher", "teacher_lse"):
+            p[name].copy_(fresh[name])
+        for old, new in zip((d.lse, d.lse_rest), forward(fresh)[1:3]):
+            old.copy_(new)
+        grad.fill_(7.0)
+        g.replay()
+        if turn % 2:
+            torch.cuda.synchronize()
+        want = R.distill(fresh["logits"], fresh["ids"], fresh["teacher"], fresh["teacher_lse"],
+                         True, 1.0, weight)
+        R.check_distill(dict(grad=grad), want)
+        assert torch.equal(backward(fresh, weight, d), grad)
